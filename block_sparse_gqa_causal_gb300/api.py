@@ -8,11 +8,14 @@ built, the first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
 import threading
 from dataclasses import dataclass
+from functools import cached_property
+from typing import NamedTuple
 
 import torch
 
@@ -21,12 +24,15 @@ LIB_PATH = os.path.join(_HERE, "libmsa.so")
 
 OP_INDEX_SELECT, OP_SPARSE_ATTN_FWD, OP_KL_FWD, OP_FUSED_BWD, OP_FUSED_BWD_KL, OP_TRAIN_STEP = 0, 1, 2, 3, 4, 5
 OP_WARMUP_KL = 6
+OP_PAGED_PLAN, OP_PAGED_APPEND, OP_PAGED_BLOCK_SCORES, OP_PAGED_BLOCK_TOPK, OP_PAGED_ATTN = 16, 17, 18, 19, 20
+PAGE = 128      # tokens of a cache page
 STATUS = {0: "MSA_OK", 1: "MSA_ERR_INVALID_ARGUMENT", 2: "MSA_ERR_UNSUPPORTED", 3: "MSA_ERR_WORKSPACE",
           4: "MSA_ERR_CUDA", 5: "MSA_ERR_TIMEOUT", 6: "MSA_ERR_DEVICE"}
 EXPORTS = ("msa_workspace_size", "msa_index_select", "msa_sparse_attn_fwd", "msa_kl_fwd", "msa_fused_bwd",
            "msa_fused_bwd_kl", "msa_train_step", "msa_train_step_staged", "msa_block_mask", "msa_warmup_kl",
            "msa_index_proj_workspace_size", "msa_index_proj_fwd", "msa_index_proj_bwd", "msa_kv_append",
-           "msa_last_error", "msa_check_device_status", "msa_version", "msa_launch_count")
+           "msa_paged_workspace_size", "msa_paged_plan", "msa_paged_append", "msa_paged_block_scores",
+           "msa_paged_block_topk", "msa_paged_attn", "msa_last_error", "msa_check_device_status", "msa_version", "msa_launch_count")
 
 
 class MsaError(RuntimeError):
@@ -91,6 +97,58 @@ class Shape:
                        self.topk, self.kv_rows, self.scale, self.scale_idx)
 
 
+class _CPagedShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("R", "T", "max_blocks", "n_pages", "Hq", "Hkv", "d", "d_idx", "topk")] + [
+        ("scale", ctypes.c_float), ("scale_idx", ctypes.c_float)]
+
+
+@dataclass(frozen=True)
+class PagedShape:
+    """msa_paged_shape: R requests, T rows (query tokens) of a step, block tables
+    of max_blocks columns, a pool of n_pages pages of 128 tokens."""
+    R: int
+    T: int
+    max_blocks: int
+    n_pages: int
+    Hq: int
+    Hkv: int
+    d: int
+    d_idx: int
+    topk: int
+    scale: float = 0.0
+    scale_idx: float = 0.0
+
+    @property
+    def G(self) -> int:
+        return self.Hq // self.Hkv
+
+    @property
+    def n_segs(self) -> int:
+        """Entries of a plan's segment list before the last."""
+        return min(self.T, 2 * self.R + self.T // PAGE)
+
+    def c(self) -> _CPagedShape:
+        return _CPagedShape(self.R, self.T, self.max_blocks, self.n_pages, self.Hq, self.Hkv, self.d, self.d_idx,
+                            self.topk, self.scale, self.scale_idx)
+
+    @cached_property
+    def _ref(self):
+        return ctypes.byref(self.c())
+
+
+class PagedPlan(NamedTuple):
+    """What msa_paged_plan writes (int32 tensors): the lengths after the step
+    [R], the ring's {head, count} [2], q_starts [R+1], row_req, row_pos, slots
+    [T] and segs [n_segs+1]."""
+    lens: torch.Tensor
+    free_state: torch.Tensor
+    q_starts: torch.Tensor
+    row_req: torch.Tensor
+    row_pos: torch.Tensor
+    slots: torch.Tensor
+    segs: torch.Tensor
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -125,11 +183,20 @@ def lib() -> ctypes.CDLL:
             L.msa_index_proj_workspace_size.restype = sz
             L.msa_index_proj_fwd.argtypes = [PS, P, P, P, P, P, P, sz, P]
             L.msa_index_proj_bwd.argtypes = [PS, P, P, P, P, P, P, sz, P]
+            GS = ctypes.POINTER(_CPagedShape)
+            L.msa_paged_workspace_size.argtypes = [GS, ctypes.c_int]
+            L.msa_paged_workspace_size.restype = sz
+            L.msa_paged_plan.argtypes = [GS] + [P] * 14 + [sz, P]
+            L.msa_paged_append.argtypes = [GS] + [P] * 11 + [sz, P]
+            L.msa_paged_block_scores.argtypes = [GS] + [P] * 8 + [sz, P]
+            L.msa_paged_block_topk.argtypes = [GS] + [P] * 4 + [sz, P]
+            L.msa_paged_attn.argtypes = [GS] + [P] * 12 + [sz, P]
             L.msa_selftest_wait_timeout.argtypes = [P, ctypes.c_uint, P]
             for fn in ("msa_index_select", "msa_sparse_attn_fwd", "msa_kl_fwd", "msa_fused_bwd", "msa_fused_bwd_kl",
                        "msa_train_step", "msa_train_step_staged", "msa_check_device_status", "msa_block_mask",
                        "msa_warmup_kl", "msa_index_proj_fwd", "msa_index_proj_bwd", "msa_selftest_wait_timeout",
-                       "msa_kv_append"):
+                       "msa_kv_append", "msa_paged_plan", "msa_paged_append", "msa_paged_block_scores",
+                       "msa_paged_block_topk", "msa_paged_attn"):
                 getattr(L, fn).restype = ctypes.c_int
             L.msa_last_error.restype = ctypes.c_char_p
             L.msa_version.restype = ctypes.c_char_p
@@ -346,6 +413,169 @@ def kv_append(shape: Shape, k_new, v_new, k_idx_new, k, v, k_idx, *, stream=None
             _need(cache, "cache", (s.B, s.rows_kv) + row, torch.bfloat16)
     _check(lib().msa_kv_append(ctypes.byref(s.c()), _ptr(k_new), _ptr(v_new), _ptr(k_idx_new), _ptr(k), _ptr(v),
                                _ptr(k_idx), _stream(stream)))
+
+
+_HERE_CTX = contextlib.nullcontext()
+
+
+def _place(t: torch.Tensor, stream):
+    """The context in which a paged call allocates and launches: the tensors'
+    device and, when one is given, the stream (so that what is allocated there
+    is not handed out again before the call's kernels are done with it)."""
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+        return torch.cuda.stream(stream)
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        return torch.cuda.device(t.device)
+    return _HERE_CTX
+
+
+def _need_on(dev, specs) -> None:
+    """_need for several (tensor, name, shape, dtype), all on one CUDA device."""
+    for t, name, shape, dtype in specs:
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != dev or not t.is_cuda:
+            raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {tuple(shape)} on {dev} (a CUDA device), "
+                             f"got {t.dtype} {tuple(t.shape)} contiguous={t.is_contiguous()} on {t.device}")
+
+
+def paged_workspace_size(shape: PagedShape, op: int) -> int:
+    n = lib().msa_paged_workspace_size(shape._ref, op)
+    if n == 0:
+        _check(1)
+    return int(n)
+
+
+def new_paged_workspace(shape: PagedShape, op: int, device=None) -> torch.Tensor:
+    """A workspace of a paged call, its 256-byte status word zeroed."""
+    ws = torch.empty(paged_workspace_size(shape, op), dtype=torch.uint8, device=device or "cuda")
+    ws[:256].zero_()
+    return ws
+
+
+def _paged_ws(ws, shape, op, device):
+    if ws is None:
+        return new_paged_workspace(shape, op, device)
+    if ws.device != device or ws.dtype is not torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"workspace: need a contiguous uint8 tensor on {device}, got {ws.dtype} on {ws.device}")
+    return ws
+
+
+def paged_plan(shape: PagedShape, new_lens, lens, block_table, free_pages, free_state, *, ended=None, out=None,
+               workspace=None, stream=None) -> PagedPlan:
+    """msa_paged_plan: the step's pages, block tables and slot maps from the
+    requests' lengths.  new_lens, lens, ended [R], free_state [2] int32; block_table
+    [R, max_blocks] and free_pages [n_pages] int32 are updated in place.  Returns a
+    PagedPlan (pass `out` to reuse its tensors; its lens and free_state may be
+    the tensors passed in)."""
+    s, i32, dev = shape, torch.int32, new_lens.device
+    specs = [(new_lens, "new_lens", (s.R,), i32), (lens, "lens", (s.R,), i32),
+             (block_table, "block_table", (s.R, s.max_blocks), i32), (free_pages, "free_pages", (s.n_pages,), i32),
+             (free_state, "free_state", (2,), i32)]
+    if ended is not None:
+        specs.append((ended, "ended", (s.R,), i32))
+    sizes = [s.R, 2, s.R + 1, s.T, s.T, s.T, s.n_segs + 1]
+    if out is not None:
+        specs += [(t, n, (m,), i32) for t, n, m in zip(out, PagedPlan._fields, sizes)]
+    _need_on(dev, specs)
+    with _place(new_lens, stream):
+        ws = _paged_ws(workspace, s, OP_PAGED_PLAN, dev)
+        if out is None:
+            out = PagedPlan(*torch.empty(sum(sizes), dtype=i32, device=dev).split(sizes))
+        _check(lib().msa_paged_plan(s._ref, new_lens.data_ptr(), lens.data_ptr(), None if ended is None else ended.data_ptr(),
+                                    block_table.data_ptr(), free_pages.data_ptr(), free_state.data_ptr(),
+                                    *[t.data_ptr() for t in out], ws.data_ptr(), ws.numel(),
+                                    torch.cuda.current_stream(dev).cuda_stream))
+    return out
+
+
+def paged_append(shape: PagedShape, k_new, v_new, k_idx_new, slots, segs, k8, v8, k_scale, v_scale, k_idx, *,
+                 workspace=None, stream=None) -> None:
+    """msa_paged_append: the rows k_new, v_new [T, Hkv, d] and k_idx_new [T, d_idx]
+    (bf16) into the caches k8, v8 [n_pages, Hkv, 128, d] (float8_e4m3fn) with
+    k_scale, v_scale [n_pages, Hkv] (fp32), and k_idx [n_pages, 128, d_idx] (bf16),
+    at a plan's slots and segs.  The K and V group, or the K_idx pair, may be None."""
+    s, bf, dev = shape, torch.bfloat16, slots.device
+    specs = [(slots, "slots", (s.T,), torch.int32), (segs, "segs", (s.n_segs + 1,), torch.int32)]
+    for t, name, shp, dtype in ((k_new, "k_new", (s.T, s.Hkv, s.d), bf), (v_new, "v_new", (s.T, s.Hkv, s.d), bf),
+                                (k_idx_new, "k_idx_new", (s.T, s.d_idx), bf),
+                                (k8, "k8", (s.n_pages, s.Hkv, PAGE, s.d), torch.float8_e4m3fn),
+                                (v8, "v8", (s.n_pages, s.Hkv, PAGE, s.d), torch.float8_e4m3fn),
+                                (k_scale, "k_scale", (s.n_pages, s.Hkv), torch.float32),
+                                (v_scale, "v_scale", (s.n_pages, s.Hkv), torch.float32),
+                                (k_idx, "k_idx", (s.n_pages, PAGE, s.d_idx), bf)):
+        if t is not None:
+            specs.append((t, name, shp, dtype))
+    _need_on(dev, specs)
+    ptr = [None if t is None else t.data_ptr() for t in (k_new, v_new, k_idx_new, slots, segs, k8, v8, k_scale, v_scale, k_idx)]
+    with _place(slots, stream):
+        ws = _paged_ws(workspace, s, OP_PAGED_APPEND, dev)
+        _check(lib().msa_paged_append(s._ref, *ptr, ws.data_ptr(), ws.numel(), torch.cuda.current_stream(dev).cuda_stream))
+
+
+def paged_block_scores(shape: PagedShape, q_idx, k_idx, block_table, q_starts, row_req, row_pos, *, block_scores=None,
+                       workspace=None, stream=None):
+    """msa_paged_block_scores: [T, Hkv, max_blocks] fp32 of q_idx [T, Hkv, d_idx] and
+    the pages k_idx [n_pages, 128, d_idx] (bf16)."""
+    s, i32, dev = shape, torch.int32, q_idx.device
+    specs = [(q_idx, "q_idx", (s.T, s.Hkv, s.d_idx), torch.bfloat16), (k_idx, "k_idx", (s.n_pages, PAGE, s.d_idx), torch.bfloat16),
+             (block_table, "block_table", (s.R, s.max_blocks), i32), (q_starts, "q_starts", (s.R + 1,), i32),
+             (row_req, "row_req", (s.T,), i32), (row_pos, "row_pos", (s.T,), i32)]
+    if block_scores is not None:
+        specs.append((block_scores, "block_scores", (s.T, s.Hkv, s.max_blocks), torch.float32))
+    _need_on(dev, specs)
+    with _place(q_idx, stream):
+        ws = _paged_ws(workspace, s, OP_PAGED_BLOCK_SCORES, dev)
+        if block_scores is None:
+            block_scores = torch.empty((s.T, s.Hkv, s.max_blocks), dtype=torch.float32, device=dev)
+        _check(lib().msa_paged_block_scores(s._ref, q_idx.data_ptr(), k_idx.data_ptr(), block_table.data_ptr(),
+                                            q_starts.data_ptr(), row_req.data_ptr(), row_pos.data_ptr(),
+                                            block_scores.data_ptr(), ws.data_ptr(), ws.numel(),
+                                            torch.cuda.current_stream(dev).cuda_stream))
+    return block_scores
+
+
+def paged_block_topk(shape: PagedShape, block_scores, row_pos, *, sel_idx=None, workspace=None, stream=None):
+    """msa_paged_block_topk: sel_idx [T, Hkv, topk] int32 of block_scores [T, Hkv, max_blocks]."""
+    s, dev = shape, block_scores.device
+    specs = [(block_scores, "block_scores", (s.T, s.Hkv, s.max_blocks), torch.float32), (row_pos, "row_pos", (s.T,), torch.int32)]
+    if sel_idx is not None:
+        specs.append((sel_idx, "sel_idx", (s.T, s.Hkv, s.topk), torch.int32))
+    _need_on(dev, specs)
+    with _place(block_scores, stream):
+        ws = _paged_ws(workspace, s, OP_PAGED_BLOCK_TOPK, dev)
+        if sel_idx is None:
+            sel_idx = torch.empty((s.T, s.Hkv, s.topk), dtype=torch.int32, device=dev)
+        _check(lib().msa_paged_block_topk(s._ref, block_scores.data_ptr(), row_pos.data_ptr(), sel_idx.data_ptr(),
+                                          ws.data_ptr(), ws.numel(), torch.cuda.current_stream(dev).cuda_stream))
+    return sel_idx
+
+
+def paged_attn(shape: PagedShape, q, k8, v8, k_scale, v_scale, block_table, row_req, row_pos, *, sel_idx=None, o=None,
+               lse=None, workspace=None, stream=None):
+    """msa_paged_attn: (o [T, Hq, d] bf16, lse [T, Hq] fp32) of q [T, Hq, d] bf16 over
+    the 8-bit cache: the blocks of sel_idx [T, Hkv, topk], or all of them when it is None."""
+    s, i32, f32, dev = shape, torch.int32, torch.float32, q.device
+    specs = [(q, "q", (s.T, s.Hq, s.d), torch.bfloat16), (k8, "k8", (s.n_pages, s.Hkv, PAGE, s.d), torch.float8_e4m3fn),
+             (v8, "v8", (s.n_pages, s.Hkv, PAGE, s.d), torch.float8_e4m3fn), (k_scale, "k_scale", (s.n_pages, s.Hkv), f32),
+             (v_scale, "v_scale", (s.n_pages, s.Hkv), f32), (block_table, "block_table", (s.R, s.max_blocks), i32),
+             (row_req, "row_req", (s.T,), i32), (row_pos, "row_pos", (s.T,), i32)]
+    if sel_idx is not None:
+        specs.append((sel_idx, "sel_idx", (s.T, s.Hkv, s.topk), i32))
+    if o is not None:
+        specs.append((o, "o", (s.T, s.Hq, s.d), torch.bfloat16))
+    if lse is not None:
+        specs.append((lse, "lse", (s.T, s.Hq), f32))
+    _need_on(dev, specs)
+    with _place(q, stream):
+        ws = _paged_ws(workspace, s, OP_PAGED_ATTN, dev)
+        o = torch.empty((s.T, s.Hq, s.d), dtype=torch.bfloat16, device=dev) if o is None else o
+        lse = torch.empty((s.T, s.Hq), dtype=f32, device=dev) if lse is None else lse
+        _check(lib().msa_paged_attn(s._ref, q.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                    block_table.data_ptr(), row_req.data_ptr(), row_pos.data_ptr(),
+                                    None if sel_idx is None else sel_idx.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                    ws.data_ptr(), ws.numel(), torch.cuda.current_stream(dev).cuda_stream))
+    return o, lse
 
 
 def check_device_status(workspace, stream=None) -> None:

@@ -1,0 +1,67 @@
+// paged.h -- problem description and launchers of the paged-cache operators
+// (plan, append, block scores, block selection, attention), shared by their
+// C-ABI layer (paged_api.cu) and kernels.
+#pragma once
+
+#include "msa_internal.h"
+
+namespace msa {
+
+constexpr int kPage = 128;   // tokens of a page: one MSA block
+
+struct PagedProblem {
+    int R, T, max_blocks, n_pages, Hq, Hkv, G, d, d_idx, topk;
+    float scale, scale_idx;
+    int num_sms;
+};
+
+// Entries of a plan's segment list: a request of n new tokens touches at most
+// 2 + n/128 pages and at most n of them.
+inline int paged_segments(const PagedProblem &p)
+{
+    const long long s = 2LL * p.R + p.T / kPage;
+    return s < p.T ? (int)s : p.T;
+}
+
+// The least power of two s with amax <= 448 s (448: the largest e4m3 value),
+// at least 2^-112, as fp32 bits, from the bits of |amax| in bf16: with
+// amax = m 2^x, m in [1, 2), s = 2^(x-8) when m <= 1.75 and 2^(x-7) above.
+__host__ __device__ __forceinline__ uint32_t pow2_scale_bits(uint32_t abs_bf16)
+{
+    int e = (int)(abs_bf16 >> 7) - 127 - 8 + ((abs_bf16 & 0x7Fu) > 0x60u ? 1 : 0);
+    if (abs_bf16 == 0 || e < -112) e = -112;
+    return (uint32_t)(e + 127) << 23;
+}
+
+// 3-D byte TMA tensor map (dims innermost first), box {box0, box1, 1}, with a
+// 128-byte (box0 = 128) or 64-byte (box0 = 64) swizzle, zero fill out of bounds.
+cudaError_t make_tmap_u8_3d(CUtensorMap *map, const void *base, unsigned long long d0, unsigned long long d1,
+                            unsigned long long d2, unsigned box0, unsigned box1);
+
+struct PlanArgs {
+    const int32_t *new_lens, *lens_in, *ended, *free_in;
+    int32_t *block_table, *free_pages, *lens_out, *free_out, *q_starts, *row_req, *row_pos, *slots, *segs;
+};
+size_t paged_plan_scratch_ints(const PagedProblem &p);
+cudaError_t launch_paged_plan(const PagedProblem &p, const PlanArgs &a, int32_t *scratch, DeviceStatus *st, cudaStream_t s);
+
+cudaError_t launch_paged_append(const PagedProblem &p, const bf16 *k_new, const bf16 *v_new, const bf16 *ki_new,
+                                const int32_t *slots, const int32_t *segs, uint8_t *k8, uint8_t *v8, float *k_scale,
+                                float *v_scale, bf16 *k_idx, DeviceStatus *st, cudaStream_t s);
+
+cudaError_t launch_paged_block_scores(const PagedProblem &p, const bf16 *q_idx, const bf16 *k_idx,
+                                      const int32_t *block_table, const int32_t *q_starts, const int32_t *row_req,
+                                      const int32_t *row_pos, float *scores, DeviceStatus *st, cudaStream_t s);
+
+cudaError_t launch_paged_block_topk(const PagedProblem &p, const float *scores, const int32_t *row_pos, int32_t *sel,
+                                    DeviceStatus *st, cudaStream_t s);
+
+// Floats of partial outputs and (max, sum) pairs, for either form (with a
+// selection and without).
+size_t paged_attn_scratch_floats(const PagedProblem &p);
+cudaError_t launch_paged_attn(const PagedProblem &p, const bf16 *q, const uint8_t *k8, const uint8_t *v8,
+                              const float *k_scale, const float *v_scale, const int32_t *block_table,
+                              const int32_t *row_req, const int32_t *row_pos, const int32_t *sel, bf16 *o, float *lse,
+                              float *scratch, DeviceStatus *st, cudaStream_t s);
+
+}  // namespace msa

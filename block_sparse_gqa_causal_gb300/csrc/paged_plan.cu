@@ -1,0 +1,236 @@
+// paged_plan.cu -- the plan of a serving step over a paged cache: which pages
+// the step's new tokens take, each row's request, position and cache slot.
+//
+// Request r holds ceil(l/128) pages for its l tokens and brings n new ones; it
+// takes ceil((l+n)/128) - ceil(l/128) pages from the front of a ring of free
+// pages, requests in order.  A request that ended gives its pages back behind
+// the ring's free ones, so a step's releases never meet its takes and the two
+// need no order.  Everything else is exclusive sums over the requests: first
+// row, first page taken, first segment.
+//
+// One CTA sums (the work is a few thousand integers; latency is all there is)
+// and decides whether the step fits before anything is written.  Rows are
+// independent after that: a row finds its request by bisection of q_starts.
+// Up to kFusedRows rows the same CTA fills them, a launch fewer; above that a
+// second kernel does.
+#include <algorithm>
+
+#include "paged.h"
+
+namespace msa {
+namespace {
+
+constexpr int kFusedRows = 4096;
+constexpr int kFillThreads = 256;
+
+// scratch: {ring head, segments, -, -}, then per request {first page taken,
+// first segment, length before, pages held before}
+__device__ __forceinline__ int pages_of(int n) { return (n + kPage - 1) / kPage; }
+
+__device__ __forceinline__ void fill_entry(const PagedProblem &p, const PlanArgs &a, const int32_t *scratch, int S,
+                                           int n_rows, int n_segs, int head, int i, DeviceStatus *st)
+{
+    if (i >= n_segs && i <= S) a.segs[i] = n_rows;
+    if (i >= p.T) return;
+    if (i >= n_rows) {
+        a.row_req[i] = -1;
+        a.row_pos[i] = -1;
+        a.slots[i] = -1;
+        return;
+    }
+    int lo = 0, hi = p.R;                       // the last r with q_starts[r] <= i
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.q_starts[mid] <= i) lo = mid;
+        else hi = mid;
+    }
+    const int4 rq = reinterpret_cast<const int4 *>(scratch)[1 + lo];
+    const int q0 = a.q_starts[lo];
+    const int pos = rq.z + (i - q0), blk = pos / kPage, off = pos % kPage;
+    int32_t *entry = a.block_table + (long long)lo * p.max_blocks + blk;
+    int page;
+    if (blk >= rq.w) {
+        page = a.free_pages[((long long)head + rq.x + (blk - rq.w)) % p.n_pages];
+        if (off == 0) *entry = page;            // every page taken is opened by one row of the step
+    } else {
+        page = *entry;                          // the partly filled last page
+    }
+    a.row_req[i] = lo;
+    a.row_pos[i] = pos;
+    if ((unsigned)page < (unsigned)p.n_pages) {
+        a.slots[i] = page * kPage + off;
+    } else {
+        a.slots[i] = -1;
+        report(st, kDevCheck, 102, page);
+    }
+    if (i == q0 || off == 0) a.segs[rq.y + blk - rq.z / kPage] = i;
+}
+
+struct Sums {
+    long long rows, take, gone, segs;
+};
+__device__ __forceinline__ Sums operator+(const Sums &x, const Sums &y)
+{
+    return {x.rows + y.rows, x.take + y.take, x.gone + y.gone, x.segs + y.segs};
+}
+__device__ __forceinline__ Sums shfl_up(const Sums &x, int d)
+{
+    return {__shfl_up_sync(0xffffffffu, x.rows, d), __shfl_up_sync(0xffffffffu, x.take, d),
+            __shfl_up_sync(0xffffffffu, x.gone, d), __shfl_up_sync(0xffffffffu, x.segs, d)};
+}
+
+__global__ void __launch_bounds__(1024) plan_kernel(PagedProblem p, PlanArgs a, int32_t *scratch, int S, int fused,
+                                                    DeviceStatus *st)
+{
+    __shared__ Sums warp_sum[32];
+    __shared__ int bad;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, nwarp = nthr >> 5;
+    const int head = a.free_in[0], count = a.free_in[1];
+    const int most = p.max_blocks * kPage;
+    if (tid == 0) bad = 0;
+    __syncthreads();
+
+    struct Req {
+        int had, old, n, held, after;
+        Sums s;
+    };
+    auto load = [&](int r) {
+        Req q{};
+        if (r < p.R) {
+            q.had = a.lens_in[r];
+            q.n = a.new_lens[r];
+            const bool ended = a.ended && a.ended[r] != 0;
+            if (q.had < 0 || q.had > most || q.n < 0 || q.n > most - (ended ? 0 : q.had)) {
+                bad = 1;
+                return q;
+            }
+            q.old = ended ? 0 : q.had;
+            q.held = pages_of(q.old);
+            q.after = pages_of(q.old + q.n);
+            q.s = {q.n, q.after - q.held, ended ? pages_of(q.had) : 0, q.n > 0 ? q.after - q.old / kPage : 0};
+        }
+        return q;
+    };
+    // exclusive sum over the CTA's requests of this round; the round's total too
+    auto scan = [&](const Sums &x, Sums &total) {
+        Sums inc = x;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const Sums o = shfl_up(inc, d);
+            if (lane >= d) inc = inc + o;
+        }
+        __syncthreads();
+        if (lane == 31) warp_sum[warp] = inc;
+        __syncthreads();
+        Sums before{}, all{};
+        for (int w = 0; w < nwarp; ++w) {
+            if (w < warp) before = before + warp_sum[w];
+            all = all + warp_sum[w];
+        }
+        total = all;
+        return Sums{before.rows + inc.rows - x.rows, before.take + inc.take - x.take, before.gone + inc.gone - x.gone,
+                    before.segs + inc.segs - x.segs};
+    };
+
+    // the step's totals decide whether it fits; nothing is written before that
+    Sums total{};
+    Req one{};
+    Sums one_at{};
+    for (int base = 0; base < p.R; base += nthr) {
+        const Req q = load(base + tid);
+        Sums t;
+        const Sums at = scan(q.s, t);
+        one = q;
+        one_at = {total.rows + at.rows, total.take + at.take, total.gone + at.gone, total.segs + at.segs};
+        total = total + t;
+    }
+    const bool ring_ok = head >= 0 && head < p.n_pages && count >= 0 && count <= p.n_pages;
+    int why = 0;
+    if (bad) why = 1;                                            // a length out of range
+    else if (!ring_ok || total.gone + count > p.n_pages) why = 2;  // the ring's state
+    else if (total.rows > p.T) why = 3;                          // more rows than T
+    else if (total.take > count) why = 4;                        // too few free pages
+    if (why) {
+        if (tid == 0) report(st, kDevCheck, 101, why);
+        total = Sums{};
+    }
+    if (tid == 0) {
+        scratch[0] = head;
+        scratch[1] = (int)total.segs;
+    }
+    const bool single = p.R <= nthr;                             // the scan above already is the whole one
+    Sums run{};
+    for (int base = 0; base < p.R; base += nthr) {
+        const int r = base + tid;
+        Req q;
+        Sums at;
+        if (single) {
+            q = one;
+            at = one_at;
+        } else {
+            q = load(r);
+            Sums t;
+            at = scan(q.s, t);
+            at = at + run;
+            run = run + t;
+        }
+        if (r < p.R) {
+            a.q_starts[r] = why ? 0 : (int)at.rows;
+            a.lens_out[r] = why ? a.lens_in[r] : q.old + q.n;
+            if (!why) reinterpret_cast<int4 *>(scratch)[1 + r] = make_int4((int)at.take, (int)at.segs, q.old, q.held);
+        }
+        // pages of ended requests go behind the free ones, a warp to a request
+        unsigned todo = __ballot_sync(0xffffffffu, !why && q.s.gone > 0);
+        while (todo) {
+            const int l = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const int n = __shfl_sync(0xffffffffu, (int)q.s.gone, l), b = __shfl_sync(0xffffffffu, (int)at.gone, l);
+            const int32_t *row = a.block_table + (long long)(base + (warp << 5) + l) * p.max_blocks;
+            for (int j = lane; j < n; j += 32)
+                a.free_pages[((long long)head + count + b + j) % p.n_pages] = row[j];
+        }
+    }
+    if (tid == 0) {
+        a.q_starts[p.R] = (int)total.rows;
+        a.free_out[0] = why ? head : (int)((head + total.take) % p.n_pages);
+        a.free_out[1] = why ? count : (int)(count - total.take + total.gone);
+    }
+    if (!fused) return;
+    __syncthreads();
+    const int n = max(p.T, S + 1);
+    for (int i = tid; i < n; i += nthr)
+        fill_entry(p, a, scratch, S, (int)total.rows, (int)total.segs, head, i, st);
+}
+
+__global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(PagedProblem p, PlanArgs a, const int32_t *scratch, int S,
+                                                                 DeviceStatus *st)
+{
+    const int i = blockIdx.x * kFillThreads + threadIdx.x;
+    fill_entry(p, a, scratch, S, a.q_starts[p.R], scratch[1], scratch[0], i, st);
+}
+
+}  // namespace
+
+size_t paged_plan_scratch_ints(const PagedProblem &p) { return 4 + 4 * (size_t)p.R; }
+
+cudaError_t launch_paged_plan(const PagedProblem &p, const PlanArgs &a, int32_t *scratch, DeviceStatus *st, cudaStream_t s)
+{
+    const int S = paged_segments(p);
+    const bool fused = p.T <= kFusedRows;
+    const int want = std::max(p.R, fused ? p.T : 1);
+    const int threads = std::min(1024, std::max(64, (want + 31) / 32 * 32));
+    {
+        TimedLaunch timed_("paged_plan_kernel", s);
+        plan_kernel<<<1, threads, 0, s>>>(p, a, scratch, S, fused ? 1 : 0, st);
+    }
+    note_launch();
+    if (!fused) {
+        const int n = std::max(p.T, S + 1);
+        TimedLaunch timed_("paged_plan_fill_kernel", s);
+        plan_fill_kernel<<<(n + kFillThreads - 1) / kFillThreads, kFillThreads, 0, s>>>(p, a, scratch, S, st);
+        note_launch();
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace msa

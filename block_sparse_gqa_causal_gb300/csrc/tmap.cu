@@ -2,7 +2,7 @@
 // driver entry point, so the library needs no link-time libcuda.
 #include <cudaTypedefs.h>
 
-#include "msa_internal.h"
+#include "paged.h"
 
 namespace msa {
 
@@ -39,6 +39,21 @@ cudaError_t make_tmap_bf16(CUtensorMap *map, const void *base, int rank, const u
     CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(base), d, str, bx, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t make_tmap_u8_3d(CUtensorMap *map, const void *base, unsigned long long d0, unsigned long long d1,
+                            unsigned long long d2, unsigned box0, unsigned box1)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (!fn) return cudaErrorNotSupported;
+    if (box0 != 128 && box0 != 64) return cudaErrorInvalidValue;
+    const cuuint64_t d[3] = {d0, d1, d2}, str[2] = {d0, d0 * d1};
+    const cuuint32_t bx[3] = {box0, box1, 1}, estr[3] = {1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), d, str, bx, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    box0 == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 

@@ -326,6 +326,137 @@ msa_status msa_block_mask(const msa_shape *shape, const int32_t *sel_idx, uint32
 msa_status msa_kv_append(const msa_shape *shape, const void *k_new, const void *v_new, const void *k_idx_new,
                          void *k, void *v, void *k_idx, void *stream);
 
+/*
+ * Serving from a paged cache: the calls of one step (decoding, speculative
+ * rows, prompt chunks, mixed) over a ragged batch of requests.  "Sparse
+ * Attention · Part II" defines the attention and its selection (section 3.2)
+ * and names the KV cache's reading as what dominates decoding (section 4.1);
+ * it says nothing of how caches are stored.  Here they live in pages of 128
+ * tokens (MSA's block) from one pool, K and V in 8 bits.
+ *
+ *   R requests, T rows (the step's query tokens, one after another by request;
+ *   T is the capacity of the row arrays: rows behind the last request carry
+ *   row_req = row_pos = slots = -1, and every call leaves their outputs as
+ *   they were)
+ *   block_table [R, max_blocks] int32   page of each of a request's blocks
+ *   q_starts    [R + 1] int32           first row of each request
+ *   row_req, row_pos, slots [T] int32   a row's request, absolute position and
+ *                                       cache slot (page * 128 + offset)
+ *   segs        [S + 1] int32, S = min(T, 2 R + T / 128): first row of each
+ *                                       run of rows of one request on one page,
+ *                                       ascending; the entries left over hold
+ *                                       the number of rows
+ *   k8, v8      [n_pages, Hkv, 128, d]  e4m3 codes
+ *   k_scale, v_scale [n_pages, Hkv]     fp32, powers of two: a row's values
+ *                                       are code * scale
+ *   k_idx       [n_pages, 128, d_idx]   bf16
+ * A row at position p sees its request's tokens 0 .. p.  All shape fields have
+ * to be valid in every call.  Supported: d, d_idx in {64, 128}; Hq/Hkv in
+ * {1, 2, 4, 8}; topk <= 32; max_blocks, n_pages <= 2^23; R <= 2^24; Hkv <=
+ * 32768; n_pages * Hkv < 2^31; T * Hq < 2^24.  16-byte alignment of the bf16
+ * and code arrays, 4-byte of the others.  Every call takes a workspace of
+ * msa_paged_workspace_size bytes with the status word of the other calls.
+ * What device memory says (lengths, pages, selections) is checked on the
+ * device: an entry out of range is left out and recorded in the status word.
+ */
+typedef struct {
+    int R, T, max_blocks, n_pages, Hq, Hkv, d, d_idx, topk;
+    float scale;         /* main logit scale; 0 -> 1/sqrt(d) */
+    float scale_idx;     /* index score scale; 0 -> 1/sqrt(d_idx) */
+} msa_paged_shape;
+
+enum {
+    MSA_OP_PAGED_PLAN = 16,
+    MSA_OP_PAGED_APPEND = 17,
+    MSA_OP_PAGED_BLOCK_SCORES = 18,
+    MSA_OP_PAGED_BLOCK_TOPK = 19,
+    MSA_OP_PAGED_ATTN = 20
+};
+size_t msa_paged_workspace_size(const msa_paged_shape *shape, int op);
+
+/*
+ * The plan of a step: block tables, slot maps and page allocation from the
+ * requests' lengths.  Request r has lens_in[r] tokens cached and brings
+ * new_lens[r] (0 or more).  ended (may be NULL) marks slots whose request is
+ * over: its pages go back first, and the slot's new tokens, if any, are the
+ * first of another request.
+ *   free_pages [n_pages]  ring of free pages; free_in = {head, count}: the
+ *                         free ones are free_pages[(head + i) % n_pages], i < count
+ * Takes ceil((l + n)/128) - ceil(l/128) pages for each request, requests in
+ * order, from the ring's head, and writes them to block_table (columns that
+ * are already held stay as they are); pages of ended requests are written
+ * behind the free ones, in the order of slots and blocks.  Writes lens_out
+ * (= l + n), free_out, q_starts, row_req, row_pos, slots and segs.  lens_out
+ * may be lens_in and free_out may be free_in; no other arrays may overlap.
+ * A step that does not fit (a negative length, one past 128 * max_blocks,
+ * more rows than T, too few free pages, a ring state out of range) is not
+ * made: lengths, ring and block_table stay as they were, the plan has no rows
+ * (q_starts 0, every row -1), and the status word is set.
+ */
+msa_status msa_paged_plan(const msa_paged_shape *shape, const int32_t *new_lens, const int32_t *lens_in,
+                          const int32_t *ended, int32_t *block_table, int32_t *free_pages, const int32_t *free_in,
+                          int32_t *lens_out, int32_t *free_out, int32_t *q_starts, int32_t *row_req, int32_t *row_pos,
+                          int32_t *slots, int32_t *segs, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * New tokens into the paged cache: k_new, v_new [T, Hkv, d] and k_idx_new
+ * [T, d_idx] bf16, the rows of segs to the slots of each segment's first row
+ * and those behind it.  Per page and KV head, K and V each:
+ *   s     = max(the page's scale if it already holds tokens,
+ *               the least power of two (>= 2^-112) with |x| <= 448 s for the new rows)
+ *   codes = x / s rounded to e4m3 (nearest, ties to even); codes already on
+ *           the page are rounded to the new scale when it grew (exact unless
+ *           they become e4m3 subnormals)
+ * A NaN or infinite x becomes a NaN code and does not enter s.  K_idx rows are
+ * copied.  k_new, v_new and their caches may all be NULL, and so may
+ * k_idx_new and k_idx.  A page is written by one segment of a step; rows of a
+ * page behind the tokens written are left as they were.
+ */
+msa_status msa_paged_append(const msa_paged_shape *shape, const void *k_new, const void *v_new, const void *k_idx_new,
+                            const int32_t *slots, const int32_t *segs, void *k8, void *v8, float *k_scale, float *v_scale,
+                            void *k_idx, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * msa_index_select's block scores for a ragged batch: for row t, group g and
+ * block c of the row's request,
+ *   block_scores[t, g, c] = max over tokens j <= row_pos[t] of block c of
+ *                           scale_idx * <q_idx[t, g, :], k_idx[j, :]>
+ * and -inf for blocks past the row's own.  q_idx [T, Hkv, d_idx] bf16,
+ * block_scores [T, Hkv, max_blocks] fp32.  A token whose score is NaN is
+ * passed over.
+ */
+msa_status msa_paged_block_scores(const msa_paged_shape *shape, const void *q_idx, const void *k_idx,
+                                  const int32_t *block_table, const int32_t *q_starts, const int32_t *row_req,
+                                  const int32_t *row_pos, float *block_scores, void *workspace, size_t workspace_bytes,
+                                  void *stream);
+
+/*
+ * msa_index_select's selection for a ragged batch, from block scores: the
+ * row's own block c0 = row_pos / 128 and the topk - 1 blocks c < c0 of largest
+ * score, ties to the lower block (-0 = +0, a NaN ranks as -inf); all blocks
+ * when c0 < topk.  sel_idx [T, Hkv, topk] int32, ascending, then -1.
+ */
+msa_status msa_paged_block_topk(const msa_paged_shape *shape, const float *block_scores, const int32_t *row_pos,
+                                int32_t *sel_idx, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * msa_sparse_attn_fwd for a ragged batch over the 8-bit cache: for row t and
+ * head h of group g, over the tokens j <= row_pos[t] of the blocks in
+ * sel_idx[t, g, :] (every block of the request when sel_idx is NULL),
+ *   l_j = scale * <q[t, h, :], k_j>,  o = sum_j softmax(l)_j v_j,
+ *   lse[t, h] = log sum_j exp(l_j).
+ * q, o [T, Hq, d] bf16, lse [T, Hq] fp32, sel_idx [T, Hkv, topk] int32,
+ * distinct and ascending with -1 anywhere; an entry that does not ascend or
+ * lies past the row's own block is left out and recorded in the status word.
+ * A row without any block has o = 0 and lse = -inf.  Queries and
+ * probabilities enter the products with 8 significant bits or more, sums are
+ * fp32.  Deterministic.
+ */
+msa_status msa_paged_attn(const msa_paged_shape *shape, const void *q, const void *k8, const void *v8, const float *k_scale,
+                          const float *v_scale, const int32_t *block_table, const int32_t *row_req, const int32_t *row_pos,
+                          const int32_t *sel_idx, void *o, float *lse, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
 /* Message of the last failed call on this host thread ("" if none). */
 const char *msa_last_error(void);
 
