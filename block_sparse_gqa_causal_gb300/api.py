@@ -431,6 +431,15 @@ def _place(t: torch.Tensor, stream):
     return _HERE_CTX
 
 
+# The current stream's handle of a device; the public call builds a Stream object first, which
+# costs as much as half of a small kernel's launch.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(dev) -> int:
+    return _raw_stream(dev.index) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
 def _need_on(dev, specs) -> None:
     """_need for several (tensor, name, shape, dtype), all on one CUDA device."""
     for t, name, shape, dtype in specs:
@@ -481,11 +490,11 @@ def paged_plan(shape: PagedShape, new_lens, lens, block_table, free_pages, free_
     with _place(new_lens, stream):
         ws = _paged_ws(workspace, s, OP_PAGED_PLAN, dev)
         if out is None:
-            out = PagedPlan(*torch.empty(sum(sizes), dtype=i32, device=dev).split(sizes))
+            out = PagedPlan(*[torch.empty(n, dtype=i32, device=dev) for n in sizes])
         _check(lib().msa_paged_plan(s._ref, new_lens.data_ptr(), lens.data_ptr(), None if ended is None else ended.data_ptr(),
                                     block_table.data_ptr(), free_pages.data_ptr(), free_state.data_ptr(),
                                     *[t.data_ptr() for t in out], ws.data_ptr(), ws.numel(),
-                                    torch.cuda.current_stream(dev).cuda_stream))
+                                    _stream_on(dev)))
     return out
 
 
@@ -510,7 +519,7 @@ def paged_append(shape: PagedShape, k_new, v_new, k_idx_new, slots, segs, k8, v8
     ptr = [None if t is None else t.data_ptr() for t in (k_new, v_new, k_idx_new, slots, segs, k8, v8, k_scale, v_scale, k_idx)]
     with _place(slots, stream):
         ws = _paged_ws(workspace, s, OP_PAGED_APPEND, dev)
-        _check(lib().msa_paged_append(s._ref, *ptr, ws.data_ptr(), ws.numel(), torch.cuda.current_stream(dev).cuda_stream))
+        _check(lib().msa_paged_append(s._ref, *ptr, ws.data_ptr(), ws.numel(), _stream_on(dev)))
 
 
 def paged_block_scores(shape: PagedShape, q_idx, k_idx, block_table, q_starts, row_req, row_pos, *, block_scores=None,
@@ -531,7 +540,7 @@ def paged_block_scores(shape: PagedShape, q_idx, k_idx, block_table, q_starts, r
         _check(lib().msa_paged_block_scores(s._ref, q_idx.data_ptr(), k_idx.data_ptr(), block_table.data_ptr(),
                                             q_starts.data_ptr(), row_req.data_ptr(), row_pos.data_ptr(),
                                             block_scores.data_ptr(), ws.data_ptr(), ws.numel(),
-                                            torch.cuda.current_stream(dev).cuda_stream))
+                                            _stream_on(dev)))
     return block_scores
 
 
@@ -547,7 +556,7 @@ def paged_block_topk(shape: PagedShape, block_scores, row_pos, *, sel_idx=None, 
         if sel_idx is None:
             sel_idx = torch.empty((s.T, s.Hkv, s.topk), dtype=torch.int32, device=dev)
         _check(lib().msa_paged_block_topk(s._ref, block_scores.data_ptr(), row_pos.data_ptr(), sel_idx.data_ptr(),
-                                          ws.data_ptr(), ws.numel(), torch.cuda.current_stream(dev).cuda_stream))
+                                          ws.data_ptr(), ws.numel(), _stream_on(dev)))
     return sel_idx
 
 
@@ -574,7 +583,7 @@ def paged_attn(shape: PagedShape, q, k8, v8, k_scale, v_scale, block_table, row_
         _check(lib().msa_paged_attn(s._ref, q.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                     block_table.data_ptr(), row_req.data_ptr(), row_pos.data_ptr(),
                                     None if sel_idx is None else sel_idx.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                                    ws.data_ptr(), ws.numel(), torch.cuda.current_stream(dev).cuda_stream))
+                                    ws.data_ptr(), ws.numel(), _stream_on(dev)))
     return o, lse
 
 

@@ -5,6 +5,7 @@
 #include <stdio.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "msa.h"
 #include "paged.h"
@@ -27,11 +28,16 @@ msa_status refuse(msa_status st, const char *fmt, ...)
     return set_error(st, buf);
 }
 
+// SMs of the current device (asked for once per device).
 int current_sms()
 {
+    static std::atomic<int> known[64];
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+    const bool keep = dev >= 0 && dev < 64;
+    if (keep && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+    if (keep) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 

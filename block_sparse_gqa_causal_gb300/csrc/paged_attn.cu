@@ -16,17 +16,21 @@
 // two to fill the range), and the probabilities with the precision that bf16
 // gives them.  Sums, maxima and the outputs are fp32.
 //
-// A producer warp streams pages (K and V tiles of one head, contiguous and
-// swizzled by TMA) through a ring of stages.  Each of four warps takes 32 of a
-// page's 128 tokens and keeps its own running maximum, sum and output; they
-// are joined at the end.  V's operand needs its tokens along a register:
-// ldmatrix with 8-bit transposition gives that from the row-major tile.  The
-// tokens' order inside a 32-token step is chosen so that a lane's scores are
-// the probabilities it has to feed back and no shared-memory phase has a bank
-// conflict.
+// Each of four warps takes 32 of a page's 128 tokens and keeps its own running
+// maximum, sum and output; they are joined where a row ends.  V's operand
+// needs its tokens along a register: ldmatrix with 8-bit transposition gives
+// that from the row-major tile.  The tokens' order inside a 32-token step is
+// chosen so that a lane's scores are the probabilities it has to feed back and
+// no shared-memory phase has a bank conflict.
 //
-// A row's blocks are cut into shares of `per` blocks, one CTA to a share; a
-// second kernel joins the shares' states where there is more than one.
+// The work is one long list of blocks, those of (row 0, group 0), then (row 0,
+// group 1) and so on, cut into equal stretches for the two CTAs that each SM
+// holds.  So every CTA reads the same number of pages whatever the rows'
+// lengths, and a producer warp streams the stretch through one ring of stages
+// (K and V tiles of a page and head, contiguous and swizzled by TMA) without a
+// pause where a row ends and the next begins.  A stretch ends inside a row at
+// most twice; those pieces' states go to the workspace, and a second kernel
+// joins each cut row's pieces in order.
 #include <algorithm>
 #include <type_traits>
 
@@ -42,18 +46,27 @@ constexpr int kWarps = 4;                       // consumer warps, 32 tokens of 
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kStages = 3;
 
+constexpr int kPrefixRows = 512;                // most rows whose blocks are cut evenly; above, whole rows are dealt out
+constexpr int kMinBlocks = 2;                   // a stretch has at least this many blocks
+
+enum { kFirst = 1, kLast = 2, kEnd = 4 };       // of a piece; of the CTA's stretch
 struct Meta {
-    int len;        // visible tokens of the block; -1 after the last block
+    int len;        // visible tokens of the block
     float ks, vs;   // the page's scales for this head
+    int flags;
+    int t, r;       // the piece's row and group
+    int part;       // the piece's place among the partial states; -1: a whole row
 };
 
 template <int D>
 struct AttnSmem {
     static constexpr int TILE = kPage * D;      // K or V codes of a page and head
     static constexpr int STAGE = 2 * TILE;
-    static constexpr int BYTES = kStages * STAGE + 1024;   // + alignment
+    static constexpr int Q = 8 * D * 2;         // the group's queries, with a piece's first block
+    static constexpr int OFF_Q = kStages * STAGE;
+    static constexpr int OFF_O = OFF_Q + kStages * Q;
+    static constexpr int BYTES = OFF_O + 8 * D * 4 + 1024;   // + alignment
 };
-static_assert(AttnSmem<64>::STAGE * kStages >= kWarps * 8 * 64 * 4 + 512, "the warps' states fit the stages");
 
 // byte offset of 16-byte word w of token row r in a TMA-swizzled tile
 template <int D>
@@ -102,11 +115,17 @@ __device__ __forceinline__ void split4(float x0, float x1, float x2, float x3, u
     lo = e4m3x2(16.f * (x0 - f01.x), 16.f * (x1 - f01.y)) | (e4m3x2(16.f * (x2 - f23.x), 16.f * (x3 - f23.y)) << 16);
 }
 
-// The share's blocks, 32 at a time: what lane `lane` holds of them.
-struct Entry {
-    int page, len;
-    float ks, vs;
+// A cut row: its (row, group) and the CTAs that hold its pieces.
+struct CutRow {
+    int pair, first, last, pad;
 };
+
+MSA_DEV void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -114,31 +133,32 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
             const __grid_constant__ CUtensorMap tm_v, const float *__restrict__ k_scale,
             const float *__restrict__ v_scale, const int32_t *__restrict__ block_table,
             const int32_t *__restrict__ row_req, const int32_t *__restrict__ row_pos, const int32_t *__restrict__ sel,
-            bf16 *__restrict__ o, float *__restrict__ lse, int per, int shares, float *__restrict__ part_o,
-            float2 *__restrict__ part_ml, DeviceStatus *st)
+            bf16 *__restrict__ o, float *__restrict__ lse, float *__restrict__ part_o, float2 *__restrict__ part_ml,
+            CutRow *__restrict__ cut, DeviceStatus *st)
 {
     using S = AttnSmem<D>;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     __shared__ uint64_t full[kStages], empty[kStages];
     __shared__ Meta meta[kStages];
+    __shared__ float sM[kWarps][8], sL[kWarps][8];
+    __shared__ long long before[kPrefixRows + 1];   // blocks of the rows before each row, one group
     __shared__ int abort_flag;
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int sp = blockIdx.x % shares;
-    const int rt = blockIdx.x / shares, r = rt % p.Hkv, t = rt / p.Hkv;
-    const int req = row_req[t], pos = row_pos[t];
-    if (req < 0 || pos < 0) return;                    // a row behind the last request
-    const int c0 = pos / kPage;
-    if (req >= p.R || c0 >= p.max_blocks) {
-        if (tid == 0) report(st, kDevCheck, 141, req >= p.R ? req : pos);
-        return;
-    }
-    // without a selection a short row has fewer shares than the longest
-    const int lo = sp * per, hi = sel ? min(lo + per, p.topk) : min(lo + per, c0 + 1);
-    if (!sel && lo > c0) return;
-    const bool alone = shares == 1 || (!sel && c0 < per);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = p.G;
+    const bool even = p.T <= kPrefixRows;
 
+    // blocks that a group of row t has to look at; 0: not a row (entries of a selection may sit in any of its slots)
+    auto blocks_of = [&](int t, int &req, int &pos) {
+        req = row_req[t];
+        pos = row_pos[t];
+        if (req < 0 || pos < 0) return 0;              // behind the last request
+        if (req >= p.R || pos / kPage >= p.max_blocks) {
+            report(st, kDevCheck, 141, req >= p.R ? req : pos);
+            return 0;
+        }
+        return sel ? p.topk : pos / kPage + 1;
+    };
     if (tid == 0) {
         abort_flag = 0;
         for (int i = 0; i < kStages; ++i) {
@@ -147,104 +167,205 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
         }
         fence_mbar_init();
     }
+    if (even)
+        for (int t = tid; t < p.T; t += kThreads) {
+            int req, pos;
+            before[t] = blocks_of(t, req, pos);
+        }
+    __syncthreads();
+    if (even && warp == 0) {
+        long long sum = 0;
+        for (int t0 = 0; t0 < p.T; t0 += 32) {
+            const long long n = t0 + lane < p.T ? before[t0 + lane] : 0;
+            long long inc = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const long long v = __shfl_up_sync(0xffffffffu, inc, d);
+                if (lane >= d) inc += v;
+            }
+            if (t0 + lane < p.T) before[t0 + lane] = sum + inc - n;
+            sum += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (lane == 0) before[p.T] = sum;
+    }
     __syncthreads();
 
     if (warp == kWarps) {
         int step = 0;
         bool live = true;
-        for (int base = lo; base < hi && live; base += 32) {
-            int c = -1;
-            if (sel) {
-                // selected blocks ascend; an entry that does not, or lies past the row's own block, is no block
-                c = lane < p.topk ? sel[((long long)t * p.Hkv + r) * p.topk + lane] : -1;
-                int before = c;
+        auto publish = [&](const Meta &m, int page) {
+            const int s = step % kStages;
+            if (step >= kStages && !mbar_wait_warp(&empty[s], (step / kStages - 1) & 1, st, 144, &abort_flag)) {
+                live = false;
+                return;
+            }
+            if (lane == 0) {
+                meta[s] = m;
+                const int boxes = (m.len + 31) / 32;           // 32-token boxes, none past the row
+                const uint32_t qb = m.flags & kFirst ? G * D * 2 : 0, bytes = boxes * 64 * D + qb;
+                if (bytes) mbar_arrive_expect_tx(&full[s], bytes);
+                else mbar_arrive(&full[s]);
+                if (qb) bulk_load(smem + S::OFF_Q + s * S::Q, q + ((long long)m.t * p.Hq + (long long)m.r * G) * D, qb, &full[s]);
+                uint8_t *dst = smem + s * S::STAGE;
+                for (int x = 0; x < boxes; ++x)
+                    tma_load_3d(dst + x * 32 * D, &tm_k, &full[s], 0, x * 32, page * p.Hkv + m.r);
+                for (int x = 0; x < boxes; ++x)
+                    tma_load_3d(dst + S::TILE + x * 32 * D, &tm_v, &full[s], 0, x * 32, page * p.Hkv + m.r);
+            }
+            ++step;
+        };
+        // blocks (a selection: slots) j0 .. j1 - 1 of group r of row t
+        auto piece = [&](int t, int r, int req, int pos, int j0, int j1, int part) {
+            const int c0 = pos / kPage;
+            for (int base = j0; base < j1 && live; base += 32) {
+                int c = -1;
+                if (sel) {
+                    // selected blocks ascend; an entry that does not, or lies past the row's own block, is no block
+                    c = lane < p.topk ? sel[((long long)t * p.Hkv + r) * p.topk + lane] : -1;
+                    int most = c;
 #pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int v = __shfl_up_sync(0xffffffffu, before, d);
-                    if (lane >= d) before = max(before, v);
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const int v = __shfl_up_sync(0xffffffffu, most, d);
+                        if (lane >= d) most = max(most, v);
+                    }
+                    most = __shfl_up_sync(0xffffffffu, most, 1);
+                    if (c >= 0 && (c > c0 || (lane > 0 && c <= most))) {
+                        report(st, kDevCheck, 142, c);
+                        c = -1;
+                    }
+                    if (lane < j0 || lane >= j1) c = -1;
+                } else if (base + lane < j1) {
+                    c = base + lane;
                 }
-                before = __shfl_up_sync(0xffffffffu, before, 1);
-                if (c >= 0 && (c > c0 || (lane > 0 && c <= before))) {
-                    report(st, kDevCheck, 142, c);
-                    c = -1;
+                int page = -1, len = 0;
+                float ks = 0.f, vs = 0.f;
+                if (c >= 0) {
+                    page = block_table[(long long)req * p.max_blocks + c];
+                    if ((unsigned)page >= (unsigned)p.n_pages) {
+                        report(st, kDevCheck, 143, page);
+                    } else {
+                        len = min(kPage, pos - c * kPage + 1);
+                        ks = k_scale[(long long)page * p.Hkv + r];
+                        vs = v_scale[(long long)page * p.Hkv + r];
+                    }
                 }
-                c = __shfl_sync(0xffffffffu, c, (base + lane) & 31);
-                if (base + lane >= hi) c = -1;
-            } else if (base + lane < hi) {
-                c = base + lane;
+                // a block without a page is an empty step, and so is a piece without any block
+                unsigned todo = __ballot_sync(0xffffffffu, c >= 0);
+                if (sel && !todo) todo = 1;
+                bool first = base == j0;
+                while (todo && live) {
+                    const int l = __ffs(todo) - 1;
+                    todo &= todo - 1;
+                    Meta m;
+                    m.len = __shfl_sync(0xffffffffu, len, l);
+                    m.ks = __shfl_sync(0xffffffffu, ks, l);
+                    m.vs = __shfl_sync(0xffffffffu, vs, l);
+                    m.flags = (first ? kFirst : 0) | (!todo && (sel || base + 32 >= j1) ? kLast : 0);
+                    m.t = t;
+                    m.r = r;
+                    m.part = part;
+                    first = false;
+                    publish(m, __shfl_sync(0xffffffffu, page, l));
+                }
+                if (sel) break;                        // at most 32 slots: one round
             }
-            Entry e{-1, 0, 0.f, 0.f};
-            if (c >= 0) {
-                e.page = block_table[(long long)req * p.max_blocks + c];
-                if ((unsigned)e.page >= (unsigned)p.n_pages) {
-                    report(st, kDevCheck, 143, e.page);
-                    c = -1;
-                } else {
-                    e.len = min(kPage, pos - c * kPage + 1);
-                    e.ks = k_scale[(long long)e.page * p.Hkv + r];
-                    e.vs = v_scale[(long long)e.page * p.Hkv + r];
+        };
+        const int me = blockIdx.x;
+        CutRow row{-1, 0, 0, 0};
+        if (even) {
+            const long long W = before[p.T] * p.Hkv;
+            const long long n = max(1LL, min((long long)gridDim.x, W / kMinBlocks));
+            long long x = me < n ? W * me / n : 0;
+            const long long x1 = me < n ? W * (me + 1) / n : 0;
+            int t = 0;
+            if (x < x1) {                              // the last row that starts at or before x
+                int hi = p.T;
+                while (hi - t > 1) {
+                    const int mid = (t + hi) >> 1;
+                    if (before[mid] * p.Hkv <= x) t = mid;
+                    else hi = mid;
                 }
             }
-            unsigned todo = __ballot_sync(0xffffffffu, c >= 0);
-            while (todo) {
-                const int l = __ffs(todo) - 1, s = step % kStages;
-                todo &= todo - 1;
-                const int page = __shfl_sync(0xffffffffu, e.page, l), len = __shfl_sync(0xffffffffu, e.len, l);
-                const float ks = __shfl_sync(0xffffffffu, e.ks, l), vs = __shfl_sync(0xffffffffu, e.vs, l);
-                if (step >= kStages && !mbar_wait_warp(&empty[s], (step / kStages - 1) & 1, st, 144, &abort_flag)) {
-                    live = false;
-                    break;
+            while (x < x1 && live) {
+                const int nt = (int)(before[t + 1] - before[t]);
+                const long long y = x - before[t] * p.Hkv;
+                if (y >= (long long)nt * p.Hkv) {
+                    ++t;
+                    continue;
                 }
+                const int r = (int)(y / nt), j0 = (int)(y % nt), j1 = (int)min((long long)nt, j0 + (x1 - x));
+                const bool whole = j0 == 0 && j1 == nt;
+                if (!whole && j0 == 0) {
+                    const long long end = x + nt;      // the last piece is with the CTA that has block end - 1
+                    row = CutRow{t * p.Hkv + r, me, (int)((end * n + W - 1) / W - 1), 0};
+                }
+                piece(t, r, row_req[t], row_pos[t], j0, j1, whole ? -1 : 2 * me + (j0 > 0 ? 0 : 1));
+                x += j1 - j0;
+            }
+            if (lane == 0 && cut) cut[me] = row;
+        } else {
+            const long long pairs = (long long)p.T * p.Hkv;
+            for (long long i = me; i < pairs && live; i += gridDim.x) {
+                int req, pos;
+                const int t = (int)(i / p.Hkv), nt = blocks_of(t, req, pos);
+                if (nt) piece(t, (int)(i % p.Hkv), req, pos, 0, nt, -1);
+            }
+        }
+        const int copied = step;
+        if (live) {
+            const int s = step % kStages;
+            if (step < kStages || mbar_wait_warp(&empty[s], (step / kStages - 1) & 1, st, 144, &abort_flag)) {
                 if (lane == 0) {
-                    meta[s] = Meta{len, ks, vs};
-                    const int boxes = (len + 31) / 32;             // 32-token boxes, none past the row
-                    mbar_arrive_expect_tx(&full[s], boxes * 64 * D);
-                    uint8_t *dst = smem + s * S::STAGE;
-                    for (int x = 0; x < boxes; ++x)
-                        tma_load_3d(dst + x * 32 * D, &tm_k, &full[s], 0, x * 32, page * p.Hkv + r);
-                    for (int x = 0; x < boxes; ++x)
-                        tma_load_3d(dst + S::TILE + x * 32 * D, &tm_v, &full[s], 0, x * 32, page * p.Hkv + r);
+                    meta[s].flags = kEnd;
+                    meta[s].len = 0;
+                    mbar_arrive(&full[s]);
                 }
                 ++step;
             }
         }
-        const int s = step % kStages;
-        if (live && step >= kStages) live = mbar_wait_warp(&empty[s], (step / kStages - 1) & 1, st, 144, &abort_flag);
-        if (live && lane == 0) {
-            meta[s].len = -1;
-            mbar_arrive(&full[s]);
-        }
-        // stay until the last copies have landed
-        for (int k = max(0, step - kStages); k < step; ++k)
-            if (!live || k % kStages != s) mbar_wait_warp(&full[k % kStages], (k / kStages) & 1, st, 145, nullptr);
+        // stay until the last copies have landed (the stage of the end mark has been read)
+        for (int k = max(0, step - kStages); k < copied; ++k) mbar_wait_warp(&full[k % kStages], (k / kStages) & 1, st, 145, nullptr);
+        return;
     }
 
-    const int g = lane >> 2, t4 = lane & 3, G = p.G;
+    const int g = lane >> 2, t4 = lane & 3;
     float acc[D / 8][2];                               // head g, features 8n + 2 t4, + 1
-    float m_run = -INFINITY, l_run = 0.f;
+    float m_run = -INFINITY, l_run = 0.f, sql = 0.f;
+    uint32_t a[D / 32][4];                             // the queries' terms, features 32 ks + 4 t4 .. + 3 and + 16 ..
+    float *sO = reinterpret_cast<float *>(smem + S::OFF_O);
+    const int kw = warp * 32;                          // this warp's first token of a page
+    // K rows: token column j of score tile n is token 8n + (j ^ 4 (n & 1))
+    const int kj = lane & 7, km = lane >> 3;
+    // V rows: probability k (of 16) is lane (k / 4)'s value e = k & 1 of tile (k / 2) & 1
+    const int vk = lane & 15, vn = (vk >> 1) & 1;
+    const int vrow = kw + 16 * (lane >> 4) + 8 * vn + ((2 * (vk >> 2) + (vk & 1)) ^ (4 * vn));
 #pragma unroll
     for (int n = 0; n < D / 8; ++n) acc[n][0] = acc[n][1] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < D / 32; ++ks) a[ks][0] = a[ks][1] = a[ks][2] = a[ks][3] = 0u;
 
-    if (warp < kWarps) {
-        // the queries as hi and lo terms, features 32 ks + 4 t4 .. + 3 and + 16 ..
-        uint32_t a[D / 32][4];
-        float sq;
-        {
+    for (int step = 0;; ++step) {
+        const int s = step % kStages;
+        if (!mbar_wait_warp(&full[s], (step / kStages) & 1, st, 146, &abort_flag)) return;
+        const Meta me = meta[s];
+        if (me.flags & kEnd) return;
+        if (me.flags & kFirst) {
             const bool ok = g < G;
-            const uint2 *src = reinterpret_cast<const uint2 *>(q + ((long long)t * p.Hq + (long long)r * G + (ok ? g : 0)) * D);
+            const uint2 *src = reinterpret_cast<const uint2 *>(smem + S::OFF_Q + s * S::Q + (ok ? g : 0) * D * 2);
             uint2 x[D / 32][2];
             uint32_t top = 0;
 #pragma unroll
             for (int ks = 0; ks < D / 32; ++ks)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    x[ks][e] = ok ? __ldg(src + ks * 8 + e * 4 + t4) : make_uint2(0u, 0u);
+                    x[ks][e] = ok ? src[ks * 8 + e * 4 + t4] : make_uint2(0u, 0u);
                     top = __vmaxu2(top, __vmaxu2(x[ks][e].x & 0x7FFF7FFFu, x[ks][e].y & 0x7FFF7FFFu));
                 }
             top = max(top & 0xFFFFu, top >> 16);
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            sq = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : __uint_as_float(pow2_scale_bits(top));   // NaN: so are the scores
+            // not finite: NaN, and so are the scores
+            const float sq = __uint_as_float(top >= 0x7F80u ? 0x7FC00000u : pow2_scale_bits(top));
             const float inv = 1.f / sq;
 #pragma unroll
             for (int ks = 0; ks < D / 32; ++ks)
@@ -253,184 +374,173 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                     const float2 u = unpack_bf16(x[ks][e].x), v = unpack_bf16(x[ks][e].y);
                     split4(u.x * inv, u.y * inv, v.x * inv, v.y * inv, a[ks][2 * e], a[ks][2 * e + 1]);
                 }
+            sql = sq * (p.scale * kLog2e);
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) acc[n][0] = acc[n][1] = 0.f;
+            m_run = -INFINITY;
+            l_run = 0.f;
         }
-        const float sql = sq * (p.scale * kLog2e);
-        const int kw = warp * 32;                      // this warp's first token of a page
-        // K rows: token column j of score tile n is token 8n + (j ^ 4 (n & 1))
-        const int kj = lane & 7, km = lane >> 3;
-        // V rows: probability k (of 16) is lane (k / 4)'s value e = k & 1 of tile (k / 2) & 1
-        const int vk = lane & 15, vn = (vk >> 1) & 1;
-        const int vrow = kw + 16 * (lane >> 4) + 8 * vn + ((2 * (vk >> 2) + (vk & 1)) ^ (4 * vn));
-
-        for (int step = 0;; ++step) {
-            const int s = step % kStages;
-            if (!mbar_wait_warp(&full[s], (step / kStages) & 1, st, 146, &abort_flag)) break;
-            const Meta me = meta[s];
-            if (me.len < 0) break;
-            if (kw < me.len) {
-                uint8_t *sk = smem + s * S::STAGE, *sv = sk + S::TILE;
-                if (me.len < kw + 32) {
-                    // rows behind the last visible token: whatever they hold must not reach 0 * V
-                    for (int x = lane; x < (kw + 32 - me.len) * (D / 16); x += 32)
-                        reinterpret_cast<uint4 *>(sv + me.len * D)[x] = make_uint4(0u, 0u, 0u, 0u);
-                    fence_proxy_async();
-                    __syncwarp();
-                }
-                float sc[4][2];
-                float mx = -INFINITY;
-                const float fac = sql * me.ks;
+        if (kw < me.len) {
+            uint8_t *sk = smem + s * S::STAGE, *sv = sk + S::TILE;
+            if (me.len < kw + 32) {
+                // rows behind the last visible token: whatever they hold must not reach 0 * V
+                for (int x = lane; x < (kw + 32 - me.len) * (D / 16); x += 32)
+                    reinterpret_cast<uint4 *>(sv + me.len * D)[x] = make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async();
+                __syncwarp();
+            }
+            float sc[4][2];
+            float mx = -INFINITY;
+            const float fac = sql * me.ks;
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
-                    const int row = kw + 8 * n + (kj ^ (4 * (n & 1)));
+            for (int n = 0; n < 4; ++n) {
+                float c[4] = {0.f, 0.f, 0.f, 0.f};
+                const int row = kw + 8 * n + (kj ^ (4 * (n & 1)));
 #pragma unroll
-                    for (int kp = 0; kp < D / 64; ++kp) {
-                        uint32_t b[4];
-                        ldsm_x4(b[0], b[1], b[2], b[3], sk + at<D>(row, 4 * kp + km));
-                        mma_e4m3(c, a[2 * kp], b[0], b[1]);
-                        mma_e4m3(c, a[2 * kp + 1], b[2], b[3]);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        sc[n][e] = fmaf(c[2 + e], 0.0625f, c[e]) * fac;
-                        if (kw + 8 * n + ((2 * t4 + e) ^ (4 * (n & 1))) >= me.len) sc[n][e] = -INFINITY;
-                        mx = fmaxf(mx, sc[n][e]);
-                    }
-                }
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float m_new = fmaxf(m_run, mx);
-                const float m_use = m_new == -INFINITY ? 0.f : m_new;
-                const float alpha = exp2f(m_run - m_use);
-                m_run = m_new;
-                float ps = 0.f;
-#pragma unroll
-                for (int n = 0; n < 4; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        sc[n][e] = exp2f(sc[n][e] - m_use);
-                        ps += sc[n][e];
-                        sc[n][e] *= 256.f;             // the upper end of e4m3's range
-                    }
-                l_run = fmaf(l_run, alpha, ps);
-                uint32_t pa[4];
-                split4(sc[0][0], sc[0][1], sc[1][0], sc[1][1], pa[0], pa[1]);
-                split4(sc[2][0], sc[2][1], sc[3][0], sc[3][1], pa[2], pa[3]);
-                const float vf = me.vs * (1.f / 256.f);
-#pragma unroll
-                for (int w = 0; w < D / 16; ++w) {
+                for (int kp = 0; kp < D / 64; ++kp) {
                     uint32_t b[4];
-                    ldsm_b8_t(b, sv + at<D>(vrow, w));
+                    ldsm_x4(b[0], b[1], b[2], b[3], sk + at<D>(row, 4 * kp + km));
+                    mma_e4m3(c, a[2 * kp], b[0], b[1]);
+                    mma_e4m3(c, a[2 * kp + 1], b[2], b[3]);
+                }
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float c[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma_e4m3(c, pa, b[e], b[2 + e]);
-                        float(&x)[2] = acc[2 * w + e];
-                        x[0] = fmaf(fmaf(c[2], 0.0625f, c[0]), vf, x[0] * alpha);
-                        x[1] = fmaf(fmaf(c[3], 0.0625f, c[1]), vf, x[1] * alpha);
-                    }
+                for (int e = 0; e < 2; ++e) {
+                    sc[n][e] = fmaf(c[2 + e], 0.0625f, c[e]) * fac;
+                    if (kw + 8 * n + ((2 * t4 + e) ^ (4 * (n & 1))) >= me.len) sc[n][e] = -INFINITY;
+                    mx = fmaxf(mx, sc[n][e]);
                 }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[s]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float m_new = fmaxf(m_run, mx);
+            const float m_use = m_new == -INFINITY ? 0.f : m_new;
+            const float alpha = exp2f(m_run - m_use);
+            m_run = m_new;
+            float ps = 0.f;
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    sc[n][e] = exp2f(sc[n][e] - m_use);
+                    ps += sc[n][e];
+                    sc[n][e] *= 256.f;                 // the upper end of e4m3's range
+                }
+            l_run = fmaf(l_run, alpha, ps);
+            uint32_t pa[4];
+            split4(sc[0][0], sc[0][1], sc[1][0], sc[1][1], pa[0], pa[1]);
+            split4(sc[2][0], sc[2][1], sc[3][0], sc[3][1], pa[2], pa[3]);
+            const float vf = me.vs * (1.f / 256.f);
+#pragma unroll
+            for (int w = 0; w < D / 16; ++w) {
+                uint32_t b[4];
+                ldsm_b8_t(b, sv + at<D>(vrow, w));
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float c[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma_e4m3(c, pa, b[e], b[2 + e]);
+                    float(&x)[2] = acc[2 * w + e];
+                    x[0] = fmaf(fmaf(c[2], 0.0625f, c[0]), vf, x[0] * alpha);
+                    x[1] = fmaf(fmaf(c[3], 0.0625f, c[1]), vf, x[1] * alpha);
+                }
+            }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);
+        if (!(me.flags & kLast)) continue;
+
+        // join the warps' states, in order
         l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
         l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
-    }
-
-    // join the four warps' states, in order
-    __syncthreads();                                   // the stages are read and no copy is in flight
-    float *sO = reinterpret_cast<float *>(smem), *sM = sO + kWarps * 8 * D, *sL = sM + kWarps * 8;
-    if (warp < kWarps && g < G) {
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-            *reinterpret_cast<float2 *>(sO + (warp * 8 + g) * D + n * 8 + 2 * t4) = make_float2(acc[n][0], acc[n][1]);
         if (t4 == 0) {
-            sM[warp * 8 + g] = m_run;
-            sL[warp * 8 + g] = l_run;
+            sM[warp][g] = m_run;
+            sL[warp][g] = l_run;
         }
-    }
-    __syncthreads();
-    for (int idx = tid; idx < G * D; idx += kThreads) {
-        const int h = idx / D, col = idx % D;
-        float M = -INFINITY;
+        named_bar_sync(1, 32 * kWarps);
+        float M = -INFINITY, L = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sM[w * 8 + h]);
-        float L = 0.f, x = 0.f;
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sM[w][g]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)               // an empty state is all zeros, one of NaN scores NaN
+            L += (sM[w][g] == -INFINITY ? 1.f : exp2f(sM[w][g] - M)) * sL[w][g];
+        const float f = m_run == -INFINITY ? 1.f : exp2f(m_run - M);
+        const bool whole = me.part < 0;
+        const float z = whole ? (L == 0.f ? 0.f : f / L) : f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float f = sM[w * 8 + h] == -INFINITY ? 1.f : exp2f(sM[w * 8 + h] - M);
-            L += f * sL[w * 8 + h];                    // an empty state is all zeros, one of NaN scores NaN
-            x += f * sO[(w * 8 + h) * D + col];
+            if (warp == w && g < G) {
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n) {
+                    float2 *dst = reinterpret_cast<float2 *>(sO + g * D + n * 8 + 2 * t4);
+                    float2 v = w == 0 ? make_float2(0.f, 0.f) : *dst;
+                    v.x = fmaf(acc[n][0], z, v.x);
+                    v.y = fmaf(acc[n][1], z, v.y);
+                    *dst = v;
+                }
+            }
+            named_bar_sync(1, 32 * kWarps);
         }
-        const long long row = (long long)t * p.Hq + (long long)r * G + h;
-        if (alone) {
-            o[row * D + col] = __float2bfloat16_rn(L == 0.f ? 0.f : x / L);
-            if (col == 0) lse[row] = (M + log2f(L)) * kLn2;
-        } else {
-            part_o[(row * shares + sp) * D + col] = x;
-            if (col == 0) part_ml[row * shares + sp] = make_float2(M, L);
+        const long long row = (long long)me.t * p.Hq + (long long)me.r * G;
+        if (warp == 0 && t4 == 0 && g < G) {
+            if (whole) lse[row + g] = (M + log2f(L)) * kLn2;
+            else part_ml[me.part * 8 + g] = make_float2(M, L);
         }
+        for (int idx = tid * 4; idx < G * D; idx += 32 * kWarps * 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(sO + idx);
+            if (whole) *reinterpret_cast<uint2 *>(o + row * D + idx) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+            else *reinterpret_cast<float4 *>(part_o + (long long)me.part * 8 * D + idx) = v;
+        }
+        named_bar_sync(1, 32 * kWarps);                // sO, sM and sL are free again
     }
 }
 
-// Joins the shares of a (row, head): a warp each, shares in order.
+// Joins the pieces of the row that CTA blockIdx.x of the main kernel cut off,
+// in order; a warp to a head.
 template <int D>
 __global__ void __launch_bounds__(256)
-join_kernel(PagedProblem p, const int32_t *__restrict__ row_req, const int32_t *__restrict__ row_pos, int sparse, int per,
-            int shares, const float *__restrict__ part_o, const float2 *__restrict__ part_ml, bf16 *__restrict__ o,
-            float *__restrict__ lse)
+join_kernel(PagedProblem p, const CutRow *__restrict__ cut, const float *__restrict__ part_o,
+            const float2 *__restrict__ part_ml, bf16 *__restrict__ o, float *__restrict__ lse)
 {
-    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= (long long)p.T * p.Hq) return;
-    const int t = (int)(row / p.Hq), req = row_req[t], pos = row_pos[t];
-    if (req < 0 || pos < 0 || req >= p.R || pos / kPage >= p.max_blocks) return;
-    const int c0 = pos / kPage, ns = sparse ? shares : c0 / per + 1;
-    if (ns == 1 && !sparse) return;                    // the row's only share wrote the outputs
-    const float2 *ml = part_ml + row * shares;
+    const CutRow c = cut[blockIdx.x];
+    const int h = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (c.pair < 0 || h >= p.G) return;
+    const int n = c.last - c.first + 1;
+    auto part = [&](int i) { return 2 * (c.first + i) + (i == 0 ? 1 : 0); };
     float M = -INFINITY;
-    for (int i = lane; i < ns; i += 32) M = fmaxf(M, ml[i].x);
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, part_ml[part(i) * 8 + h].x);
     M = warp_max(M);
     constexpr int PER = D / 32;
     float L = 0.f, acc[PER];
 #pragma unroll
     for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-    for (int i = 0; i < ns; ++i) {
-        const float2 x = ml[i];
-        const float f = x.x == -INFINITY ? 1.f : exp2f(x.x - M);
-        L += f * x.y;
-        const float *src = part_o + (row * shares + i) * D + lane;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const float2 ml = part_ml[part(i) * 8 + h];
+        const float f = ml.x == -INFINITY ? 1.f : exp2f(ml.x - M);
+        L += f * ml.y;
+        const float *src = part_o + ((long long)part(i) * 8 + h) * D + lane;
 #pragma unroll
         for (int e = 0; e < PER; ++e) acc[e] += f * src[32 * e];
     }
+    const long long row = (long long)(c.pair / p.Hkv) * p.Hq + (long long)(c.pair % p.Hkv) * p.G + h;
 #pragma unroll
     for (int e = 0; e < PER; ++e) o[row * D + lane + 32 * e] = __float2bfloat16_rn(L == 0.f ? 0.f : acc[e] / L);
     if (lane == 0) lse[row] = (M + log2f(L)) * kLn2;
 }
 
-// Blocks of a share: the rows' shares should fill the GPU's CTA slots (two to
-// an SM) about four times, in shares of at least two blocks, at most 128 of
-// them to a row.
-int share_blocks(const PagedProblem &p, bool sparse)
+// Two CTAs to an SM, fewer where that leaves stretches under kMinBlocks.
+int attn_ctas(const PagedProblem &p, bool sparse)
 {
-    const int blocks = sparse ? p.topk : p.max_blocks;
-    const long long rows = (long long)p.T * p.Hkv;
-    const long long want = std::max<long long>(1, std::min<long long>(128, 8LL * p.num_sms / rows));
-    return (int)std::max<long long>(std::min(2, blocks), (blocks + want - 1) / want);
-}
-int share_count(const PagedProblem &p, bool sparse)
-{
-    const int per = share_blocks(p, sparse);
-    return ((sparse ? p.topk : p.max_blocks) + per - 1) / per;
+    const long long rows = (long long)p.T * p.Hkv, most = 2LL * p.num_sms;
+    if (p.T > kPrefixRows) return (int)std::min(most, rows);
+    return (int)std::max<long long>(1, std::min(most, rows * (sparse ? p.topk : p.max_blocks) / kMinBlocks));
 }
 
 }  // namespace
 
 size_t paged_attn_scratch_floats(const PagedProblem &p)
 {
-    const size_t n = std::max(share_count(p, true), share_count(p, false));
-    return n == 1 ? 0 : (size_t)p.T * p.Hq * n * (p.d + 2);
+    if (p.T > kPrefixRows) return 0;
+    return (size_t)2 * p.num_sms * (2 * 8 * (p.d + 2) + sizeof(CutRow) / 4);
 }
 
 cudaError_t launch_paged_attn(const PagedProblem &p, const bf16 *q, const uint8_t *k8, const uint8_t *v8,
@@ -438,10 +548,11 @@ cudaError_t launch_paged_attn(const PagedProblem &p, const bf16 *q, const uint8_
                               const int32_t *row_req, const int32_t *row_pos, const int32_t *sel, bf16 *o, float *lse,
                               float *scratch, DeviceStatus *st, cudaStream_t s)
 {
-    const int per = share_blocks(p, sel != nullptr), shares = share_count(p, sel != nullptr);
-    const long long rows = (long long)p.T * p.Hq;
-    float *part_o = scratch;
-    float2 *part_ml = reinterpret_cast<float2 *>(scratch + (shares > 1 ? rows * shares * p.d : 0));
+    const int ctas = attn_ctas(p, sel != nullptr);
+    const bool cuts = p.T <= kPrefixRows && ctas > 1;
+    CutRow *cut = cuts ? reinterpret_cast<CutRow *>(scratch) : nullptr;
+    float *part_o = scratch + (size_t)2 * p.num_sms * sizeof(CutRow) / 4;
+    float2 *part_ml = reinterpret_cast<float2 *>(part_o + (size_t)2 * p.num_sms * 2 * 8 * p.d);
     CUtensorMap tk, tv;
     cudaError_t e = make_tmap_u8_3d(&tk, k8, p.d, kPage, (unsigned long long)p.n_pages * p.Hkv, p.d, 32);
     if (e == cudaSuccess) e = make_tmap_u8_3d(&tv, v8, p.d, kPage, (unsigned long long)p.n_pages * p.Hkv, p.d, 32);
@@ -452,14 +563,13 @@ cudaError_t launch_paged_attn(const PagedProblem &p, const bf16 *q, const uint8_
         if (e != cudaSuccess) return;
         {
             TimedLaunch timed_("paged_attn_kernel", s);
-            attn_kernel<D><<<(unsigned)((long long)p.T * p.Hkv * shares), kThreads, AttnSmem<D>::BYTES, s>>>(
-                p, q, tk, tv, k_scale, v_scale, block_table, row_req, row_pos, sel, o, lse, per, shares, part_o, part_ml, st);
+            attn_kernel<D><<<ctas, kThreads, AttnSmem<D>::BYTES, s>>>(p, q, tk, tv, k_scale, v_scale, block_table, row_req,
+                                                                      row_pos, sel, o, lse, part_o, part_ml, cut, st);
         }
         note_launch();
-        if (shares > 1) {
+        if (cuts) {
             TimedLaunch timed_("paged_attn_join_kernel", s);
-            join_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(p, row_req, row_pos, sel != nullptr, per, shares,
-                                                                      part_o, part_ml, o, lse);
+            join_kernel<D><<<ctas, 256, 0, s>>>(p, cut, part_o, part_ml, o, lse);
             note_launch();
         }
     };

@@ -186,8 +186,15 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedProblem p, PlanArgs a, 
             todo &= todo - 1;
             const int n = __shfl_sync(0xffffffffu, (int)q.s.gone, l), b = __shfl_sync(0xffffffffu, (int)at.gone, l);
             const int32_t *row = a.block_table + (long long)(base + (warp << 5) + l) * p.max_blocks;
-            for (int j = lane; j < n; j += 32)
-                a.free_pages[((long long)head + count + b + j) % p.n_pages] = row[j];
+            constexpr int U = 16;                                // loads in flight before the stores they may not pass
+            for (int j0 = lane; j0 < n; j0 += 32 * U) {
+                int32_t page[U];
+#pragma unroll
+                for (int i = 0; i < U; ++i) page[i] = j0 + 32 * i < n ? row[j0 + 32 * i] : 0;
+#pragma unroll
+                for (int i = 0; i < U; ++i)
+                    if (j0 + 32 * i < n) a.free_pages[((long long)head + count + b + j0 + 32 * i) % p.n_pages] = page[i];
+            }
         }
     }
     if (tid == 0) {

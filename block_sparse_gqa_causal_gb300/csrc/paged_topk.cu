@@ -4,11 +4,14 @@
 //
 // Candidates are ranked by 64-bit keys (score, then lower block), all
 // distinct, so the order is total and the result does not depend on how the
-// work is split.  A warp keeps its 32 best, one to a lane, in descending order.
-// A tile of 32 candidates is sorted and merged in only when one of them beats
-// the (topk-1)-th best so far, which for scores in random order stops
-// happening soon.  Rows of many blocks are cut over the CTA's warps, whose
-// lists the first warp merges.
+// work is split.  A warp takes 1,024 blocks at a time, 32 to a lane, in
+// registers.  The (topk-1)-th largest of the 32 lanes' maxima is a lower bound
+// of the (topk-1)-th best score, and only about twenty of 1,024 scores in
+// random order reach it: these alone are listed, sorted across the lanes and
+// merged into the warp's 32 best.  (Scores that tie make the list longer, not
+// wrong.)  Every score is read once; what is left is a few hundred
+// instructions a row.  Rows of more than 1,024 blocks are cut over a CTA's
+// warps, whose lists the first warp merges.
 #include <algorithm>
 
 #include "paged.h"
@@ -16,7 +19,8 @@
 namespace msa {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kPer = 32;                 // scores of a lane
+constexpr int kTile = 32 * kPer;         // blocks a warp takes at a time
 
 __device__ __forceinline__ unsigned long long merged(unsigned long long best, unsigned long long more, int lane)
 {
@@ -24,15 +28,32 @@ __device__ __forceinline__ unsigned long long merged(unsigned long long best, un
     return merge_desc64(best > o ? best : o, lane);
 }
 
-// W: warps of a row (1: a CTA takes eight rows, 8: one)
-template <int W>
-__global__ void __launch_bounds__(32 * kWarps)
+// descending bitonic sort of one 32-bit value per lane
+__device__ __forceinline__ uint32_t sort_desc32(uint32_t v, int lane)
+{
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1) {
+#pragma unroll
+        for (int stride = size >> 1; stride > 0; stride >>= 1) {
+            const uint32_t o = __shfl_xor_sync(0xffffffffu, v, stride);
+            const bool desc = (lane & size) == 0 || size == 32;
+            v = ((lane & stride) == 0) == desc ? max(v, o) : min(v, o);
+        }
+    }
+    return v;
+}
+
+// W: warps of a row; R: rows of a CTA
+template <int W, int R>
+__global__ void __launch_bounds__(32 * W * R)
 topk_kernel(PagedProblem p, const float *__restrict__ scores, const int32_t *__restrict__ row_pos,
             int32_t *__restrict__ sel, DeviceStatus *st)
 {
-    __shared__ unsigned long long lists[kWarps][32];
+    static_assert(W == 1 || R == 1, "a row's warps fill the CTA");
+    __shared__ int list[W * R][kTile];                        // the blocks of a tile that reach the bound, ascending
+    __shared__ unsigned long long lists[W][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long row = W == 1 ? (long long)blockIdx.x * kWarps + warp : blockIdx.x;
+    const long long row = W == 1 ? (long long)blockIdx.x * R + warp : blockIdx.x;
     if (row >= (long long)p.T * p.Hkv) return;
     const int pos = row_pos[row / p.Hkv];
     if (pos < 0) return;                                      // a row behind the last request
@@ -42,25 +63,53 @@ topk_kernel(PagedProblem p, const float *__restrict__ scores, const int32_t *__r
         return;
     }
     const float *sc = scores + row * p.max_blocks;
-    unsigned long long best = 0;                              // 0: none
+    unsigned long long best = 0;                              // this lane's of the warp's 32 best; 0: none
     if (c0 >= k && k > 1) {
-        const int w = W == 1 ? 0 : warp;
-        unsigned long long bar = 0;
-        for (int base = w * 32; base < c0; base += 32 * W) {
-            const int c = base + lane;
-            float s = c < c0 ? sc[c] : 0.f;
-            if (s != s) s = -INFINITY;                        // a NaN ranks last
-            const unsigned long long key = c < c0 ? block_key(s, c) : 0ull;
-            if (__ballot_sync(0xffffffffu, key > bar) == 0) continue;
-            best = merged(best, sort_desc64(key, lane), lane);
-            bar = shfl64(best, k - 2);
+        int *mine = list[warp];
+        for (int base = (W == 1 ? 0 : warp) * kTile; base < c0; base += W * kTile) {
+            uint32_t v[kPer], top = 0;                        // 0 below every score's key
+            const int n = min(kTile, c0 - base);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                v[i] = 0;
+                if (i * 32 < n && i * 32 + lane < n) {
+                    const float s = sc[base + i * 32 + lane];
+                    v[i] = float_key(s != s ? -INFINITY : s);  // a NaN ranks last
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) top = max(top, v[i]);
+            const uint32_t bound = max(__shfl_sync(0xffffffffu, sort_desc32(top, lane), k - 2),
+                                       (uint32_t)(shfl64(best, k - 2) >> 32));
+            int m = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                if (i * 32 >= n) break;
+                const bool in = v[i] >= bound && v[i] != 0;
+                const uint32_t b = __ballot_sync(0xffffffffu, in);
+                if (in) mine[m + __popc(b & ((1u << lane) - 1))] = base + i * 32 + lane;
+                m += __popc(b);
+            }
+            __syncwarp();
+            for (int i = 0; i < m; i += 32) {
+                unsigned long long key = 0;
+                if (i + lane < m) {
+                    const int c = mine[i + lane];
+                    const float s = sc[c];
+                    key = block_key(s != s ? -INFINITY : s, c);
+                }
+                if (__ballot_sync(0xffffffffu, key > shfl64(best, k - 2)) == 0) continue;
+                key = sort_desc64(key, lane);
+                best = base == 0 && i == 0 ? key : merged(best, key, lane);
+            }
+            __syncwarp();
         }
         if (W > 1) {
             lists[warp][lane] = best;
             __syncthreads();
             if (warp != 0) return;
-            for (int w2 = 1; w2 < W; ++w2) {
-                const unsigned long long more = lists[w2][lane];
+            for (int w = 1; w < W; ++w) {
+                const unsigned long long more = lists[w][lane];
                 if (__ballot_sync(0xffffffffu, more > shfl64(best, k - 2)) == 0) continue;
                 best = merged(best, more, lane);
             }
@@ -69,16 +118,16 @@ topk_kernel(PagedProblem p, const float *__restrict__ scores, const int32_t *__r
         return;
     }
     // ascending blocks, then -1: sorted as 2^32 - 1 - block, none as 0
-    uint32_t c = 0xFFFFFFFFu;
+    uint32_t c = 0;
     if (c0 < k) {
-        if (lane <= c0) c = (uint32_t)lane;
+        if (lane <= c0) c = 0xFFFFFFFFu - (uint32_t)lane;
     } else if (lane < k - 1) {
-        c = 0xFFFFFFFFu - (uint32_t)best;
+        c = (uint32_t)best;                                   // a key's low half
     } else if (lane == k - 1) {
-        c = (uint32_t)c0;
+        c = 0xFFFFFFFFu - (uint32_t)c0;
     }
-    const unsigned long long asc = sort_desc64(c == 0xFFFFFFFFu ? 0ull : 0xFFFFFFFFull - c, lane);
-    if (lane < k) sel[row * k + lane] = asc ? (int32_t)(0xFFFFFFFFu - (uint32_t)asc) : -1;
+    c = sort_desc32(c, lane);
+    if (lane < k) sel[row * k + lane] = c ? (int32_t)(0xFFFFFFFFu - c) : -1;
 }
 
 }  // namespace
@@ -86,12 +135,12 @@ topk_kernel(PagedProblem p, const float *__restrict__ scores, const int32_t *__r
 cudaError_t launch_paged_block_topk(const PagedProblem &p, const float *scores, const int32_t *row_pos, int32_t *sel,
                                     DeviceStatus *st, cudaStream_t s)
 {
+    constexpr int W = 8, R = 4;
     const long long rows = (long long)p.T * p.Hkv;
-    const bool wide = p.max_blocks > 64 && rows < 8LL * p.num_sms * kWarps;
     {
         TimedLaunch timed_("paged_block_topk_kernel", s);
-        if (wide) topk_kernel<kWarps><<<(unsigned)rows, 32 * kWarps, 0, s>>>(p, scores, row_pos, sel, st);
-        else topk_kernel<1><<<(unsigned)((rows + kWarps - 1) / kWarps), 32 * kWarps, 0, s>>>(p, scores, row_pos, sel, st);
+        if (p.max_blocks > kTile) topk_kernel<W, 1><<<(unsigned)rows, 32 * W, 0, s>>>(p, scores, row_pos, sel, st);
+        else topk_kernel<1, R><<<(unsigned)((rows + R - 1) / R), 32 * R, 0, s>>>(p, scores, row_pos, sel, st);
     }
     note_launch();
     return cudaGetLastError();
