@@ -38,15 +38,9 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t two)
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(h) : "h"((uint16_t)two));
     return __half22float2(*reinterpret_cast<__half2 *>(&h));
 }
-// infinities become NaN: e4m3 has none, and 448 s would pass for a value
-__device__ __forceinline__ uint32_t nan_for_inf(uint32_t w)
-{
-    const uint32_t a = w & 0x7FFF7FFFu;
-    return w | (__vcmpgeu2(a, 0x7F807F80u) & 0x7FFF7FFFu);
-}
 
 template <int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
 append_kernel(PagedProblem p, const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new,
               const uint4 *__restrict__ ki_new, const int32_t *__restrict__ slots, const int32_t *__restrict__ segs,
               uint8_t *__restrict__ k8, uint8_t *__restrict__ v8, float *__restrict__ k_scale,
@@ -95,20 +89,32 @@ append_kernel(PagedProblem p, const uint4 *__restrict__ k_new, const uint4 *__re
         x[i] = make_uint4(0u, 0u, 0u, 0u);
         if (row < cnt) x[i] = __ldg(src + ((long long)(t0 + row) * p.Hkv + h) * LPR + col);
     }
+    auto largest = [&](uint32_t v) {
+        v = __reduce_max_sync(0xffffffffu, max(v & 0xFFFFu, v >> 16));
+        if ((tid & 31) == 0) part[half][(tid >> 5) & 3] = v;
+        named_bar_sync(1 + half, kThreads / 2);
+        return max(max(part[half][0], part[half][1]), max(part[half][2], part[half][3]));
+    };
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        uint32_t *w = &x[i].x;
+    for (int i = 0; i < N; ++i)
+        top = __vmaxu2(__vmaxu2(top, __vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu)),
+                       __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu));
+    top = largest(top);
+    if (top >= 0x7F80u) {                     // rare: NaN for infinities, and the largest finite value
+        top = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t a = w[e] & 0x7FFF7FFFu;
-            top = __vmaxu2(top, a & ~__vcmpgeu2(a, 0x7F807F80u));   // finite values only
+        for (int i = 0; i < N; ++i) {
+            uint32_t *w = &x[i].x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t a = w[e] & 0x7FFF7FFFu, bad = __vcmpgeu2(a, 0x7F807F80u);
+                top = __vmaxu2(top, a & ~bad);
+                w[e] |= bad & 0x7FFF7FFFu;    // e4m3 has no infinity, and 448 s would pass for a value
+            }
         }
+        named_bar_sync(1 + half, kThreads / 2);   // the first maxima have been read
+        top = largest(top);
     }
-    top = max(top & 0xFFFFu, top >> 16);
-    top = __reduce_max_sync(0xffffffffu, top);
-    if ((tid & 31) == 0) part[half][(tid >> 5) & 3] = top;
-    named_bar_sync(1 + half, kThreads / 2);
-    top = max(max(part[half][0], part[half][1]), max(part[half][2], part[half][3]));
     const float s = fmaxf(had, __uint_as_float(pow2_scale_bits(top)));
     const float inv = 1.f / s;
     if (off > 0 && s > had) {                 // the page's older codes, to the larger scale
@@ -133,7 +139,7 @@ append_kernel(PagedProblem p, const uint4 *__restrict__ k_new, const uint4 *__re
         uint32_t c[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float2 f = unpack_bf16(nan_for_inf(w[e]));
+            const float2 f = unpack_bf16(w[e]);
             c[e] = e4m3x2(f.x * inv, f.y * inv);
         }
         *reinterpret_cast<uint2 *>(codes + (off + row) * D + col * 8) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));

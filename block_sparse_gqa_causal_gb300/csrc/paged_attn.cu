@@ -16,6 +16,17 @@
 // two to fill the range), and the probabilities with the precision that bf16
 // gives them.  Sums, maxima and the outputs are fp32.
 //
+// With t_j = l_j log2 e + log2 vs, the weight of token j's codes is 2^t_j and
+// that of the sum 2^t_j / vs, so one reference m bounds both and the products
+// P V add up in the MMA's own accumulators across pages of different scales.
+// m is the largest t so far, or up to 4 less: P = 16 * 2^(t - m) stays within
+// 256 and the accumulators are only rescaled when t has outgrown m by more
+// than that, which after a row's first pages is rare.  (Rescaling on every
+// new maximum and joining each page's product in fp32 cost 830 instructions a
+// warp and page instead of 300, and made them the bound: 55 us against 45 at
+// 64 rows x 8 groups x 16 pages.)  P's small terms are off by at most 2^-18
+// of the largest weight.
+//
 // Each of four warps takes 32 of a page's 128 tokens and keeps its own running
 // maximum, sum and output; they are joined where a row ends.  V's operand
 // needs its tokens along a register: ldmatrix with 8-bit transposition gives
@@ -52,7 +63,8 @@ constexpr int kMinBlocks = 2;                   // a stretch has at least this m
 enum { kFirst = 1, kLast = 2, kEnd = 4 };       // of a piece; of the CTA's stretch
 struct Meta {
     int len;        // visible tokens of the block
-    float ks, vs;   // the page's scales for this head
+    float ks;       // the page's K scale for this head
+    float lv, pv;   // log2 of its V scale (-100 at least), and 16 x what that leaves of the scale (1)
     int flags;
     int t, r;       // the piece's row and group
     int part;       // the piece's place among the partial states; -1: a whole row
@@ -145,6 +157,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
     __shared__ long long before[kPrefixRows + 1];   // blocks of the rows before each row, one group
     __shared__ int abort_flag;
 
+    asm volatile("griddepcontrol.launch_dependents;\n");   // the join may be set up meanwhile; it waits for this kernel's end
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = p.G;
     const bool even = p.T <= kPrefixRows;
 
@@ -238,7 +251,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                     c = base + lane;
                 }
                 int page = -1, len = 0;
-                float ks = 0.f, vs = 0.f;
+                float ks = 0.f, lv = 0.f, pv = 0.f;
                 if (c >= 0) {
                     page = block_table[(long long)req * p.max_blocks + c];
                     if ((unsigned)page >= (unsigned)p.n_pages) {
@@ -246,7 +259,9 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                     } else {
                         len = min(kPage, pos - c * kPage + 1);
                         ks = k_scale[(long long)page * p.Hkv + r];
-                        vs = v_scale[(long long)page * p.Hkv + r];
+                        const float vs = v_scale[(long long)page * p.Hkv + r];
+                        lv = fmaxf(log2f(vs), -100.f);
+                        pv = 16.f * (vs * exp2f(-lv));
                     }
                 }
                 // a block without a page is an empty step, and so is a piece without any block
@@ -259,7 +274,8 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                     Meta m;
                     m.len = __shfl_sync(0xffffffffu, len, l);
                     m.ks = __shfl_sync(0xffffffffu, ks, l);
-                    m.vs = __shfl_sync(0xffffffffu, vs, l);
+                    m.lv = __shfl_sync(0xffffffffu, lv, l);
+                    m.pv = __shfl_sync(0xffffffffu, pv, l);
                     m.flags = (first ? kFirst : 0) | (!todo && (sel || base + 32 >= j1) ? kLast : 0);
                     m.t = t;
                     m.r = r;
@@ -329,8 +345,8 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
     }
 
     const int g = lane >> 2, t4 = lane & 3;
-    float acc[D / 8][2];                               // head g, features 8n + 2 t4, + 1
-    float m_run = -INFINITY, l_run = 0.f, sql = 0.f;
+    float acc[D / 8][4];                               // head g, features 8n + 2 t4, + 1: the hi rows' sums, then the lo rows'
+    float m_run = -INFINITY, l_run = 0.f, sql = 0.f;   // reference of head g; this lane's share of its sum
     uint32_t a[D / 32][4];                             // the queries' terms, features 32 ks + 4 t4 .. + 3 and + 16 ..
     float *sO = reinterpret_cast<float *>(smem + S::OFF_O);
     const int kw = warp * 32;                          // this warp's first token of a page
@@ -340,7 +356,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
     const int vk = lane & 15, vn = (vk >> 1) & 1;
     const int vrow = kw + 16 * (lane >> 4) + 8 * vn + ((2 * (vk >> 2) + (vk & 1)) ^ (4 * vn));
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n) acc[n][0] = acc[n][1] = 0.f;
+    for (int n = 0; n < D / 8; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
 #pragma unroll
     for (int ks = 0; ks < D / 32; ++ks) a[ks][0] = a[ks][1] = a[ks][2] = a[ks][3] = 0u;
 
@@ -376,7 +392,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                 }
             sql = sq * (p.scale * kLog2e);
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n) acc[n][0] = acc[n][1] = 0.f;
+            for (int n = 0; n < D / 8; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
             m_run = -INFINITY;
             l_run = 0.f;
         }
@@ -390,7 +406,6 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                 __syncwarp();
             }
             float sc[4][2];
-            float mx = -INFINITY;
             const float fac = sql * me.ks;
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
@@ -404,18 +419,33 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                     mma_e4m3(c, a[2 * kp + 1], b[2], b[3]);
                 }
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    sc[n][e] = fmaf(c[2 + e], 0.0625f, c[e]) * fac;
-                    if (kw + 8 * n + ((2 * t4 + e) ^ (4 * (n & 1))) >= me.len) sc[n][e] = -INFINITY;
-                    mx = fmaxf(mx, sc[n][e]);
+                for (int e = 0; e < 2; ++e) sc[n][e] = fmaf(fmaf(c[2 + e], 0.0625f, c[e]), fac, me.lv);
+            }
+            if (me.len < kw + 32) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (kw + 8 * n + ((2 * t4 + e) ^ (4 * (n & 1))) >= me.len) sc[n][e] = -INFINITY;
+            }
+            float mx = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1])),
+                             fmaxf(fmaxf(sc[2][0], sc[2][1]), fmaxf(sc[3][0], sc[3][1])));
+            if (__any_sync(0xffffffffu, mx > m_run + 4.f)) {
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const float m_new = fmaxf(m_run, mx);
+                const float alpha = m_new == m_run ? 1.f : exp2f(m_run - m_new);
+                m_run = m_new;
+                l_run *= alpha;
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n) {
+                    acc[n][0] *= alpha;
+                    acc[n][1] *= alpha;
+                    acc[n][2] *= alpha;
+                    acc[n][3] *= alpha;
                 }
             }
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float m_new = fmaxf(m_run, mx);
-            const float m_use = m_new == -INFINITY ? 0.f : m_new;
-            const float alpha = exp2f(m_run - m_use);
-            m_run = m_new;
+            const float m_use = m_run == -INFINITY ? 0.f : m_run;   // no score yet but -inf (or NaN)
             float ps = 0.f;
 #pragma unroll
             for (int n = 0; n < 4; ++n)
@@ -423,25 +453,18 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                 for (int e = 0; e < 2; ++e) {
                     sc[n][e] = exp2f(sc[n][e] - m_use);
                     ps += sc[n][e];
-                    sc[n][e] *= 256.f;                 // the upper end of e4m3's range
+                    sc[n][e] *= me.pv;
                 }
-            l_run = fmaf(l_run, alpha, ps);
+            l_run = fmaf(ps, exp2f(-me.lv), l_run);
             uint32_t pa[4];
             split4(sc[0][0], sc[0][1], sc[1][0], sc[1][1], pa[0], pa[1]);
             split4(sc[2][0], sc[2][1], sc[3][0], sc[3][1], pa[2], pa[3]);
-            const float vf = me.vs * (1.f / 256.f);
 #pragma unroll
             for (int w = 0; w < D / 16; ++w) {
                 uint32_t b[4];
                 ldsm_b8_t(b, sv + at<D>(vrow, w));
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma_e4m3(c, pa, b[e], b[2 + e]);
-                    float(&x)[2] = acc[2 * w + e];
-                    x[0] = fmaf(fmaf(c[2], 0.0625f, c[0]), vf, x[0] * alpha);
-                    x[1] = fmaf(fmaf(c[3], 0.0625f, c[1]), vf, x[1] * alpha);
-                }
+                mma_e4m3(acc[2 * w], pa, b[0], b[2]);
+                mma_e4m3(acc[2 * w + 1], pa, b[1], b[3]);
             }
         }
         __syncwarp();
@@ -464,7 +487,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
             L += (sM[w][g] == -INFINITY ? 1.f : exp2f(sM[w][g] - M)) * sL[w][g];
         const float f = m_run == -INFINITY ? 1.f : exp2f(m_run - M);
         const bool whole = me.part < 0;
-        const float z = whole ? (L == 0.f ? 0.f : f / L) : f;
+        const float z = (whole ? (L == 0.f ? 0.f : f / L) : f) * 0.0625f;   // P carries 16
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             if (warp == w && g < G) {
@@ -472,8 +495,8 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                 for (int n = 0; n < D / 8; ++n) {
                     float2 *dst = reinterpret_cast<float2 *>(sO + g * D + n * 8 + 2 * t4);
                     float2 v = w == 0 ? make_float2(0.f, 0.f) : *dst;
-                    v.x = fmaf(acc[n][0], z, v.x);
-                    v.y = fmaf(acc[n][1], z, v.y);
+                    v.x = fmaf(fmaf(acc[n][2], 0.0625f, acc[n][0]), z, v.x);
+                    v.y = fmaf(fmaf(acc[n][3], 0.0625f, acc[n][1]), z, v.y);
                     *dst = v;
                 }
             }
@@ -500,6 +523,7 @@ __global__ void __launch_bounds__(256)
 join_kernel(PagedProblem p, const CutRow *__restrict__ cut, const float *__restrict__ part_o,
             const float2 *__restrict__ part_ml, bf16 *__restrict__ o, float *__restrict__ lse)
 {
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");   // launched before the main kernel's end
     const CutRow c = cut[blockIdx.x];
     const int h = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (c.pair < 0 || h >= p.G) return;
@@ -569,7 +593,16 @@ cudaError_t launch_paged_attn(const PagedProblem &p, const bf16 *q, const uint8_
         note_launch();
         if (cuts) {
             TimedLaunch timed_("paged_attn_join_kernel", s);
-            join_kernel<D><<<ctas, 256, 0, s>>>(p, cut, part_o, part_ml, o, lse);
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(ctas);
+            cfg.blockDim = dim3(256);
+            cfg.stream = s;
+            cudaLaunchAttribute attr{};
+            attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr.val.programmaticStreamSerializationAllowed = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            e = cudaLaunchKernelEx(&cfg, join_kernel<D>, p, (const CutRow *)cut, (const float *)part_o, (const float2 *)part_ml, o, lse);
             note_launch();
         }
     };

@@ -133,7 +133,9 @@ def attn(q, k8, v8, ks, vs, table, req, pos, sel, scale):
               the row's largest scaled feature (448, at most twice its share):
               ds <= d 2^-23 sum|q k| scale + 2^-22 max|q| sum|k| scale
       exp     p relative 2 max ds + 2^-21 (exp2's error, the running maximum's factors)
-      split   p relative 2^-8, absolute 2^-22 (of p's largest, 1)
+      split   p relative 2^-8, or 2^-18 of the largest weight p vs (x = 16 p vs / reference is the sum of two e4m3
+              terms, hi + lo / 16, off by 2^-8 x or half the least subnormal, 2^-10 / 16; the reference is at
+              most the largest weight), on codes V / vs
       sums    n 2^-24 relative
       o       rounded once to bf16, 2^-8 relative."""
     T, Hq, d = q.shape
@@ -152,6 +154,7 @@ def attn(q, k8, v8, ks, vs, table, req, pos, sel, scale):
             seen = ((blocks[:, None] * PAGE + np.arange(PAGE)) <= pos[t]).reshape(-1)
             K = (e4m3_decode(k8[pages, h]) * ks[pages, h].astype(np.float64)[:, None, None]).reshape(-1, d)[seen]
             V = (e4m3_decode(v8[pages, h]) * vs[pages, h].astype(np.float64)[:, None, None]).reshape(-1, d)[seen]
+            sv = np.repeat(vs[pages, h].astype(np.float64), PAGE)[seen]
             n = len(K)
             for x in range(h * G, (h + 1) * G):
                 s = K @ q[t, x] * scale
@@ -162,6 +165,6 @@ def attn(q, k8, v8, ks, vs, table, req, pos, sel, scale):
                 z = e.sum()
                 o[t, x], lse[t, x] = (e / z) @ V, m + np.log(z)
                 rel = 2 * ds + 2.0 ** -8 + 2.0 ** -20 + 2 * n * 2.0 ** -24
-                do[t, x] = rel * ((e / z) @ np.abs(V)) + 2.0 ** -22 * np.abs(V).sum(0) / z + 2.0 ** -8 * np.abs(o[t, x]) + 1e-30
+                do[t, x] = rel * ((e / z) @ np.abs(V)) + 2.0 ** -18 * np.nanmax(e * sv) * np.abs(V / sv[:, None]).sum(0) / z + 2.0 ** -8 * np.abs(o[t, x]) + 1e-30
                 dl[t, x] = ds + n * 2.0 ** -24 + 2.0 ** -21 * (1 + np.abs(lse[t, x]) + abs(m))
     return o, lse, do, dl
