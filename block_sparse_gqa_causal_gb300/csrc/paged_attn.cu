@@ -76,8 +76,9 @@ struct AttnSmem {
     static constexpr int STAGE = 2 * TILE;
     static constexpr int Q = 8 * D * 2;         // the group's queries, with a piece's first block
     static constexpr int OFF_Q = kStages * STAGE;
-    static constexpr int OFF_O = OFF_Q + kStages * Q;
-    static constexpr int BYTES = OFF_O + 8 * D * 4 + 1024;   // + alignment
+    static constexpr int BYTES = OFF_Q + kStages * Q + 1024;   // + alignment
+    static constexpr int OROW = D + 8;          // a warp's output row: 8 more keeps the rows on different banks
+    static_assert(kWarps * 8 * OROW * 4 <= STAGE, "the warps' outputs fit a stage");
 };
 
 // byte offset of 16-byte word w of token row r in a TMA-swizzled tile
@@ -132,6 +133,10 @@ struct CutRow {
     int pair, first, last, pad;
 };
 
+MSA_DEV void mbar_expect_tx(uint64_t *bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
 MSA_DEV void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
 {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(smem_u32(dst)),
@@ -206,24 +211,31 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
     if (warp == kWarps) {
         int step = 0;
         bool live = true;
-        auto publish = [&](const Meta &m, int page) {
+        // Waits for the next stage and starts its copies.  The arrival that completes the phase comes with the
+        // block's Meta, so that the copies do not wait for the scales.
+        auto start = [&](int page, int t, int r, int len, bool first) {
             const int s = step % kStages;
             if (step >= kStages && !mbar_wait_warp(&empty[s], (step / kStages - 1) & 1, st, 144, &abort_flag)) {
                 live = false;
                 return;
             }
             if (lane == 0) {
-                meta[s] = m;
-                const int boxes = (m.len + 31) / 32;           // 32-token boxes, none past the row
-                const uint32_t qb = m.flags & kFirst ? G * D * 2 : 0, bytes = boxes * 64 * D + qb;
-                if (bytes) mbar_arrive_expect_tx(&full[s], bytes);
-                else mbar_arrive(&full[s]);
-                if (qb) bulk_load(smem + S::OFF_Q + s * S::Q, q + ((long long)m.t * p.Hq + (long long)m.r * G) * D, qb, &full[s]);
+                const int boxes = (len + 31) / 32;             // 32-token boxes, none past the row
+                const uint32_t qb = first ? G * D * 2 : 0;
+                mbar_expect_tx(&full[s], boxes * 64 * D + qb);
+                if (first) bulk_load(smem + S::OFF_Q + s * S::Q, q + ((long long)t * p.Hq + (long long)r * G) * D, qb, &full[s]);
                 uint8_t *dst = smem + s * S::STAGE;
                 for (int x = 0; x < boxes; ++x)
-                    tma_load_3d(dst + x * 32 * D, &tm_k, &full[s], 0, x * 32, page * p.Hkv + m.r);
+                    tma_load_3d(dst + x * 32 * D, &tm_k, &full[s], 0, x * 32, page * p.Hkv + r);
                 for (int x = 0; x < boxes; ++x)
-                    tma_load_3d(dst + S::TILE + x * 32 * D, &tm_v, &full[s], 0, x * 32, page * p.Hkv + m.r);
+                    tma_load_3d(dst + S::TILE + x * 32 * D, &tm_v, &full[s], 0, x * 32, page * p.Hkv + r);
+            }
+        };
+        auto publish = [&](const Meta &m) {
+            const int s = step % kStages;
+            if (lane == 0) {
+                meta[s] = m;
+                mbar_arrive(&full[s]);
             }
             ++step;
         };
@@ -251,7 +263,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                     c = base + lane;
                 }
                 int page = -1, len = 0;
-                float ks = 0.f, lv = 0.f, pv = 0.f;
+                float ks = 0.f, vscale = 0.f;
                 if (c >= 0) {
                     page = block_table[(long long)req * p.max_blocks + c];
                     if ((unsigned)page >= (unsigned)p.n_pages) {
@@ -259,9 +271,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                     } else {
                         len = min(kPage, pos - c * kPage + 1);
                         ks = k_scale[(long long)page * p.Hkv + r];
-                        const float vs = v_scale[(long long)page * p.Hkv + r];
-                        lv = fmaxf(log2f(vs), -100.f);
-                        pv = 16.f * (vs * exp2f(-lv));
+                        vscale = v_scale[(long long)page * p.Hkv + r];
                     }
                 }
                 // a block without a page is an empty step, and so is a piece without any block
@@ -271,17 +281,21 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                 while (todo && live) {
                     const int l = __ffs(todo) - 1;
                     todo &= todo - 1;
+                    const int blen = __shfl_sync(0xffffffffu, len, l);
+                    start(__shfl_sync(0xffffffffu, page, l), t, r, blen, first);
+                    if (!live) break;
                     Meta m;
-                    m.len = __shfl_sync(0xffffffffu, len, l);
+                    m.len = blen;
                     m.ks = __shfl_sync(0xffffffffu, ks, l);
-                    m.lv = __shfl_sync(0xffffffffu, lv, l);
-                    m.pv = __shfl_sync(0xffffffffu, pv, l);
+                    const float vs = __shfl_sync(0xffffffffu, vscale, l);
+                    m.lv = fmaxf(log2f(vs), -100.f);
+                    m.pv = 16.f * (vs * exp2f(-m.lv));
                     m.flags = (first ? kFirst : 0) | (!todo && (sel || base + 32 >= j1) ? kLast : 0);
                     m.t = t;
                     m.r = r;
                     m.part = part;
                     first = false;
-                    publish(m, __shfl_sync(0xffffffffu, page, l));
+                    publish(m);
                 }
                 if (sel) break;                        // at most 32 slots: one round
             }
@@ -348,7 +362,6 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
     float acc[D / 8][4];                               // head g, features 8n + 2 t4, + 1: the hi rows' sums, then the lo rows'
     float m_run = -INFINITY, l_run = 0.f, sql = 0.f;   // reference of head g; this lane's share of its sum
     uint32_t a[D / 32][4];                             // the queries' terms, features 32 ks + 4 t4 .. + 3 and + 16 ..
-    float *sO = reinterpret_cast<float *>(smem + S::OFF_O);
     const int kw = warp * 32;                          // this warp's first token of a page
     // K rows: token column j of score tile n is token 8n + (j ^ 4 (n & 1))
     const int kj = lane & 7, km = lane >> 3;
@@ -467,11 +480,13 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                 mma_e4m3(acc[2 * w + 1], pa, b[1], b[3]);
             }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[s]);
-        if (!(me.flags & kLast)) continue;
+        if (!(me.flags & kLast)) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[s]);
+            continue;
+        }
 
-        // join the warps' states, in order
+        // join the warps' states, in order; once all four have read it, the last block's stage takes the outputs
         l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
         l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
         if (t4 == 0) {
@@ -488,31 +503,33 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
         const float f = m_run == -INFINITY ? 1.f : exp2f(m_run - M);
         const bool whole = me.part < 0;
         const float z = (whole ? (L == 0.f ? 0.f : f / L) : f) * 0.0625f;   // P carries 16
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (warp == w && g < G) {
-#pragma unroll
-                for (int n = 0; n < D / 8; ++n) {
-                    float2 *dst = reinterpret_cast<float2 *>(sO + g * D + n * 8 + 2 * t4);
-                    float2 v = w == 0 ? make_float2(0.f, 0.f) : *dst;
-                    v.x = fmaf(fmaf(acc[n][2], 0.0625f, acc[n][0]), z, v.x);
-                    v.y = fmaf(fmaf(acc[n][3], 0.0625f, acc[n][1]), z, v.y);
-                    *dst = v;
-                }
-            }
-            named_bar_sync(1, 32 * kWarps);
-        }
+        float *sO = reinterpret_cast<float *>(smem + s * S::STAGE);
         const long long row = (long long)me.t * p.Hq + (long long)me.r * G;
-        if (warp == 0 && t4 == 0 && g < G) {
-            if (whole) lse[row + g] = (M + log2f(L)) * kLn2;
-            else part_ml[me.part * 8 + g] = make_float2(M, L);
+        if (g < G) {
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n)
+                *reinterpret_cast<float2 *>(sO + (warp * 8 + g) * S::OROW + n * 8 + 2 * t4) =
+                    make_float2(fmaf(acc[n][2], 0.0625f, acc[n][0]) * z, fmaf(acc[n][3], 0.0625f, acc[n][1]) * z);
+            if (warp == 0 && t4 == 0) {
+                if (whole) lse[row + g] = (M + log2f(L)) * kLn2;
+                else part_ml[me.part * 8 + g] = make_float2(M, L);
+            }
         }
+        named_bar_sync(1, 32 * kWarps);
         for (int idx = tid * 4; idx < G * D; idx += 32 * kWarps * 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(sO + idx);
+            const float *src = sO + idx / D * S::OROW + idx % D;
+            float4 v = *reinterpret_cast<const float4 *>(src);
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) {
+                const float4 u = *reinterpret_cast<const float4 *>(src + w * 8 * S::OROW);
+                v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+            }
             if (whole) *reinterpret_cast<uint2 *>(o + row * D + idx) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
             else *reinterpret_cast<float4 *>(part_o + (long long)me.part * 8 * D + idx) = v;
         }
-        named_bar_sync(1, 32 * kWarps);                // sO, sM and sL are free again
+        fence_proxy_async();                           // the stage goes back to the copies
+        named_bar_sync(1, 32 * kWarps);                // sM and sL are free again, too
+        if (lane == 0) mbar_arrive(&empty[s]);
     }
 }
 
@@ -529,21 +546,36 @@ join_kernel(PagedProblem p, const CutRow *__restrict__ cut, const float *__restr
     if (c.pair < 0 || h >= p.G) return;
     const int n = c.last - c.first + 1;
     auto part = [&](int i) { return 2 * (c.first + i) + (i == 0 ? 1 : 0); };
-    float M = -INFINITY;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, part_ml[part(i) * 8 + h].x);
-    M = warp_max(M);
-    constexpr int PER = D / 32;
-    float L = 0.f, acc[PER];
+    constexpr int PER = D / 32, U = 4;                 // pieces whose loads are in flight together
+    float M = -INFINITY, L = 0.f, acc[PER];
 #pragma unroll
     for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-        const float2 ml = part_ml[part(i) * 8 + h];
-        const float f = ml.x == -INFINITY ? 1.f : exp2f(ml.x - M);
-        L += f * ml.y;
-        const float *src = part_o + ((long long)part(i) * 8 + h) * D + lane;
+    for (int i0 = 0; i0 < n; i0 += U) {
+        float2 ml[U];
+        float x[U][PER];
 #pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] += f * src[32 * e];
+        for (int u = 0; u < U; ++u) {
+            const int i = min(i0 + u, n - 1);
+            ml[u] = part_ml[part(i) * 8 + h];
+#pragma unroll
+            for (int e = 0; e < PER; ++e) x[u][e] = part_o[((long long)part(i) * 8 + h) * D + lane + 32 * e];
+        }
+        float m = M;
+#pragma unroll
+        for (int u = 0; u < U; ++u) m = fmaxf(m, ml[u].x);
+        const float keep = M == -INFINITY ? 1.f : exp2f(M - m);   // an empty state is all zeros, one of NaN scores NaN
+        L *= keep;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[e] *= keep;
+        M = m;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i0 + u >= n) break;
+            const float f = ml[u].x == -INFINITY ? 1.f : exp2f(ml[u].x - M);
+            L += f * ml[u].y;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) acc[e] += f * x[u][e];
+        }
     }
     const long long row = (long long)(c.pair / p.Hkv) * p.Hq + (long long)(c.pair % p.Hkv) * p.G + h;
 #pragma unroll
