@@ -3,6 +3,9 @@
 // C-ABI layer (paged_api.cu) and kernels.
 #pragma once
 
+#include <atomic>
+#include <utility>
+
 #include "msa_internal.h"
 
 namespace msa {
@@ -37,6 +40,48 @@ __host__ __device__ __forceinline__ uint32_t pow2_scale_bits(uint32_t abs_bf16)
 // 128-byte (box0 = 128) or 64-byte (box0 = 64) swizzle, zero fill out of bounds.
 cudaError_t make_tmap_u8_3d(CUtensorMap *map, const void *base, unsigned long long d0, unsigned long long d1,
                             unsigned long long d2, unsigned box0, unsigned box1);
+
+// The paged kernels follow one another in a step, each a few microseconds to a
+// few tens, so each may be set up while its predecessor still runs: it is
+// launched with programmatic stream serialisation, lets its own successor be
+// set up in turn (chain_next) and waits for the predecessor's end, its writes
+// visible, before it touches global memory (chain_wait).  After any other
+// kernel this is an ordinary launch.
+MSA_DEV void chain_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+MSA_DEV void chain_next() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+
+template <class... P, class... A>
+cudaError_t launch_chained(const char *name, void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t s, A &&...args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    TimedLaunch timed_(name, s);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+    if (e == cudaSuccess) note_launch();
+    return e;
+}
+
+// Allows `bytes` of dynamic shared memory for a kernel, once per device (`done`: the kernel's own).
+template <class K>
+cudaError_t allow_smem(K *kernel, int bytes, std::atomic<unsigned long long> &done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (bit & done.load(std::memory_order_acquire)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && bit) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 struct PlanArgs {
     const int32_t *new_lens, *lens_in, *ended, *free_in;

@@ -51,6 +51,8 @@ append_kernel(PagedProblem p, const uint4 *__restrict__ k_new, const uint4 *__re
     constexpr int N = kPage / RPI;            // loads that cover a page
     __shared__ uint32_t part[2][4];
 
+    chain_next();
+    chain_wait();
     const int u = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
     const int t0 = segs[u], t1 = segs[u + 1], cnt = t1 - t0;
     if (cnt <= 0) return;
@@ -154,16 +156,10 @@ cudaError_t launch_paged_append(const PagedProblem &p, const bf16 *k_new, const 
                                 float *v_scale, bf16 *k_idx, DeviceStatus *st, cudaStream_t s)
 {
     const dim3 grid(paged_segments(p), p.Hkv + (ki_new ? 1 : 0));
-    auto run = [&](auto *kernel) {
-        TimedLaunch timed_("paged_append_kernel", s);
-        kernel<<<grid, kThreads, 0, s>>>(p, reinterpret_cast<const uint4 *>(k_new), reinterpret_cast<const uint4 *>(v_new),
-                                         reinterpret_cast<const uint4 *>(ki_new), slots, segs, k8, v8, k_scale, v_scale,
-                                         reinterpret_cast<uint4 *>(k_idx), st);
-    };
-    if (p.d == 128) run(append_kernel<128>);
-    else run(append_kernel<64>);
-    note_launch();
-    return cudaGetLastError();
+    return launch_chained("paged_append_kernel", p.d == 128 ? append_kernel<128> : append_kernel<64>, grid, kThreads, 0, s, p,
+                          reinterpret_cast<const uint4 *>(k_new), reinterpret_cast<const uint4 *>(v_new),
+                          reinterpret_cast<const uint4 *>(ki_new), slots, segs, k8, v8, k_scale, v_scale,
+                          reinterpret_cast<uint4 *>(k_idx), st);
 }
 
 }  // namespace msa

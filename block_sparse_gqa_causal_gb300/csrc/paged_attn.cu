@@ -162,7 +162,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
     __shared__ long long before[kPrefixRows + 1];   // blocks of the rows before each row, one group
     __shared__ int abort_flag;
 
-    asm volatile("griddepcontrol.launch_dependents;\n");   // the join may be set up meanwhile; it waits for this kernel's end
+    chain_next();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = p.G;
     const bool even = p.T <= kPrefixRows;
 
@@ -185,6 +185,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
         }
         fence_mbar_init();
     }
+    chain_wait();
     if (even)
         for (int t = tid; t < p.T; t += kThreads) {
             int req, pos;
@@ -540,7 +541,8 @@ __global__ void __launch_bounds__(256)
 join_kernel(PagedProblem p, const CutRow *__restrict__ cut, const float *__restrict__ part_o,
             const float2 *__restrict__ part_ml, bf16 *__restrict__ o, float *__restrict__ lse)
 {
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");   // launched before the main kernel's end
+    chain_next();
+    chain_wait();
     const CutRow c = cut[blockIdx.x];
     const int h = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (c.pair < 0 || h >= p.G) return;
@@ -615,32 +617,15 @@ cudaError_t launch_paged_attn(const PagedProblem &p, const bf16 *q, const uint8_
     if (e != cudaSuccess) return e;
     auto run = [&](auto dtag) {
         constexpr int D = decltype(dtag)::value;
-        e = cudaFuncSetAttribute(attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnSmem<D>::BYTES);
-        if (e != cudaSuccess) return;
-        {
-            TimedLaunch timed_("paged_attn_kernel", s);
-            attn_kernel<D><<<ctas, kThreads, AttnSmem<D>::BYTES, s>>>(p, q, tk, tv, k_scale, v_scale, block_table, row_req,
-                                                                      row_pos, sel, o, lse, part_o, part_ml, cut, st);
-        }
-        note_launch();
-        if (cuts) {
-            TimedLaunch timed_("paged_attn_join_kernel", s);
-            cudaLaunchConfig_t cfg{};
-            cfg.gridDim = dim3(ctas);
-            cfg.blockDim = dim3(256);
-            cfg.stream = s;
-            cudaLaunchAttribute attr{};
-            attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-            attr.val.programmaticStreamSerializationAllowed = 1;
-            cfg.attrs = &attr;
-            cfg.numAttrs = 1;
-            e = cudaLaunchKernelEx(&cfg, join_kernel<D>, p, (const CutRow *)cut, (const float *)part_o, (const float2 *)part_ml, o, lse);
-            note_launch();
-        }
+        static std::atomic<unsigned long long> allowed{0};
+        if ((e = allow_smem(attn_kernel<D>, AttnSmem<D>::BYTES, allowed)) != cudaSuccess) return e;
+        e = launch_chained("paged_attn_kernel", attn_kernel<D>, dim3(ctas), kThreads, AttnSmem<D>::BYTES, s, p, q, tk, tv, k_scale,
+                           v_scale, block_table, row_req, row_pos, sel, o, lse, part_o, part_ml, cut, st);
+        if (e != cudaSuccess || !cuts) return e;
+        return launch_chained("paged_attn_join_kernel", join_kernel<D>, dim3(ctas), 256, 0, s, p, (const CutRow *)cut,
+                              (const float *)part_o, (const float2 *)part_ml, o, lse);
     };
-    if (p.d == 128) run(std::integral_constant<int, 128>{});
-    else run(std::integral_constant<int, 64>{});
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return p.d == 128 ? run(std::integral_constant<int, 128>{}) : run(std::integral_constant<int, 64>{});
 }
 
 }  // namespace msa

@@ -84,6 +84,8 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedProblem p, PlanArgs a, 
 {
     __shared__ Sums warp_sum[32];
     __shared__ int bad;
+    chain_next();
+    chain_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, nwarp = nthr >> 5;
     const int head = a.free_in[0], count = a.free_in[1];
     const int most = p.max_blocks * kPage;
@@ -212,6 +214,8 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedProblem p, PlanArgs a, 
 __global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(PagedProblem p, PlanArgs a, const int32_t *scratch, int S,
                                                                  DeviceStatus *st)
 {
+    chain_next();
+    chain_wait();
     const int i = blockIdx.x * kFillThreads + threadIdx.x;
     fill_entry(p, a, scratch, S, a.q_starts[p.R], scratch[1], scratch[0], i, st);
 }
@@ -226,18 +230,11 @@ cudaError_t launch_paged_plan(const PagedProblem &p, const PlanArgs &a, int32_t 
     const bool fused = p.T <= kFusedRows;
     const int want = std::max(p.R, fused ? p.T : 1);
     const int threads = std::min(1024, std::max(64, (want + 31) / 32 * 32));
-    {
-        TimedLaunch timed_("paged_plan_kernel", s);
-        plan_kernel<<<1, threads, 0, s>>>(p, a, scratch, S, fused ? 1 : 0, st);
-    }
-    note_launch();
-    if (!fused) {
-        const int n = std::max(p.T, S + 1);
-        TimedLaunch timed_("paged_plan_fill_kernel", s);
-        plan_fill_kernel<<<(n + kFillThreads - 1) / kFillThreads, kFillThreads, 0, s>>>(p, a, scratch, S, st);
-        note_launch();
-    }
-    return cudaGetLastError();
+    cudaError_t e = launch_chained("paged_plan_kernel", plan_kernel, dim3(1), threads, 0, s, p, a, scratch, S, fused ? 1 : 0, st);
+    if (e != cudaSuccess || fused) return e;
+    const int n = std::max(p.T, S + 1);
+    return launch_chained("paged_plan_fill_kernel", plan_fill_kernel, dim3((n + kFillThreads - 1) / kFillThreads), kFillThreads, 0,
+                          s, p, a, (const int32_t *)scratch, S, st);
 }
 
 }  // namespace msa

@@ -14,6 +14,7 @@
 // consecutive blocks; the scale, a positive factor, is applied after the
 // maximum.
 #include <algorithm>
+#include <type_traits>
 
 #include "paged.h"
 #include "tc.cuh"
@@ -50,6 +51,8 @@ scores_kernel(PagedProblem p, const bf16 *__restrict__ q_idx, const __grid_const
     __shared__ int valid[kStages];
     __shared__ int abort_flag;
 
+    chain_next();
+    chain_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int t = blockIdx.x / head_tiles, h0 = blockIdx.x % head_tiles * M;
     const int req = row_req[t];
@@ -215,23 +218,19 @@ cudaError_t launch_paged_block_scores(const PagedProblem &p, const bf16 *q_idx, 
     CUtensorMap tm;
     cudaError_t e = make_tmap_bf16_3d(&tm, k_idx, p.d_idx, kPage, p.n_pages, p.d_idx * 2ull, (unsigned long long)kPage * p.d_idx * 2, 64, kPage);
     if (e != cudaSuccess) return e;
-    auto run = [&](auto *kernel, int smem) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return;
-        TimedLaunch timed_("paged_block_scores_kernel", s);
-        kernel<<<grid, kThreads, smem, s>>>(p, q_idx, tm, block_table, q_starts, row_req, row_pos, scores, rows_per_tile,
-                                            head_tiles, per, st);
+    auto run = [&](auto dtag, auto mtag) {
+        constexpr int DI = decltype(dtag)::value, MT = decltype(mtag)::value, smem = ScoreSmem<DI>::BYTES;
+        static std::atomic<unsigned long long> allowed{0};
+        if ((e = allow_smem(scores_kernel<DI, MT>, smem, allowed)) != cudaSuccess) return e;
+        return launch_chained("paged_block_scores_kernel", scores_kernel<DI, MT>, grid, kThreads, smem, s, p, q_idx, tm, block_table,
+                              q_starts, row_req, row_pos, scores, rows_per_tile, head_tiles, per, st);
     };
-    if (p.d_idx == 128) {
-        if (M == 16) run(scores_kernel<128, 1>, ScoreSmem<128>::BYTES);
-        else run(scores_kernel<128, 2>, ScoreSmem<128>::BYTES);
-    } else {
-        if (M == 16) run(scores_kernel<64, 1>, ScoreSmem<64>::BYTES);
-        else run(scores_kernel<64, 2>, ScoreSmem<64>::BYTES);
-    }
-    if (e != cudaSuccess) return e;
-    note_launch();
-    return cudaGetLastError();
+    using std::integral_constant;
+    if (p.d_idx == 128)
+        return M == 16 ? run(integral_constant<int, 128>{}, integral_constant<int, 1>{})
+                       : run(integral_constant<int, 128>{}, integral_constant<int, 2>{});
+    return M == 16 ? run(integral_constant<int, 64>{}, integral_constant<int, 1>{})
+                   : run(integral_constant<int, 64>{}, integral_constant<int, 2>{});
 }
 
 }  // namespace msa

@@ -52,6 +52,8 @@ topk_kernel(PagedProblem p, const float *__restrict__ scores, const int32_t *__r
     static_assert(W == 1 || R == 1, "a row's warps fill the CTA");
     __shared__ int list[W * R][kTile];                        // the blocks of a tile that reach the bound, ascending
     __shared__ unsigned long long lists[W][32];
+    chain_next();
+    chain_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long row = W == 1 ? (long long)blockIdx.x * R + warp : blockIdx.x;
     if (row >= (long long)p.T * p.Hkv) return;
@@ -137,13 +139,9 @@ cudaError_t launch_paged_block_topk(const PagedProblem &p, const float *scores, 
 {
     constexpr int W = 8, R = 4;
     const long long rows = (long long)p.T * p.Hkv;
-    {
-        TimedLaunch timed_("paged_block_topk_kernel", s);
-        if (p.max_blocks > kTile) topk_kernel<W, 1><<<(unsigned)rows, 32 * W, 0, s>>>(p, scores, row_pos, sel, st);
-        else topk_kernel<1, R><<<(unsigned)((rows + R - 1) / R), 32 * R, 0, s>>>(p, scores, row_pos, sel, st);
-    }
-    note_launch();
-    return cudaGetLastError();
+    const bool wide = p.max_blocks > kTile;
+    return launch_chained("paged_block_topk_kernel", wide ? topk_kernel<W, 1> : topk_kernel<1, R>,
+                          dim3((unsigned)(wide ? rows : (rows + R - 1) / R)), 32 * (wide ? W : R), 0, s, p, scores, row_pos, sel, st);
 }
 
 }  // namespace msa
