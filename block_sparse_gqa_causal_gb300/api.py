@@ -8,7 +8,6 @@ built, the first call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -134,6 +133,33 @@ class PagedShape:
     @cached_property
     def _ref(self):
         return ctypes.byref(self.c())
+
+    @cached_property
+    def _specs(self) -> dict:
+        """What each call takes: (name, shape, dtype, may be None) of its tensors, in the order of the C arguments."""
+        i32, f32, bf, f8 = torch.int32, torch.float32, torch.bfloat16, torch.float8_e4m3fn
+        table = ("block_table", (self.R, self.max_blocks), i32, False)
+        rows = [(n, (self.T,), i32, False) for n in ("row_req", "row_pos")]
+        cache = [(n, (self.n_pages, self.Hkv, PAGE, self.d), f8, False) for n in ("k8", "v8")]
+        scales = [(n, (self.n_pages, self.Hkv), f32, False) for n in ("k_scale", "v_scale")]
+        k_idx = ("k_idx", (self.n_pages, PAGE, self.d_idx), bf, False)
+        new = [(n, (self.T, self.Hkv, self.d), bf, True) for n in ("k_new", "v_new")] + [("k_idx_new", (self.T, self.d_idx), bf, True)]
+        sel = (self.T, self.Hkv, self.topk)
+        scores = (self.T, self.Hkv, self.max_blocks)
+        plan = [("lens", (self.R,)), ("free_state", (2,)), ("q_starts", (self.R + 1,)), ("row_req", (self.T,)), ("row_pos", (self.T,)),
+                ("slots", (self.T,)), ("segs", (self.n_segs + 1,))]
+        return {
+            OP_PAGED_PLAN: [("new_lens", (self.R,), i32, False), ("lens", (self.R,), i32, False), ("ended", (self.R,), i32, True), table,
+                            ("free_pages", (self.n_pages,), i32, False), ("free_state", (2,), i32, False)]
+            + [(n, s, i32, False) for n, s in plan],
+            OP_PAGED_APPEND: new + [("slots", (self.T,), i32, False), ("segs", (self.n_segs + 1,), i32, False)]
+            + [(n, s, t, True) for n, s, t, _ in cache + scales + [k_idx]],
+            OP_PAGED_BLOCK_SCORES: [("q_idx", (self.T, self.Hkv, self.d_idx), bf, False), k_idx, table, ("q_starts", (self.R + 1,), i32, False)]
+            + rows + [("block_scores", scores, f32, False)],
+            OP_PAGED_BLOCK_TOPK: [("block_scores", scores, f32, False), rows[1], ("sel_idx", sel, i32, False)],
+            OP_PAGED_ATTN: [("q", (self.T, self.Hq, self.d), bf, False)] + cache + scales + [table] + rows
+            + [("sel_idx", sel, i32, True), ("o", (self.T, self.Hq, self.d), bf, False), ("lse", (self.T, self.Hq), f32, False)],
+        }
 
 
 class PagedPlan(NamedTuple):
@@ -415,20 +441,16 @@ def kv_append(shape: Shape, k_new, v_new, k_idx_new, k, v, k_idx, *, stream=None
                                _ptr(k_idx), _stream(stream)))
 
 
-_HERE_CTX = contextlib.nullcontext()
-
-
-def _place(t: torch.Tensor, stream):
-    """The context in which a paged call allocates and launches: the tensors'
-    device and, when one is given, the stream (so that what is allocated there
-    is not handed out again before the call's kernels are done with it)."""
+def _place(dev, stream):
+    """None where the tensors' device is the current one and no stream is given;
+    else the context in which a paged call allocates and launches (the stream, so
+    that what is allocated there is not handed out again before the call's
+    kernels are done with it)."""
     if stream is not None:
-        if stream.device != t.device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+        if stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
         return torch.cuda.stream(stream)
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        return torch.cuda.device(t.device)
-    return _HERE_CTX
+    return torch.cuda.device(dev) if dev.type == "cuda" and dev.index != torch.cuda.current_device() else None
 
 
 # The current stream's handle of a device; the public call builds a Stream object first, which
@@ -440,12 +462,26 @@ def _stream_on(dev) -> int:
     return _raw_stream(dev.index) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
-def _need_on(dev, specs) -> None:
-    """_need for several (tensor, name, shape, dtype), all on one CUDA device."""
-    for t, name, shape, dtype in specs:
-        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != dev or not t.is_cuda:
-            raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {tuple(shape)} on {dev} (a CUDA device), "
+def _paged_call(fn, shape: PagedShape, op: int, dev, tensors, workspace) -> None:
+    """Checks the tensors against the call's specs, all on one CUDA device, and makes the call."""
+    ptrs = []
+    for (name, shp, dtype, optional), t in zip(shape._specs[op], tensors):
+        if t is None:
+            if not optional:
+                raise ValueError(f"{name} is None")
+            ptrs.append(None)
+            continue
+        if t.dtype is not dtype or t.shape != shp or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {shp} on {dev}, "
                              f"got {t.dtype} {tuple(t.shape)} contiguous={t.is_contiguous()} on {t.device}")
+        ptrs.append(t.data_ptr())
+    if dev.type != "cuda":
+        raise ValueError(f"need CUDA tensors, got {dev}")
+    if workspace is None:
+        workspace = new_paged_workspace(shape, op, dev)
+    elif workspace.device != dev or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        raise ValueError(f"workspace: need a contiguous uint8 tensor on {dev}, got {workspace.dtype} on {workspace.device}")
+    _check(fn(shape._ref, *ptrs, workspace.data_ptr(), workspace.numel(), _stream_on(dev)))
 
 
 def paged_workspace_size(shape: PagedShape, op: int) -> int:
@@ -462,14 +498,6 @@ def new_paged_workspace(shape: PagedShape, op: int, device=None) -> torch.Tensor
     return ws
 
 
-def _paged_ws(ws, shape, op, device):
-    if ws is None:
-        return new_paged_workspace(shape, op, device)
-    if ws.device != device or ws.dtype is not torch.uint8 or not ws.is_contiguous():
-        raise ValueError(f"workspace: need a contiguous uint8 tensor on {device}, got {ws.dtype} on {ws.device}")
-    return ws
-
-
 def paged_plan(shape: PagedShape, new_lens, lens, block_table, free_pages, free_state, *, ended=None, out=None,
                workspace=None, stream=None) -> PagedPlan:
     """msa_paged_plan: the step's pages, block tables and slot maps from the
@@ -477,24 +505,17 @@ def paged_plan(shape: PagedShape, new_lens, lens, block_table, free_pages, free_
     [R, max_blocks] and free_pages [n_pages] int32 are updated in place.  Returns a
     PagedPlan (pass `out` to reuse its tensors; its lens and free_state may be
     the tensors passed in)."""
-    s, i32, dev = shape, torch.int32, new_lens.device
-    specs = [(new_lens, "new_lens", (s.R,), i32), (lens, "lens", (s.R,), i32),
-             (block_table, "block_table", (s.R, s.max_blocks), i32), (free_pages, "free_pages", (s.n_pages,), i32),
-             (free_state, "free_state", (2,), i32)]
-    if ended is not None:
-        specs.append((ended, "ended", (s.R,), i32))
-    sizes = [s.R, 2, s.R + 1, s.T, s.T, s.T, s.n_segs + 1]
-    if out is not None:
-        specs += [(t, n, (m,), i32) for t, n, m in zip(out, PagedPlan._fields, sizes)]
-    _need_on(dev, specs)
-    with _place(new_lens, stream):
-        ws = _paged_ws(workspace, s, OP_PAGED_PLAN, dev)
-        if out is None:
-            out = PagedPlan(*[torch.empty(n, dtype=i32, device=dev) for n in sizes])
-        _check(lib().msa_paged_plan(s._ref, new_lens.data_ptr(), lens.data_ptr(), None if ended is None else ended.data_ptr(),
-                                    block_table.data_ptr(), free_pages.data_ptr(), free_state.data_ptr(),
-                                    *[t.data_ptr() for t in out], ws.data_ptr(), ws.numel(),
-                                    _stream_on(dev)))
+    s, dev = shape, new_lens.device
+    place = _place(dev, stream)
+    if place is not None:
+        with place:
+            return paged_plan(s, new_lens, lens, block_table, free_pages, free_state, ended=ended, out=out, workspace=workspace)
+    if out is None:
+        row = torch.empty(s.T, dtype=torch.int32, device=dev)
+        out = PagedPlan(torch.empty_like(lens), torch.empty_like(free_state), torch.empty(s.R + 1, dtype=torch.int32, device=dev),
+                        row, torch.empty_like(row), torch.empty_like(row), torch.empty(s.n_segs + 1, dtype=torch.int32, device=dev))
+    _paged_call((_lib or lib()).msa_paged_plan, s, OP_PAGED_PLAN, dev,
+                (new_lens, lens, ended, block_table, free_pages, free_state, *out), workspace)
     return out
 
 
@@ -504,59 +525,41 @@ def paged_append(shape: PagedShape, k_new, v_new, k_idx_new, slots, segs, k8, v8
     (bf16) into the caches k8, v8 [n_pages, Hkv, 128, d] (float8_e4m3fn) with
     k_scale, v_scale [n_pages, Hkv] (fp32), and k_idx [n_pages, 128, d_idx] (bf16),
     at a plan's slots and segs.  The K and V group, or the K_idx pair, may be None."""
-    s, bf, dev = shape, torch.bfloat16, slots.device
-    specs = [(slots, "slots", (s.T,), torch.int32), (segs, "segs", (s.n_segs + 1,), torch.int32)]
-    for t, name, shp, dtype in ((k_new, "k_new", (s.T, s.Hkv, s.d), bf), (v_new, "v_new", (s.T, s.Hkv, s.d), bf),
-                                (k_idx_new, "k_idx_new", (s.T, s.d_idx), bf),
-                                (k8, "k8", (s.n_pages, s.Hkv, PAGE, s.d), torch.float8_e4m3fn),
-                                (v8, "v8", (s.n_pages, s.Hkv, PAGE, s.d), torch.float8_e4m3fn),
-                                (k_scale, "k_scale", (s.n_pages, s.Hkv), torch.float32),
-                                (v_scale, "v_scale", (s.n_pages, s.Hkv), torch.float32),
-                                (k_idx, "k_idx", (s.n_pages, PAGE, s.d_idx), bf)):
-        if t is not None:
-            specs.append((t, name, shp, dtype))
-    _need_on(dev, specs)
-    ptr = [None if t is None else t.data_ptr() for t in (k_new, v_new, k_idx_new, slots, segs, k8, v8, k_scale, v_scale, k_idx)]
-    with _place(slots, stream):
-        ws = _paged_ws(workspace, s, OP_PAGED_APPEND, dev)
-        _check(lib().msa_paged_append(s._ref, *ptr, ws.data_ptr(), ws.numel(), _stream_on(dev)))
+    dev = slots.device
+    place = _place(dev, stream)
+    if place is not None:
+        with place:
+            return paged_append(shape, k_new, v_new, k_idx_new, slots, segs, k8, v8, k_scale, v_scale, k_idx, workspace=workspace)
+    _paged_call((_lib or lib()).msa_paged_append, shape, OP_PAGED_APPEND, dev,
+                (k_new, v_new, k_idx_new, slots, segs, k8, v8, k_scale, v_scale, k_idx), workspace)
 
 
 def paged_block_scores(shape: PagedShape, q_idx, k_idx, block_table, q_starts, row_req, row_pos, *, block_scores=None,
                        workspace=None, stream=None):
     """msa_paged_block_scores: [T, Hkv, max_blocks] fp32 of q_idx [T, Hkv, d_idx] and
     the pages k_idx [n_pages, 128, d_idx] (bf16)."""
-    s, i32, dev = shape, torch.int32, q_idx.device
-    specs = [(q_idx, "q_idx", (s.T, s.Hkv, s.d_idx), torch.bfloat16), (k_idx, "k_idx", (s.n_pages, PAGE, s.d_idx), torch.bfloat16),
-             (block_table, "block_table", (s.R, s.max_blocks), i32), (q_starts, "q_starts", (s.R + 1,), i32),
-             (row_req, "row_req", (s.T,), i32), (row_pos, "row_pos", (s.T,), i32)]
-    if block_scores is not None:
-        specs.append((block_scores, "block_scores", (s.T, s.Hkv, s.max_blocks), torch.float32))
-    _need_on(dev, specs)
-    with _place(q_idx, stream):
-        ws = _paged_ws(workspace, s, OP_PAGED_BLOCK_SCORES, dev)
-        if block_scores is None:
-            block_scores = torch.empty((s.T, s.Hkv, s.max_blocks), dtype=torch.float32, device=dev)
-        _check(lib().msa_paged_block_scores(s._ref, q_idx.data_ptr(), k_idx.data_ptr(), block_table.data_ptr(),
-                                            q_starts.data_ptr(), row_req.data_ptr(), row_pos.data_ptr(),
-                                            block_scores.data_ptr(), ws.data_ptr(), ws.numel(),
-                                            _stream_on(dev)))
+    s, dev = shape, q_idx.device
+    place = _place(dev, stream)
+    if place is not None:
+        with place:
+            return paged_block_scores(s, q_idx, k_idx, block_table, q_starts, row_req, row_pos, block_scores=block_scores, workspace=workspace)
+    if block_scores is None:
+        block_scores = torch.empty((s.T, s.Hkv, s.max_blocks), dtype=torch.float32, device=dev)
+    _paged_call((_lib or lib()).msa_paged_block_scores, s, OP_PAGED_BLOCK_SCORES, dev,
+                (q_idx, k_idx, block_table, q_starts, row_req, row_pos, block_scores), workspace)
     return block_scores
 
 
 def paged_block_topk(shape: PagedShape, block_scores, row_pos, *, sel_idx=None, workspace=None, stream=None):
     """msa_paged_block_topk: sel_idx [T, Hkv, topk] int32 of block_scores [T, Hkv, max_blocks]."""
     s, dev = shape, block_scores.device
-    specs = [(block_scores, "block_scores", (s.T, s.Hkv, s.max_blocks), torch.float32), (row_pos, "row_pos", (s.T,), torch.int32)]
-    if sel_idx is not None:
-        specs.append((sel_idx, "sel_idx", (s.T, s.Hkv, s.topk), torch.int32))
-    _need_on(dev, specs)
-    with _place(block_scores, stream):
-        ws = _paged_ws(workspace, s, OP_PAGED_BLOCK_TOPK, dev)
-        if sel_idx is None:
-            sel_idx = torch.empty((s.T, s.Hkv, s.topk), dtype=torch.int32, device=dev)
-        _check(lib().msa_paged_block_topk(s._ref, block_scores.data_ptr(), row_pos.data_ptr(), sel_idx.data_ptr(),
-                                          ws.data_ptr(), ws.numel(), _stream_on(dev)))
+    place = _place(dev, stream)
+    if place is not None:
+        with place:
+            return paged_block_topk(s, block_scores, row_pos, sel_idx=sel_idx, workspace=workspace)
+    if sel_idx is None:
+        sel_idx = torch.empty((s.T, s.Hkv, s.topk), dtype=torch.int32, device=dev)
+    _paged_call((_lib or lib()).msa_paged_block_topk, s, OP_PAGED_BLOCK_TOPK, dev, (block_scores, row_pos, sel_idx), workspace)
     return sel_idx
 
 
@@ -564,26 +567,15 @@ def paged_attn(shape: PagedShape, q, k8, v8, k_scale, v_scale, block_table, row_
                lse=None, workspace=None, stream=None):
     """msa_paged_attn: (o [T, Hq, d] bf16, lse [T, Hq] fp32) of q [T, Hq, d] bf16 over
     the 8-bit cache: the blocks of sel_idx [T, Hkv, topk], or all of them when it is None."""
-    s, i32, f32, dev = shape, torch.int32, torch.float32, q.device
-    specs = [(q, "q", (s.T, s.Hq, s.d), torch.bfloat16), (k8, "k8", (s.n_pages, s.Hkv, PAGE, s.d), torch.float8_e4m3fn),
-             (v8, "v8", (s.n_pages, s.Hkv, PAGE, s.d), torch.float8_e4m3fn), (k_scale, "k_scale", (s.n_pages, s.Hkv), f32),
-             (v_scale, "v_scale", (s.n_pages, s.Hkv), f32), (block_table, "block_table", (s.R, s.max_blocks), i32),
-             (row_req, "row_req", (s.T,), i32), (row_pos, "row_pos", (s.T,), i32)]
-    if sel_idx is not None:
-        specs.append((sel_idx, "sel_idx", (s.T, s.Hkv, s.topk), i32))
-    if o is not None:
-        specs.append((o, "o", (s.T, s.Hq, s.d), torch.bfloat16))
-    if lse is not None:
-        specs.append((lse, "lse", (s.T, s.Hq), f32))
-    _need_on(dev, specs)
-    with _place(q, stream):
-        ws = _paged_ws(workspace, s, OP_PAGED_ATTN, dev)
-        o = torch.empty((s.T, s.Hq, s.d), dtype=torch.bfloat16, device=dev) if o is None else o
-        lse = torch.empty((s.T, s.Hq), dtype=f32, device=dev) if lse is None else lse
-        _check(lib().msa_paged_attn(s._ref, q.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                                    block_table.data_ptr(), row_req.data_ptr(), row_pos.data_ptr(),
-                                    None if sel_idx is None else sel_idx.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                                    ws.data_ptr(), ws.numel(), _stream_on(dev)))
+    s, dev = shape, q.device
+    place = _place(dev, stream)
+    if place is not None:
+        with place:
+            return paged_attn(s, q, k8, v8, k_scale, v_scale, block_table, row_req, row_pos, sel_idx=sel_idx, o=o, lse=lse, workspace=workspace)
+    o = torch.empty_like(q) if o is None else o
+    lse = torch.empty((s.T, s.Hq), dtype=torch.float32, device=dev) if lse is None else lse
+    _paged_call((_lib or lib()).msa_paged_attn, s, OP_PAGED_ATTN, dev,
+                (q, k8, v8, k_scale, v_scale, block_table, row_req, row_pos, sel_idx, o, lse), workspace)
     return o, lse
 
 

@@ -59,6 +59,7 @@ constexpr int kStages = 3;
 
 constexpr int kPrefixRows = 512;                // most rows whose blocks are cut evenly; above, whole rows are dealt out
 constexpr int kMinBlocks = 2;                   // a stretch has at least this many blocks
+constexpr int kWholeBlocks = 8;                 // rows of up to so many blocks are not cut: joining costs what it would save
 
 enum { kFirst = 1, kLast = 2, kEnd = 4 };       // of a piece; of the CTA's stretch
 struct Meta {
@@ -164,7 +165,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
 
     chain_next();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = p.G;
-    const bool even = p.T <= kPrefixRows;
+    const bool even = cut != nullptr;           // stretches of equal length; else whole rows are dealt out
 
     // blocks that a group of row t has to look at; 0: not a row (entries of a selection may sit in any of its slots)
     auto blocks_of = [&](int t, int &req, int &pos) {
@@ -333,7 +334,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                 piece(t, r, row_req[t], row_pos[t], j0, j1, whole ? -1 : 2 * me + (j0 > 0 ? 0 : 1));
                 x += j1 - j0;
             }
-            if (lane == 0 && cut) cut[me] = row;
+            if (lane == 0) cut[me] = row;
         } else {
             const long long pairs = (long long)p.T * p.Hkv;
             for (long long i = me; i < pairs && live; i += gridDim.x) {
@@ -585,19 +586,25 @@ join_kernel(PagedProblem p, const CutRow *__restrict__ cut, const float *__restr
     if (lane == 0) lse[row] = (M + log2f(L)) * kLn2;
 }
 
+// Whether rows are cut into equal stretches.  Not with many rows (the list is
+// summed up by every CTA) or short ones: at one row of two groups and eight
+// blocks, the whole rows take 17 us a call and cut ones with their join 21.
+bool cuts_rows(const PagedProblem &p, bool sparse)
+{
+    return p.T <= kPrefixRows && (sparse ? p.topk : p.max_blocks) > kWholeBlocks;
+}
 // Two CTAs to an SM, fewer where that leaves stretches under kMinBlocks.
 int attn_ctas(const PagedProblem &p, bool sparse)
 {
     const long long rows = (long long)p.T * p.Hkv, most = 2LL * p.num_sms;
-    if (p.T > kPrefixRows) return (int)std::min(most, rows);
-    return (int)std::max<long long>(1, std::min(most, rows * (sparse ? p.topk : p.max_blocks) / kMinBlocks));
+    return (int)std::min(most, cuts_rows(p, sparse) ? rows * (sparse ? p.topk : p.max_blocks) / kMinBlocks : rows);
 }
 
 }  // namespace
 
 size_t paged_attn_scratch_floats(const PagedProblem &p)
 {
-    if (p.T > kPrefixRows) return 0;
+    if (!cuts_rows(p, true) && !cuts_rows(p, false)) return 0;
     return (size_t)2 * p.num_sms * (2 * 8 * (p.d + 2) + sizeof(CutRow) / 4);
 }
 
@@ -607,7 +614,7 @@ cudaError_t launch_paged_attn(const PagedProblem &p, const bf16 *q, const uint8_
                               float *scratch, DeviceStatus *st, cudaStream_t s)
 {
     const int ctas = attn_ctas(p, sel != nullptr);
-    const bool cuts = p.T <= kPrefixRows && ctas > 1;
+    const bool cuts = cuts_rows(p, sel != nullptr);
     CutRow *cut = cuts ? reinterpret_cast<CutRow *>(scratch) : nullptr;
     float *part_o = scratch + (size_t)2 * p.num_sms * sizeof(CutRow) / 4;
     float2 *part_ml = reinterpret_cast<float2 *>(part_o + (size_t)2 * p.num_sms * 2 * 8 * p.d);

@@ -89,11 +89,12 @@ def test_workspace_sizes(api):
     assert api.paged_workspace_size(sh, api.OP_PAGED_APPEND) == 256
     assert api.paged_workspace_size(sh, api.OP_PAGED_PLAN) == 512          # 16 bytes and 16 a request
     # attention: two states of a group's heads for each of two CTAs an SM, whatever the batch; none for many rows
-    for kw in (GOOD, {**GOOD, "T": 512}, {**GOOD, "T": 1, "R": 1, "max_blocks": 8192}):
+    for kw in (GOOD, {**GOOD, "T": 512}, {**GOOD, "T": 1, "R": 1, "max_blocks": 8192}, {**GOOD, "max_blocks": 8, "topk": 9}):
         s = api.PagedShape(**kw)
         n = api.paged_workspace_size(s, api.OP_PAGED_ATTN) - 256
         assert 0 < n <= 2 * 256 * (2 * 8 * (s.d + 2) * 4 + 16) + 256
-    assert api.paged_workspace_size(api.PagedShape(**{**GOOD, "T": 513}), api.OP_PAGED_ATTN) == 256
+    for kw in ({"T": 513}, {"max_blocks": 8, "topk": 8}):
+        assert api.paged_workspace_size(api.PagedShape(**{**GOOD, **kw}), api.OP_PAGED_ATTN) == 256
     with pytest.raises(api.MsaError):
         api.paged_workspace_size(sh, 15)
     with pytest.raises(api.MsaError):
@@ -111,9 +112,11 @@ def test_binding_refuses_host_tensors_shapes_and_types(api):
     with pytest.raises(ValueError, match="q_idx"):
         api.paged_block_scores(sh, torch.zeros(8, 2, 64), torch.zeros(64, 128, 64), i32(4, 16), i32(5), i32(8), i32(8))
     with pytest.raises(ValueError, match="slots"):
-        api.paged_append(sh, None, None, torch.zeros(8, 64), i32(8), i32(9), None, None, None, None, torch.zeros(64, 128, 64))
+        api.paged_append(sh, None, None, torch.zeros(8, 64, dtype=torch.bfloat16), i32(7), i32(9), None, None, None, None, torch.zeros(64, 128, 64))
     with pytest.raises(ValueError, match="q:"):
         api.paged_attn(sh, torch.zeros(8, 8, 64), None, None, None, None, None, None, None)
+    with pytest.raises(ValueError, match="k8 is None"):
+        api.paged_attn(sh, torch.zeros(8, 8, 64, dtype=torch.bfloat16), None, None, None, None, None, None, None)
 
 
 # ------------------------------------------------------------------ the reference's pins
