@@ -10,9 +10,14 @@
 // shared-memory stages by TMA; each of three consumer warps takes a whole page
 // (no reduction across warps), always in the same stage, so that it sees every
 // phase of that stage's barriers, and multiplies it with the queries it keeps
-// in registers, 16 or 32 (row, group) pairs to a CTA.  A CTA takes a share of
-// consecutive blocks; the scale, a positive factor, is applied after the
-// maximum.
+// in registers: a tile of 16 or 32 (row, group) pairs of one request.  The
+// scale, a positive factor, is applied after the maximum.
+//
+// The tiles' pages, one tile after another, are cut into equal stretches for
+// the two CTAs that each SM holds, whatever the requests' lengths: at four
+// caches of 131,072 to 1,048,576 tokens 97 us against 100 for a grid of
+// (tile, share) CTAs.  With more rows than kPrefixRows, whole tiles are dealt
+// out.
 #include <algorithm>
 #include <type_traits>
 
@@ -36,46 +41,32 @@ struct ScoreSmem {
     static constexpr int BYTES = kStages * STAGE + 1024;   // + alignment
 };
 
+constexpr int kPrefixRows = 512;       // most rows whose pages are cut evenly
+
+struct PageMeta {
+    int t, h0, c;      // the tile's first row and group, the block; t < 0 after the last
+    int valid;
+};
+
 template <int DI, int MT>
 __global__ void __launch_bounds__(kThreads, 2)
 scores_kernel(PagedProblem p, const bf16 *__restrict__ q_idx, const __grid_constant__ CUtensorMap tm_k,
               const int32_t *__restrict__ block_table, const int32_t *__restrict__ q_starts,
               const int32_t *__restrict__ row_req, const int32_t *__restrict__ row_pos, float *__restrict__ scores,
-              int rows_per_tile, int head_tiles, int per, DeviceStatus *st)
+              int rows_per_tile, int head_tiles, DeviceStatus *st)
 {
     using S = ScoreSmem<DI>;
     constexpr int M = 16 * MT;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     __shared__ uint64_t full[kStages], empty[kStages];
-    __shared__ int valid[kStages];
+    __shared__ PageMeta meta[kStages];
+    __shared__ long long before[kPrefixRows + 1];      // pages of the tiles before each row's
     __shared__ int abort_flag;
 
-    chain_next();
-    chain_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int t = blockIdx.x / head_tiles, h0 = blockIdx.x % head_tiles * M;
-    const int req = row_req[t];
-    if (req < 0) return;                               // a row behind the last request
-    if (req >= p.R) {
-        if (tid == 0) report(st, kDevCheck, 121, req);
-        return;
-    }
-    // a tile is up to rows_per_tile rows of one request, owned by its first row
-    const int first = q_starts[req], end = min(q_starts[req + 1], p.T);
-    if ((t - first) % rows_per_tile != 0) return;
-    const int nrows = max(1, min(rows_per_tile, end - t));
-    const int pairs = min(M, nrows * min(p.Hkv, M));   // (row, group) pairs, groups fastest
-    const int last_pos = row_pos[t + nrows - 1];
-    const int c_lo = blockIdx.y * per, c_hi = min(c_lo + per, p.max_blocks);
-    const int seen = last_pos < 0 ? 0 : min(last_pos / kPage + 1, p.max_blocks);
-    const int n = max(0, min(c_hi, seen) - c_lo);      // pages of this share that some row sees
-    if (last_pos / kPage >= p.max_blocks && tid == 0) report(st, kDevCheck, 122, last_pos);
-
-    auto pair_row = [&](int m) { return t + (p.Hkv >= M ? 0 : m / p.Hkv); };
-    auto pair_head = [&](int m) { return p.Hkv >= M ? h0 + m : m % p.Hkv; };
-    auto pair_ok = [&](int m) { return m < pairs && pair_head(m) < p.Hkv; };
-
+    const bool even = p.T <= kPrefixRows;
+    chain_next();
     if (tid == 0) {
         abort_flag = 0;
         for (int i = 0; i < kStages; ++i) {
@@ -84,71 +75,148 @@ scores_kernel(PagedProblem p, const bf16 *__restrict__ q_idx, const __grid_const
         }
         fence_mbar_init();
     }
+    chain_wait();
+
+    // the rows of the tile that row t begins (a tile is up to rows_per_tile rows of one request); 0: t begins none
+    auto tile_rows = [&](int t) {
+        const int req = row_req[t];
+        if (req < 0) return 0;                         // a row behind the last request
+        if (req >= p.R) {
+            report(st, kDevCheck, 121, req);
+            return 0;
+        }
+        const int first = q_starts[req], end = min(q_starts[req + 1], p.T);
+        return t < first || t >= end || (t - first) % rows_per_tile != 0 ? 0 : min(rows_per_tile, end - t);
+    };
+    // pages that some row of the tile sees
+    auto tile_pages = [&](int t) {
+        const int n = tile_rows(t);
+        const int last = n ? row_pos[t + n - 1] : -1;
+        if (last >= 0 && last / kPage >= p.max_blocks) report(st, kDevCheck, 122, last);
+        return last < 0 ? 0 : min(last / kPage + 1, p.max_blocks);
+    };
+    if (even)
+        for (int t = tid; t < p.T; t += kThreads) before[t] = (long long)tile_pages(t) * head_tiles;
+    __syncthreads();
+    if (even && warp == 0) {
+        long long sum = 0;
+        for (int t0 = 0; t0 < p.T; t0 += 32) {
+            const long long n = t0 + lane < p.T ? before[t0 + lane] : 0;
+            long long inc = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const long long v = __shfl_up_sync(0xffffffffu, inc, d);
+                if (lane >= d) inc += v;
+            }
+            if (t0 + lane < p.T) before[t0 + lane] = sum + inc - n;
+            sum += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (lane == 0) before[p.T] = sum;
+    }
     __syncthreads();
 
     if (warp == kConsumers) {
-        const int32_t *row = block_table + (long long)req * p.max_blocks + c_lo;
-        int mine = 0, i = 0;
-        for (; i < n; ++i) {
-            if (i % 32 == 0) mine = i + lane < n ? row[i + lane] : -1;
-            const int page = __shfl_sync(0xffffffffu, mine, i % 32), s = i % kStages;
-            if (i >= kStages && !mbar_wait_warp(&empty[s], (i / kStages - 1) & 1, st, 123, &abort_flag)) break;
+        int step = 0, copied = 0;
+        bool live = true;
+        auto next = [&](const PageMeta &m, int page) {
+            const int s = step % kStages;
+            if (step >= kStages && !mbar_wait_warp(&empty[s], (step / kStages - 1) & 1, st, 123, &abort_flag)) {
+                live = false;
+                return;
+            }
             if (lane == 0) {
-                const bool ok = (unsigned)page < (unsigned)p.n_pages;
-                valid[s] = ok;
-                if (ok) {
+                meta[s] = m;
+                if (m.valid) {
                     mbar_arrive_expect_tx(&full[s], S::STAGE);
                     for (int h = 0; h < DI / 64; ++h)
                         tma_load_3d(smem + s * S::STAGE + h * S::HALF, &tm_k, &full[s], h * 64, 0, page);
                 } else {
-                    report(st, kDevCheck, 124, page);
+                    if (m.t >= 0) report(st, kDevCheck, 124, page);
                     mbar_arrive(&full[s]);
                 }
             }
+            ++step;
+        };
+        auto piece = [&](int t, int h0, int c_lo, int c_hi) {
+            const int32_t *row = block_table + (long long)row_req[t] * p.max_blocks;
+            for (int base = c_lo; base < c_hi && live; base += 32) {
+                const int mine = base + lane < c_hi ? row[base + lane] : -1;
+                for (int i = 0; i < 32 && base + i < c_hi && live; ++i) {
+                    const int page = __shfl_sync(0xffffffffu, mine, i);
+                    next(PageMeta{t, h0, base + i, (unsigned)page < (unsigned)p.n_pages}, page);
+                }
+            }
+        };
+        const long long me = blockIdx.x;
+        if (even) {
+            const long long W = before[p.T], n = gridDim.x;
+            long long x = W * me / n;
+            const long long x1 = W * (me + 1) / n;
+            int t = 0, hi = p.T;
+            while (hi - t > 1) {                       // the last row that starts at or before x
+                const int mid = (t + hi) >> 1;
+                if (before[mid] <= x) t = mid;
+                else hi = mid;
+            }
+            while (x < x1 && live) {
+                const long long y = x - before[t], all = before[t + 1] - before[t];
+                if (y >= all) {
+                    ++t;
+                    continue;
+                }
+                const int seen = (int)(all / head_tiles), c = (int)(y % seen);
+                const int m = (int)min((long long)(seen - c), x1 - x);
+                piece(t, (int)(y / seen) * M, c, c + m);
+                x += m;
+            }
+        } else {
+            for (long long i = me; i < (long long)p.T * head_tiles && live; i += gridDim.x) {
+                const int t = (int)(i / head_tiles), n = tile_pages(t);
+                if (n) piece(t, (int)(i % head_tiles) * M, 0, n);
+            }
         }
-        // stay until the last copies have landed
-        for (int k = max(0, i - kStages); k < i; ++k) mbar_wait_warp(&full[k % kStages], (k / kStages) & 1, st, 125, nullptr);
+        copied = step;
+        for (int i = 0; i < kConsumers && live; ++i) next(PageMeta{-1, 0, 0, 0}, -1);   // every consumer's end
+        // stay until the last copies have landed (a stage with an end mark has been read)
+        for (int k = max(0, step - kStages); k < copied; ++k) mbar_wait_warp(&full[k % kStages], (k / kStages) & 1, st, 125, nullptr);
         return;
     }
 
-    // this lane's pairs: accumulator rows g and g + 8 of each 16-row tile
+    // this lane's pairs of the tile: accumulator rows g and g + 8 of each 16 rows, groups fastest
     const int g = lane >> 2, q4 = lane & 3;
     uint32_t a[MT][DI / 16][4];
-    int pos[MT][2];
+    int pos[MT][2], first_pos = 0, t = -1, h0 = 0;
+    for (int step = warp;; step += kConsumers) {
+        const int s = step % kStages;
+        if (!mbar_wait_warp(&full[s], (step / kStages) & 1, st, 126, &abort_flag)) return;
+        const PageMeta me = meta[s];
+        if (me.t < 0) break;
+        if (me.t != t || me.h0 != h0) {                // the next tile's queries
+            t = me.t;
+            h0 = me.h0;
+            const int rows = tile_rows(t), req = row_req[t];
+            first_pos = row_pos[t];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int m = mt * 16 + e * 8 + g;
-            const bool ok = pair_ok(m);
-            const int tr = ok ? pair_row(m) : t;
-            pos[mt][e] = ok && row_req[tr] == req ? row_pos[tr] : -1;
-            const uint32_t *src = reinterpret_cast<const uint32_t *>(q_idx + ((long long)tr * p.Hkv + (ok ? pair_head(m) : 0)) * DI);
+                for (int e = 0; e < 2; ++e) {
+                    const int m = mt * 16 + e * 8 + g;
+                    const int tr = t + (p.Hkv >= M ? 0 : m / p.Hkv), h = p.Hkv >= M ? h0 + m : m % p.Hkv;
+                    const bool ok = tr < t + rows && h < p.Hkv && row_req[min(tr, p.T - 1)] == req;
+                    pos[mt][e] = ok ? row_pos[tr] : -1;
+                    const uint32_t *src = reinterpret_cast<const uint32_t *>(q_idx + (ok ? ((long long)tr * p.Hkv + h) * DI : 0));
 #pragma unroll
-            for (int ks = 0; ks < DI / 16; ++ks) {
-                a[mt][ks][e] = ok ? __ldg(src + ks * 8 + q4) : 0u;
-                a[mt][ks][2 + e] = ok ? __ldg(src + ks * 8 + q4 + 4) : 0u;
-            }
+                    for (int ks = 0; ks < DI / 16; ++ks) {
+                        a[mt][ks][e] = ok ? __ldg(src + ks * 8 + q4) : 0u;
+                        a[mt][ks][2 + e] = ok ? __ldg(src + ks * 8 + q4 + 4) : 0u;
+                    }
+                }
         }
-    auto store = [&](int c, const float (&mx)[MT][2]) {
-        if (q4 != 0) return;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int m = mt * 16 + e * 8 + g;
-                if (pos[mt][e] >= 0)
-                    scores[((long long)pair_row(m) * p.Hkv + pair_head(m)) * p.max_blocks + c] = mx[mt][e] * p.scale_idx;
-            }
-    };
-    const int first_pos = row_pos[t];
-    for (int i = warp; i < n; i += kConsumers) {
-        const int s = i % kStages, c = c_lo + i;
-        if (!mbar_wait_warp(&full[s], (i / kStages) & 1, st, 126, &abort_flag)) return;
+        const int c = me.c;
         float mx[MT][2];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) mx[mt][0] = mx[mt][1] = -INFINITY;
-        if (valid[s]) {
+        if (me.valid) {
             const uint8_t *sk = smem + s * S::STAGE;
             const bool whole = c * kPage + kPage - 1 <= first_pos;   // every row sees every token
 #pragma unroll 2
@@ -186,15 +254,19 @@ scores_kernel(PagedProblem p, const bf16 *__restrict__ q_idx, const __grid_const
             for (int e = 0; e < 2; ++e) {
                 mx[mt][e] = fmaxf(mx[mt][e], __shfl_xor_sync(0xffffffffu, mx[mt][e], 1));
                 mx[mt][e] = fmaxf(mx[mt][e], __shfl_xor_sync(0xffffffffu, mx[mt][e], 2));
+                const int m = mt * 16 + e * 8 + g;
+                if (q4 == 0 && pos[mt][e] >= 0) {
+                    const int tr = t + (p.Hkv >= M ? 0 : m / p.Hkv), h = p.Hkv >= M ? h0 + m : m % p.Hkv;
+                    scores[((long long)tr * p.Hkv + h) * p.max_blocks + c] = mx[mt][e] * p.scale_idx;
+                }
             }
-        store(c, mx);
     }
-    // blocks of the share that no row of the tile sees
-    const int from = max(c_lo, c_lo + n);
-    for (int m = warp; m < pairs; m += kConsumers) {
-        if (!pair_ok(m) || row_req[pair_row(m)] != req) continue;
-        float *dst = scores + ((long long)pair_row(m) * p.Hkv + pair_head(m)) * p.max_blocks;
-        for (int c = from + lane; c < c_hi; c += 32) dst[c] = -INFINITY;
+    // the blocks past each row's own, a warp to a (row, group)
+    for (long long i = (long long)blockIdx.x * kConsumers + warp; i < (long long)p.T * p.Hkv; i += (long long)gridDim.x * kConsumers) {
+        const int tr = (int)(i / p.Hkv), req = row_req[tr], ps = row_pos[tr];
+        if (req < 0 || req >= p.R || ps < 0) continue;
+        float *dst = scores + i * p.max_blocks;
+        for (int c = min(ps / kPage + 1, p.max_blocks) + lane; c < p.max_blocks; c += 32) dst[c] = -INFINITY;
     }
 }
 
@@ -209,12 +281,9 @@ cudaError_t launch_paged_block_scores(const PagedProblem &p, const bf16 *q_idx, 
     const int M = (long long)avg * p.Hkv > 16 ? 32 : 16;
     const int rows_per_tile = std::max(1, M / p.Hkv);
     const int head_tiles = (p.Hkv + M - 1) / M;
-    const long long tiles = (long long)p.T * head_tiles;
-    // shares of blocks: about eight CTAs to an SM if every row filled its table, eight pages at least
-    const long long busy = std::max<long long>(1, (p.T + rows_per_tile - 1) / rows_per_tile * (long long)head_tiles);
-    const long long want = std::max<long long>(1, 8LL * p.num_sms / busy);
-    const int per = (int)std::max<long long>(8, (p.max_blocks + want - 1) / want);
-    const dim3 grid((unsigned)tiles, (p.max_blocks + per - 1) / per);
+    // two CTAs to an SM, fewer where that leaves under two pages of a full table each
+    const long long most = 2LL * p.num_sms, rows = (long long)p.T * head_tiles;
+    const long long ctas = p.T <= kPrefixRows ? std::min(most, (rows * p.max_blocks + 1) / 2) : std::min(most, rows);
     CUtensorMap tm;
     cudaError_t e = make_tmap_bf16_3d(&tm, k_idx, p.d_idx, kPage, p.n_pages, p.d_idx * 2ull, (unsigned long long)kPage * p.d_idx * 2, 64, kPage);
     if (e != cudaSuccess) return e;
@@ -222,8 +291,8 @@ cudaError_t launch_paged_block_scores(const PagedProblem &p, const bf16 *q_idx, 
         constexpr int DI = decltype(dtag)::value, MT = decltype(mtag)::value, smem = ScoreSmem<DI>::BYTES;
         static std::atomic<unsigned long long> allowed{0};
         if ((e = allow_smem(scores_kernel<DI, MT>, smem, allowed)) != cudaSuccess) return e;
-        return launch_chained("paged_block_scores_kernel", scores_kernel<DI, MT>, grid, kThreads, smem, s, p, q_idx, tm, block_table,
-                              q_starts, row_req, row_pos, scores, rows_per_tile, head_tiles, per, st);
+        return launch_chained("paged_block_scores_kernel", scores_kernel<DI, MT>, dim3((unsigned)ctas), kThreads, smem, s, p, q_idx, tm, block_table,
+                              q_starts, row_req, row_pos, scores, rows_per_tile, head_tiles, st);
     };
     using std::integral_constant;
     if (p.d_idx == 128)
