@@ -492,9 +492,9 @@ def paged_workspace_size(shape: PagedShape, op: int) -> int:
 
 
 def new_paged_workspace(shape: PagedShape, op: int, device=None) -> torch.Tensor:
-    """A workspace of a paged call, its 256-byte status word zeroed."""
+    """A workspace of a paged call, its first 4,096 bytes (status word, arrival counts) zeroed."""
     ws = torch.empty(paged_workspace_size(shape, op), dtype=torch.uint8, device=device or "cuda")
-    ws[:256].zero_()
+    ws[:4096].zero_()
     return ws
 
 

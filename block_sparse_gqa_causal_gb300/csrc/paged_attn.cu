@@ -39,9 +39,10 @@
 // holds.  So every CTA reads the same number of pages whatever the rows'
 // lengths, and a producer warp streams the stretch through one ring of stages
 // (K and V tiles of a page and head, contiguous and swizzled by TMA) without a
-// pause where a row ends and the next begins.  A stretch ends inside a row at
-// most twice; those pieces' states go to the workspace, and a second kernel
-// joins each cut row's pieces in order.
+// pause where a row ends and the next begins.  A stretch cuts at most two
+// rows; those pieces' states go to the workspace, and the CTA that ends the
+// last piece of a row joins them, in their order along the row.  (A second
+// kernel for that took 6 us more a call.)
 #include <algorithm>
 #include <type_traits>
 
@@ -59,7 +60,8 @@ constexpr int kStages = 3;
 
 constexpr int kPrefixRows = 512;                // most rows whose blocks are cut evenly; above, whole rows are dealt out
 constexpr int kMinBlocks = 2;                   // a stretch has at least this many blocks
-constexpr int kWholeBlocks = 8;                 // rows of up to so many blocks are not cut: joining costs what it would save
+constexpr int kArrivedWords = (4096 - kStatusBytes) / 4;   // the workspace's counts, one to a stretch
+constexpr int kWholeBlocks = 4;                 // rows of up to so many blocks are not cut
 
 enum { kFirst = 1, kLast = 2, kEnd = 4 };       // of a piece; of the CTA's stretch
 struct Meta {
@@ -69,6 +71,7 @@ struct Meta {
     int flags;
     int t, r;       // the piece's row and group
     int part;       // the piece's place among the partial states; -1: a whole row
+    int first, n;   // a cut row's first stretch and the number of its pieces
 };
 
 template <int D>
@@ -129,11 +132,6 @@ __device__ __forceinline__ void split4(float x0, float x1, float x2, float x3, u
     lo = e4m3x2(16.f * (x0 - f01.x), 16.f * (x1 - f01.y)) | (e4m3x2(16.f * (x2 - f23.x), 16.f * (x3 - f23.y)) << 16);
 }
 
-// A cut row: its (row, group) and the CTAs that hold its pieces.
-struct CutRow {
-    int pair, first, last, pad;
-};
-
 MSA_DEV void mbar_expect_tx(uint64_t *bar, uint32_t bytes)
 {
     asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
@@ -152,7 +150,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
             const float *__restrict__ v_scale, const int32_t *__restrict__ block_table,
             const int32_t *__restrict__ row_req, const int32_t *__restrict__ row_pos, const int32_t *__restrict__ sel,
             bf16 *__restrict__ o, float *__restrict__ lse, float *__restrict__ part_o, float2 *__restrict__ part_ml,
-            CutRow *__restrict__ cut, DeviceStatus *st)
+            unsigned *__restrict__ arrived, DeviceStatus *st)
 {
     using S = AttnSmem<D>;
     extern __shared__ uint8_t raw[];
@@ -161,11 +159,11 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
     __shared__ Meta meta[kStages];
     __shared__ float sM[kWarps][8], sL[kWarps][8];
     __shared__ long long before[kPrefixRows + 1];   // blocks of the rows before each row, one group
-    __shared__ int abort_flag;
+    __shared__ int abort_flag, joins;
 
     chain_next();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = p.G;
-    const bool even = cut != nullptr;           // stretches of equal length; else whole rows are dealt out
+    const bool even = arrived != nullptr;         // stretches of equal length; else whole rows are dealt out
 
     // blocks that a group of row t has to look at; 0: not a row (entries of a selection may sit in any of its slots)
     auto blocks_of = [&](int t, int &req, int &pos) {
@@ -242,7 +240,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
             ++step;
         };
         // blocks (a selection: slots) j0 .. j1 - 1 of group r of row t
-        auto piece = [&](int t, int r, int req, int pos, int j0, int j1, int part) {
+        auto piece = [&](int t, int r, int req, int pos, int j0, int j1, int part, int first_cut, int n_cut) {
             const int c0 = pos / kPage;
             for (int base = j0; base < j1 && live; base += 32) {
                 int c = -1;
@@ -296,6 +294,8 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                     m.t = t;
                     m.r = r;
                     m.part = part;
+                    m.first = first_cut;
+                    m.n = n_cut;
                     first = false;
                     publish(m);
                 }
@@ -303,12 +303,12 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
             }
         };
         const int me = blockIdx.x;
-        CutRow row{-1, 0, 0, 0};
         if (even) {
             const long long W = before[p.T] * p.Hkv;
             const long long n = max(1LL, min((long long)gridDim.x, W / kMinBlocks));
             long long x = me < n ? W * me / n : 0;
             const long long x1 = me < n ? W * (me + 1) / n : 0;
+            auto holder = [&](long long y) { return (int)(((y + 1) * n + W - 1) / W - 1); };   // the stretch that has block y
             int t = 0;
             if (x < x1) {                              // the last row that starts at or before x
                 int hi = p.T;
@@ -327,20 +327,16 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                 }
                 const int r = (int)(y / nt), j0 = (int)(y % nt), j1 = (int)min((long long)nt, j0 + (x1 - x));
                 const bool whole = j0 == 0 && j1 == nt;
-                if (!whole && j0 == 0) {
-                    const long long end = x + nt;      // the last piece is with the CTA that has block end - 1
-                    row = CutRow{t * p.Hkv + r, me, (int)((end * n + W - 1) / W - 1), 0};
-                }
-                piece(t, r, row_req[t], row_pos[t], j0, j1, whole ? -1 : 2 * me + (j0 > 0 ? 0 : 1));
+                const int f = whole ? 0 : holder(x - j0), last = whole ? 0 : holder(x - j0 + nt - 1);
+                piece(t, r, row_req[t], row_pos[t], j0, j1, whole ? -1 : 2 * me + (j0 > 0 ? 0 : 1), f, last - f + 1);
                 x += j1 - j0;
             }
-            if (lane == 0) cut[me] = row;
         } else {
             const long long pairs = (long long)p.T * p.Hkv;
             for (long long i = me; i < pairs && live; i += gridDim.x) {
                 int req, pos;
                 const int t = (int)(i / p.Hkv), nt = blocks_of(t, req, pos);
-                if (nt) piece(t, (int)(i % p.Hkv), req, pos, 0, nt, -1);
+                if (nt) piece(t, (int)(i % p.Hkv), req, pos, 0, nt, -1, 0, 0);
             }
         }
         const int copied = step;
@@ -529,66 +525,56 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
             if (whole) *reinterpret_cast<uint2 *>(o + row * D + idx) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
             else *reinterpret_cast<float4 *>(part_o + (long long)me.part * 8 * D + idx) = v;
         }
+        if (!whole) __threadfence();                   // the state before the arrival
         fence_proxy_async();                           // the stage goes back to the copies
         named_bar_sync(1, 32 * kWarps);                // sM and sL are free again, too
         if (lane == 0) mbar_arrive(&empty[s]);
-    }
-}
+        if (whole) continue;
 
-// Joins the pieces of the row that CTA blockIdx.x of the main kernel cut off,
-// in order; a warp to a head.
-template <int D>
-__global__ void __launch_bounds__(256)
-join_kernel(PagedProblem p, const CutRow *__restrict__ cut, const float *__restrict__ part_o,
-            const float2 *__restrict__ part_ml, bf16 *__restrict__ o, float *__restrict__ lse)
-{
-    chain_next();
-    chain_wait();
-    const CutRow c = cut[blockIdx.x];
-    const int h = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (c.pair < 0 || h >= p.G) return;
-    const int n = c.last - c.first + 1;
-    auto part = [&](int i) { return 2 * (c.first + i) + (i == 0 ? 1 : 0); };
-    constexpr int PER = D / 32, U = 4;                 // pieces whose loads are in flight together
-    float M = -INFINITY, L = 0.f, acc[PER];
+        // the last arrival of a cut row joins its pieces (and leaves the count at zero)
+        if (tid == 0) joins = atomicInc(&arrived[me.first], me.n - 1) == (unsigned)(me.n - 1);
+        named_bar_sync(1, 32 * kWarps);
+        if (!joins) continue;
+        __threadfence();
+        for (int idx = tid * 4; idx < G * D; idx += 32 * kWarps * 4) {
+            constexpr int U = 4;                       // pieces whose loads are in flight together
+            const int h = idx / D;
+            float Mj = -INFINITY, Lj = 0.f;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i0 = 0; i0 < me.n; i0 += U) {
+                float2 ml[U];
+                float4 v[U];
 #pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-    for (int i0 = 0; i0 < n; i0 += U) {
-        float2 ml[U];
-        float x[U][PER];
+                for (int u = 0; u < U; ++u) {
+                    const int i = min(i0 + u, me.n - 1);
+                    const long long part = 2 * (me.first + i) + (i == 0 ? 1 : 0);
+                    ml[u] = __ldcg(part_ml + part * 8 + h);
+                    v[u] = __ldcg(reinterpret_cast<const float4 *>(part_o + part * 8 * D + idx));
+                }
+                float m = Mj;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = min(i0 + u, n - 1);
-            ml[u] = part_ml[part(i) * 8 + h];
+                for (int u = 0; u < U; ++u) m = fmaxf(m, ml[u].x);
+                const float keep = Mj == -INFINITY ? 1.f : exp2f(Mj - m);
+                Mj = m;
+                Lj *= keep;
+                x = make_float4(x.x * keep, x.y * keep, x.z * keep, x.w * keep);
 #pragma unroll
-            for (int e = 0; e < PER; ++e) x[u][e] = part_o[((long long)part(i) * 8 + h) * D + lane + 32 * e];
-        }
-        float m = M;
-#pragma unroll
-        for (int u = 0; u < U; ++u) m = fmaxf(m, ml[u].x);
-        const float keep = M == -INFINITY ? 1.f : exp2f(M - m);   // an empty state is all zeros, one of NaN scores NaN
-        L *= keep;
-#pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] *= keep;
-        M = m;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (i0 + u >= n) break;
-            const float f = ml[u].x == -INFINITY ? 1.f : exp2f(ml[u].x - M);
-            L += f * ml[u].y;
-#pragma unroll
-            for (int e = 0; e < PER; ++e) acc[e] += f * x[u][e];
+                for (int u = 0; u < U; ++u) {
+                    if (i0 + u >= me.n) break;
+                    const float w = ml[u].x == -INFINITY ? 1.f : exp2f(ml[u].x - Mj);
+                    Lj += w * ml[u].y;
+                    x = make_float4(fmaf(w, v[u].x, x.x), fmaf(w, v[u].y, x.y), fmaf(w, v[u].z, x.z), fmaf(w, v[u].w, x.w));
+                }
+            }
+            const float inv = Lj == 0.f ? 0.f : 1.f / Lj;
+            *reinterpret_cast<uint2 *>(o + row * D + idx) = make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
+            if (idx % D == 0) lse[row + h] = (Mj + log2f(Lj)) * kLn2;
         }
     }
-    const long long row = (long long)(c.pair / p.Hkv) * p.Hq + (long long)(c.pair % p.Hkv) * p.G + h;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) o[row * D + lane + 32 * e] = __float2bfloat16_rn(L == 0.f ? 0.f : acc[e] / L);
-    if (lane == 0) lse[row] = (M + log2f(L)) * kLn2;
 }
 
 // Whether rows are cut into equal stretches.  Not with many rows (the list is
-// summed up by every CTA) or short ones: at one row of two groups and eight
-// blocks, the whole rows take 17 us a call and cut ones with their join 21.
+// summed up by every CTA) or short ones, where joining costs what cutting saves.
 bool cuts_rows(const PagedProblem &p, bool sparse)
 {
     return p.T <= kPrefixRows && (sparse ? p.topk : p.max_blocks) > kWholeBlocks;
@@ -596,7 +582,7 @@ bool cuts_rows(const PagedProblem &p, bool sparse)
 // Two CTAs to an SM, fewer where that leaves stretches under kMinBlocks.
 int attn_ctas(const PagedProblem &p, bool sparse)
 {
-    const long long rows = (long long)p.T * p.Hkv, most = 2LL * p.num_sms;
+    const long long rows = (long long)p.T * p.Hkv, most = std::min(2 * p.num_sms, kArrivedWords);
     return (int)std::min(most, cuts_rows(p, sparse) ? rows * (sparse ? p.topk : p.max_blocks) / kMinBlocks : rows);
 }
 
@@ -605,7 +591,7 @@ int attn_ctas(const PagedProblem &p, bool sparse)
 size_t paged_attn_scratch_floats(const PagedProblem &p)
 {
     if (!cuts_rows(p, true) && !cuts_rows(p, false)) return 0;
-    return (size_t)2 * p.num_sms * (2 * 8 * (p.d + 2) + sizeof(CutRow) / 4);
+    return kArrivedWords + (size_t)2 * p.num_sms * 2 * 8 * (p.d + 2);
 }
 
 cudaError_t launch_paged_attn(const PagedProblem &p, const bf16 *q, const uint8_t *k8, const uint8_t *v8,
@@ -614,9 +600,9 @@ cudaError_t launch_paged_attn(const PagedProblem &p, const bf16 *q, const uint8_
                               float *scratch, DeviceStatus *st, cudaStream_t s)
 {
     const int ctas = attn_ctas(p, sel != nullptr);
-    const bool cuts = cuts_rows(p, sel != nullptr);
-    CutRow *cut = cuts ? reinterpret_cast<CutRow *>(scratch) : nullptr;
-    float *part_o = scratch + (size_t)2 * p.num_sms * sizeof(CutRow) / 4;
+    // one count per stretch, zero between calls, then the partial outputs and (reference, sum) pairs
+    unsigned *arrived = cuts_rows(p, sel != nullptr) ? reinterpret_cast<unsigned *>(scratch) : nullptr;
+    float *part_o = scratch + kArrivedWords;
     float2 *part_ml = reinterpret_cast<float2 *>(part_o + (size_t)2 * p.num_sms * 2 * 8 * p.d);
     CUtensorMap tk, tv;
     cudaError_t e = make_tmap_u8_3d(&tk, k8, p.d, kPage, (unsigned long long)p.n_pages * p.Hkv, p.d, 32);
@@ -626,11 +612,8 @@ cudaError_t launch_paged_attn(const PagedProblem &p, const bf16 *q, const uint8_
         constexpr int D = decltype(dtag)::value;
         static std::atomic<unsigned long long> allowed{0};
         if ((e = allow_smem(attn_kernel<D>, AttnSmem<D>::BYTES, allowed)) != cudaSuccess) return e;
-        e = launch_chained("paged_attn_kernel", attn_kernel<D>, dim3(ctas), kThreads, AttnSmem<D>::BYTES, s, p, q, tk, tv, k_scale,
-                           v_scale, block_table, row_req, row_pos, sel, o, lse, part_o, part_ml, cut, st);
-        if (e != cudaSuccess || !cuts) return e;
-        return launch_chained("paged_attn_join_kernel", join_kernel<D>, dim3(ctas), 256, 0, s, p, (const CutRow *)cut,
-                              (const float *)part_o, (const float2 *)part_ml, o, lse);
+        return launch_chained("paged_attn_kernel", attn_kernel<D>, dim3(ctas), kThreads, AttnSmem<D>::BYTES, s, p, q, tk, tv,
+                              k_scale, v_scale, block_table, row_req, row_pos, sel, o, lse, part_o, part_ml, arrived, st);
     };
     return p.d == 128 ? run(std::integral_constant<int, 128>{}) : run(std::integral_constant<int, 64>{});
 }

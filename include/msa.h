@@ -355,7 +355,9 @@ msa_status msa_kv_append(const msa_shape *shape, const void *k_new, const void *
  * {1, 2, 4, 8}; topk <= 32; max_blocks, n_pages <= 2^23; R <= 2^24; Hkv <=
  * 32768; n_pages * Hkv < 2^31; T * Hq < 2^24.  16-byte alignment of the bf16
  * and code arrays, 4-byte of the others.  Every call takes a workspace of
- * msa_paged_workspace_size bytes with the status word of the other calls.
+ * msa_paged_workspace_size bytes with the status word of the other calls; its
+ * first 4,096 bytes (all of a smaller one) have to be zero before the first
+ * call on it, and again after msa_check_device_status() reported a timeout.
  * What device memory says (lengths, pages, selections) is checked on the
  * device: an entry out of range is left out and recorded in the status word.
  */

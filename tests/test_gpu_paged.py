@@ -230,7 +230,8 @@ def test_append_leaves_out_bad_segments(api):
 # ------------------------------------------------------------------ block scores and selection
 @pytest.mark.parametrize("Hkv,di,lens,q,pad", [
     (2, 64, [1], [1], 0), (8, 128, [128, 129, 127, 1000, 1, 256], [1] * 6, 2), (4, 128, [500, 700, 40], [3, 17, 40], 5),
-    (1, 64, [4000, 130], [100, 130], 0), (40, 128, [300, 260], [2, 1], 1), (5, 64, [777], [11], 0), (8, 64, [5000], [1], 0)])
+    (1, 64, [4000, 130], [100, 130], 0), (40, 128, [300, 260], [2, 1], 1), (5, 64, [777], [11], 0), (8, 64, [5000], [1], 0),
+    (2, 64, [900, 700, 1], [300, 300, 1], 2)])
 def test_block_scores(api, Hkv, di, lens, q, pad):
     import torch
     rng = np.random.default_rng(sum(lens) + Hkv)
@@ -366,11 +367,12 @@ def attn_case(api, lens, q, Hq, Hkv, d, k, sparse, pad=0, gain=1.0, scale=0.0, q
 def check_attn(api, sh, args, sel, r, n):
     import torch
     ws = api.new_paged_workspace(sh, api.OP_PAGED_ATTN)
-    ws[256:].fill_(0xFF)
+    ws[4096:].fill_(0xFF)
     o = torch.full((sh.T, sh.Hq, sh.d), 3.0, dtype=torch.bfloat16, device="cuda")
     lse = torch.full((sh.T, sh.Hq), 3.0, device="cuda")
     api.paged_attn(sh, *args, sel_idx=None if sel is None else i32(sel), o=o, lse=lse, workspace=ws)
     status_ok(api, ws)
+    assert not ws[:4096].any()                                      # as the next call needs them
     ow, lw, do, dl = ref.attn(*r)
     og, lg = o.double().cpu().numpy(), lse.double().cpu().numpy()
     assert np.all(og[n:] == 3.0) and np.all(lg[n:] == 3.0)          # rows behind the last request
@@ -386,7 +388,10 @@ CASES = [
     dict(lens=[1], q=[1], Hq=2, Hkv=2, d=64, k=4), dict(lens=[127, 128, 129, 31, 33, 2], q=[1] * 6, Hq=8, Hkv=1, d=128, k=4, pad=2),
     dict(lens=[1000, 5, 640, 2049], q=[1, 1, 1, 1], Hq=16, Hkv=4, d=128, k=8), dict(lens=[900, 300], q=[5, 130], Hq=8, Hkv=2, d=64, k=4, pad=3),
     dict(lens=[6000], q=[1], Hq=8, Hkv=8, d=128, k=16), dict(lens=[5000, 4097], q=[2, 1], Hq=8, Hkv=4, d=64, k=32),
-    dict(lens=[300], q=[1], Hq=8, Hkv=1, d=64, k=1, max_blocks=50), dict(lens=[3000, 100, 7], q=[1, 1, 1], Hq=64, Hkv=8, d=128, k=16, max_blocks=200)]
+    dict(lens=[300], q=[1], Hq=8, Hkv=1, d=64, k=1, max_blocks=50),
+    dict(lens=[2100 + 37 * i for i in range(40)], q=[1] * 40, Hq=16, Hkv=8, d=64, k=16, max_blocks=40),       # rows of several CTAs, CTAs of several rows
+    dict(lens=[400, 330], q=[300, 310], Hq=2, Hkv=1, d=64, k=2, pad=7),                                   # more rows than are cut
+    dict(lens=[3000, 100, 7], q=[1, 1, 1], Hq=64, Hkv=8, d=128, k=16, max_blocks=200)]
 
 
 @pytest.mark.parametrize("case", range(len(CASES)))
