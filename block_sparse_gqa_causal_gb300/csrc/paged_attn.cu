@@ -8,41 +8,36 @@
 // Decoding reads every selected page once for the G <= 8 heads of a group, so
 // the pages' bytes bound it; what has to be kept away is the conversion of
 // each code to 16 bits.  The codes therefore go to the tensor cores as they
-// are (e4m3 x e4m3, fp32 sums).  A 16-row MMA tile has room for twice the
-// group's heads, so the other operand is split in two e4m3 terms: rows 0-7
-// hold the heads' leading terms hi = rn(x), rows 8-15 lo = rn(16 (x - hi)),
-// and hi + lo / 16 carries the 8 significant bits of a bf16 query exactly,
-// down to 2^-23 of the row's largest feature (rows are scaled by a power of
-// two to fill the range), and the probabilities with the precision that bf16
-// gives them.  Sums, maxima and the outputs are fp32.
+// are (tcgen05, e4m3 x e4m3, fp32 sums in TMEM), tokens or features as the 128
+// rows of a product and the heads as its 16 columns:
+//   S [token][16] = K [token][d] Q~ [16][d]^T,  O [feature][16] += V [token][feature]^T P~ [16][token]^T.
+// Sixteen columns are twice the heads, so the other operand is split in two
+// e4m3 terms: columns 0-7 hold the heads' leading terms hi = rn(x), columns
+// 8-15 lo = rn(16 (x - hi)), and hi + lo / 16 carries the 8 significant bits
+// of a bf16 query exactly, down to 2^-23 of the row's largest feature (queries
+// are scaled by a power of two to fill the range), and the probabilities with
+// the precision that bf16 gives them.  (mma.sync takes e4m3 too, but the
+// compiler turns each into two 16-bit MMAs and conversions: 800 instructions a
+// warp and page, which held the pages back.)
 //
 // With t_j = l_j log2 e + log2 vs, the weight of token j's codes is 2^t_j and
-// that of the sum 2^t_j / vs, so one reference m bounds both and the products
-// P V add up in the MMA's own accumulators across pages of different scales.
-// m is the largest t so far, or up to 4 less: P = 16 * 2^(t - m) stays within
-// 256 and the accumulators are only rescaled when t has outgrown m by more
-// than that, which after a row's first pages is rare.  (Rescaling on every
-// new maximum and joining each page's product in fp32 cost 830 instructions a
-// warp and page instead of 300, and made them the bound: 55 us against 45 at
-// 64 rows x 8 groups x 16 pages.)  P's small terms are off by at most 2^-18
+// that of the sum 2^t_j / vs, so one reference m per head bounds both and the
+// products P V add up in TMEM across pages of different scales.  m is the
+// largest t so far, or up to 4 less: P = 16 * 2^(t - m) stays within 256 and
+// the sums are only rescaled when t has outgrown m by more than that, which
+// after a row's first page is rare.  P's small terms are off by at most 2^-18
 // of the largest weight.
-//
-// Each of four warps takes 32 of a page's 128 tokens and keeps its own running
-// maximum, sum and output; they are joined where a row ends.  V's operand
-// needs its tokens along a register: ldmatrix with 8-bit transposition gives
-// that from the row-major tile.  The tokens' order inside a 32-token step is
-// chosen so that a lane's scores are the probabilities it has to feed back and
-// no shared-memory phase has a bank conflict.
 //
 // The work is one long list of blocks, those of (row 0, group 0), then (row 0,
 // group 1) and so on, cut into equal stretches for the two CTAs that each SM
-// holds.  So every CTA reads the same number of pages whatever the rows'
-// lengths, and a producer warp streams the stretch through one ring of stages
-// (K and V tiles of a page and head, contiguous and swizzled by TMA) without a
-// pause where a row ends and the next begins.  A stretch cuts at most two
-// rows; those pieces' states go to the workspace, and the CTA that ends the
-// last piece of a row joins them, in their order along the row.  (A second
-// kernel for that took 6 us more a call.)
+// holds, whatever the rows' lengths.  A producer warp streams the stretch
+// through one ring of stages (K and V tiles of a page and head, contiguous and
+// swizzled by TMA) without a pause where a row ends and the next begins, and
+// lays down each row's queries; one warp issues the MMAs, the next page's S
+// before this page's P V; four warps, a token to a thread, turn scores into
+// probabilities.  A stretch cuts at most two rows; those pieces' states go to
+// the workspace, and the CTA that ends the last piece of a row joins them, in
+// their order along the row.
 #include <algorithm>
 #include <type_traits>
 
@@ -54,11 +49,12 @@ namespace {
 
 using namespace tc;
 
-constexpr int kWarps = 4;                       // consumer warps, 32 tokens of a page each
-constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kWarps = 4;                       // softmax warps, a token of the page to a thread
+constexpr int kThreads = 32 * (kWarps + 2);     // then the producer and the MMA warp
 constexpr int kStages = 3;
-
-constexpr int kPrefixRows = 512;                // most rows whose blocks are cut evenly; above, whole rows are dealt out
+constexpr int kQueries = kStages + 1;           // rows whose queries are held: one more than steps in flight
+constexpr int kColumns = 64;                    // TMEM: two S buffers and O, 16 columns each
+constexpr int kPrefixRows = 384;                // most rows whose blocks are cut evenly; above, whole rows are dealt out
 constexpr int kMinBlocks = 2;                   // a stretch has at least this many blocks
 constexpr int kArrivedWords = (4096 - kStatusBytes) / 4;   // the workspace's counts, one to a stretch
 constexpr int kWholeBlocks = 4;                 // rows of up to so many blocks are not cut
@@ -69,7 +65,7 @@ struct Meta {
     float ks;       // the page's K scale for this head
     float lv, pv;   // log2 of its V scale (-100 at least), and 16 x what that leaves of the scale (1)
     int flags;
-    int t, r;       // the piece's row and group
+    int t, r, q;    // the piece's row and group, and where its queries lie
     int part;       // the piece's place among the partial states; -1: a whole row
     int first, n;   // a cut row's first stretch and the number of its pieces
 };
@@ -78,37 +74,56 @@ template <int D>
 struct AttnSmem {
     static constexpr int TILE = kPage * D;      // K or V codes of a page and head
     static constexpr int STAGE = 2 * TILE;
-    static constexpr int Q = 8 * D * 2;         // the group's queries, with a piece's first block
+    static constexpr int Q = 16 * D;            // a row's queries: hi and lo terms of 8 heads
+    static constexpr int P = 16 * kPage;        // a page's probabilities
     static constexpr int OFF_Q = kStages * STAGE;
-    static constexpr int BYTES = OFF_Q + kStages * Q + 1024;   // + alignment
-    static constexpr int OROW = D + 8;          // a warp's output row: 8 more keeps the rows on different banks
-    static_assert(kWarps * 8 * OROW * 4 <= STAGE, "the warps' outputs fit a stage");
+    static constexpr int OFF_P = OFF_Q + kQueries * Q;
+    static constexpr int BYTES = OFF_P + 2 * P + 1024;   // + alignment
 };
 
-// byte offset of 16-byte word w of token row r in a TMA-swizzled tile
+// byte offset of 16-byte word w of row r in a tile of D-byte rows, swizzled as TMA and the MMA descriptors do
 template <int D>
 __device__ __forceinline__ int at(int r, int w)
 {
     return D == 128 ? r * 128 + ((w ^ (r & 7)) << 4) : r * 64 + ((w ^ ((r >> 1) & 3)) << 4);
 }
 
-// D(16x8, f32) += A(16x32, e4m3, row) * B(32x8, e4m3, col)
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+// Shared-memory matrix descriptor of a tile of D-byte rows (128- or 64-byte
+// swizzle).  K-major (rows are M or N): 8-row groups `group` bytes apart.
+// MN-major (rows are K, D consecutive M elements each): the same, and `atom`
+// bytes from one D of M to the next.
+template <int D>
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t group, uint32_t atom)
+{
+    uint64_t d = (uint64_t)((addr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(atom >> 4) << 16;
+    d |= (uint64_t)(group >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)(D == 128 ? 2 : 4) << 61;
+    return d;
+}
+// instruction descriptor of kind::f8f6f4: e4m3 x e4m3, fp32 sums, 128 x 16
+constexpr uint32_t kIdesc = (1u << 4) | ((16u >> 3) << 17) | ((128u >> 4) << 24);
+
+// D[tmem] (+)= A[smem] * B[smem]^T over 32 bytes of K, issued by one thread.
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
 {
     asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate));
 }
 
-// Two 16x16 byte matrices, transposed: lane l gives the address of row l % 16
-// of matrix l / 16; it gets, for columns l/4 and l/4 + 8, rows 4(l%4)..+3 of
-// the first matrix (r0, r1) and of the second (r2, r3).
-__device__ __forceinline__ void ldsm_b8_t(uint32_t (&r)[4], const void *p)
+// Barrier 1 over the softmax warps; whether any thread brought `x`.
+__device__ __forceinline__ bool any_of(bool x)
 {
-    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];\n"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(smem_u32(p)));
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"((uint32_t)x), "n"(32 * kWarps)
+        : "memory");
+    return r != 0;
 }
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
@@ -136,13 +151,6 @@ MSA_DEV void mbar_expect_tx(uint64_t *bar, uint32_t bytes)
 {
     asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
-MSA_DEV void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2)
 attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ CUtensorMap tm_k,
@@ -153,11 +161,13 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
             unsigned *__restrict__ arrived, DeviceStatus *st)
 {
     using S = AttnSmem<D>;
-    extern __shared__ uint8_t raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-    __shared__ uint64_t full[kStages], empty[kStages];
+    extern __shared__ __align__(1024) uint8_t raw[];
+    uint8_t *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);   // keeps shared addressing
+    __shared__ uint64_t full[kStages], empty[kStages], s_full[2], p_full[2], pv_done[2], drained;
     __shared__ Meta meta[kStages];
+    __shared__ float sQ[kQueries][8];           // logit factor of each head's queries, times log2 e
     __shared__ float sM[kWarps][8], sL[kWarps][8];
+    __shared__ uint32_t tmem_slot;
     __shared__ long long before[kPrefixRows + 1];   // blocks of the rows before each row, one group
     __shared__ int abort_flag, joins;
 
@@ -180,9 +190,19 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
         abort_flag = 0;
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], kWarps);
+            mbar_init(&empty[i], 1);
         }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], kWarps);
+            mbar_init(&pv_done[i], 1);
+        }
+        mbar_init(&drained, 1);
         fence_mbar_init();
+    }
+    if (warp == kWarps + 1) {
+        tmem_alloc(&tmem_slot, kColumns);
+        tmem_relinquish();
     }
     chain_wait();
     if (even)
@@ -206,14 +226,50 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
         }
         if (lane == 0) before[p.T] = sum;
     }
+    fence_before_sync();
     __syncthreads();
+    fence_after_sync();
+    const uint32_t tmem = tmem_slot;
 
     if (warp == kWarps) {
-        int step = 0;
+        int step = 0, pieces = 0;
         bool live = true;
+        uint4 x[D / 32];                               // a quarter of head lane / 4's query row
+        auto load_q = [&](int t, int r) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(q + ((long long)t * p.Hq + (long long)r * G + lane / 4) * D + lane % 4 * (D / 4));
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) x[i] = lane / 4 < G ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+        };
+        // ... as hi and lo terms, once no step in flight reads the place any more
+        auto lay_q = [&](int qi) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+                top = __vmaxu2(__vmaxu2(top, __vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu)),
+                               __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu));
+            top = max(top & 0xFFFFu, top >> 16);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // not finite: NaN, and so are the scores
+            const float sq = __uint_as_float(top >= 0x7F80u ? 0x7FC00000u : pow2_scale_bits(top)), inv = 1.f / sq;
+            uint8_t *dst = smem + S::OFF_Q + qi * S::Q;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const float2 a = unpack_bf16(x[i].x), b = unpack_bf16(x[i].y), c = unpack_bf16(x[i].z), d = unpack_bf16(x[i].w);
+                uint2 hi, lo;
+                split4(a.x * inv, a.y * inv, b.x * inv, b.y * inv, hi.x, lo.x);
+                split4(c.x * inv, c.y * inv, d.x * inv, d.y * inv, hi.y, lo.y);
+                const int f = lane % 4 * (D / 4) + 8 * i;
+                *reinterpret_cast<uint2 *>(dst + at<D>(lane / 4, f >> 4) + (f & 15)) = hi;
+                *reinterpret_cast<uint2 *>(dst + at<D>(8 + lane / 4, f >> 4) + (f & 15)) = lo;
+            }
+            if (lane % 4 == 0) sQ[qi][lane / 4] = sq * (p.scale * kLog2e);
+            fence_proxy_async();
+            __syncwarp();
+        };
         // Waits for the next stage and starts its copies.  The arrival that completes the phase comes with the
         // block's Meta, so that the copies do not wait for the scales.
-        auto start = [&](int page, int t, int r, int len, bool first) {
+        auto start = [&](int page, int r, int len) {
             const int s = step % kStages;
             if (step >= kStages && !mbar_wait_warp(&empty[s], (step / kStages - 1) & 1, st, 144, &abort_flag)) {
                 live = false;
@@ -221,9 +277,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
             }
             if (lane == 0) {
                 const int boxes = (len + 31) / 32;             // 32-token boxes, none past the row
-                const uint32_t qb = first ? G * D * 2 : 0;
-                mbar_expect_tx(&full[s], boxes * 64 * D + qb);
-                if (first) bulk_load(smem + S::OFF_Q + s * S::Q, q + ((long long)t * p.Hq + (long long)r * G) * D, qb, &full[s]);
+                if (boxes) mbar_expect_tx(&full[s], boxes * 64 * D);
                 uint8_t *dst = smem + s * S::STAGE;
                 for (int x = 0; x < boxes; ++x)
                     tma_load_3d(dst + x * 32 * D, &tm_k, &full[s], 0, x * 32, page * p.Hkv + r);
@@ -241,7 +295,8 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
         };
         // blocks (a selection: slots) j0 .. j1 - 1 of group r of row t
         auto piece = [&](int t, int r, int req, int pos, int j0, int j1, int part, int first_cut, int n_cut) {
-            const int c0 = pos / kPage;
+            const int c0 = pos / kPage, qi = pieces++ % kQueries;
+            load_q(t, r);
             for (int base = j0; base < j1 && live; base += 32) {
                 int c = -1;
                 if (sel) {
@@ -282,8 +337,9 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                     const int l = __ffs(todo) - 1;
                     todo &= todo - 1;
                     const int blen = __shfl_sync(0xffffffffu, len, l);
-                    start(__shfl_sync(0xffffffffu, page, l), t, r, blen, first);
+                    start(__shfl_sync(0xffffffffu, page, l), r, blen);
                     if (!live) break;
+                    if (first) lay_q(qi);
                     Meta m;
                     m.len = blen;
                     m.ks = __shfl_sync(0xffffffffu, ks, l);
@@ -293,6 +349,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                     m.flags = (first ? kFirst : 0) | (!todo && (sel || base + 32 >= j1) ? kLast : 0);
                     m.t = t;
                     m.r = r;
+                    m.q = qi;
                     m.part = part;
                     m.first = first_cut;
                     m.n = n_cut;
@@ -353,224 +410,232 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
         }
         // stay until the last copies have landed (the stage of the end mark has been read)
         for (int k = max(0, step - kStages); k < copied; ++k) mbar_wait_warp(&full[k % kStages], (k / kStages) & 1, st, 145, nullptr);
-        return;
-    }
-
-    const int g = lane >> 2, t4 = lane & 3;
-    float acc[D / 8][4];                               // head g, features 8n + 2 t4, + 1: the hi rows' sums, then the lo rows'
-    float m_run = -INFINITY, l_run = 0.f, sql = 0.f;   // reference of head g; this lane's share of its sum
-    uint32_t a[D / 32][4];                             // the queries' terms, features 32 ks + 4 t4 .. + 3 and + 16 ..
-    const int kw = warp * 32;                          // this warp's first token of a page
-    // K rows: token column j of score tile n is token 8n + (j ^ 4 (n & 1))
-    const int kj = lane & 7, km = lane >> 3;
-    // V rows: probability k (of 16) is lane (k / 4)'s value e = k & 1 of tile (k / 2) & 1
-    const int vk = lane & 15, vn = (vk >> 1) & 1;
-    const int vrow = kw + 16 * (lane >> 4) + 8 * vn + ((2 * (vk >> 2) + (vk & 1)) ^ (4 * vn));
-#pragma unroll
-    for (int n = 0; n < D / 8; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < D / 32; ++ks) a[ks][0] = a[ks][1] = a[ks][2] = a[ks][3] = 0u;
-
-    for (int step = 0;; ++step) {
-        const int s = step % kStages;
-        if (!mbar_wait_warp(&full[s], (step / kStages) & 1, st, 146, &abort_flag)) return;
-        const Meta me = meta[s];
-        if (me.flags & kEnd) return;
-        if (me.flags & kFirst) {
-            const bool ok = g < G;
-            const uint2 *src = reinterpret_cast<const uint2 *>(smem + S::OFF_Q + s * S::Q + (ok ? g : 0) * D * 2);
-            uint2 x[D / 32][2];
-            uint32_t top = 0;
-#pragma unroll
-            for (int ks = 0; ks < D / 32; ++ks)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    x[ks][e] = ok ? src[ks * 8 + e * 4 + t4] : make_uint2(0u, 0u);
-                    top = __vmaxu2(top, __vmaxu2(x[ks][e].x & 0x7FFF7FFFu, x[ks][e].y & 0x7FFF7FFFu));
-                }
-            top = max(top & 0xFFFFu, top >> 16);
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // not finite: NaN, and so are the scores
-            const float sq = __uint_as_float(top >= 0x7F80u ? 0x7FC00000u : pow2_scale_bits(top));
-            const float inv = 1.f / sq;
-#pragma unroll
-            for (int ks = 0; ks < D / 32; ++ks)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float2 u = unpack_bf16(x[ks][e].x), v = unpack_bf16(x[ks][e].y);
-                    split4(u.x * inv, u.y * inv, v.x * inv, v.y * inv, a[ks][2 * e], a[ks][2 * e + 1]);
-                }
-            sql = sq * (p.scale * kLog2e);
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-            m_run = -INFINITY;
-            l_run = 0.f;
-        }
-        if (kw < me.len) {
-            uint8_t *sk = smem + s * S::STAGE, *sv = sk + S::TILE;
-            if (me.len < kw + 32) {
-                // rows behind the last visible token: whatever they hold must not reach 0 * V
-                for (int x = lane; x < (kw + 32 - me.len) * (D / 16); x += 32)
-                    reinterpret_cast<uint4 *>(sv + me.len * D)[x] = make_uint4(0u, 0u, 0u, 0u);
-                fence_proxy_async();
-                __syncwarp();
+    } else if (warp == kWarps + 1) {
+        const uint32_t base = smem_u32(smem);
+        auto landed = [&](int i) { return __all_sync(0xffffffffu, mbar_test(&full[i % kStages], (i / kStages) & 1)); };
+        // step i's page has landed: its scores, or the end mark passed on
+        auto scores = [&](int i) {
+            const int s = i % kStages;
+            const Meta m = meta[s];
+            if (m.flags & kEnd) {
+                if (lane == 0) mbar_arrive(&s_full[i & 1]);
+                return false;
             }
-            float sc[4][2];
-            const float fac = sql * me.ks;
+            if (lane == 0) {
+                const uint64_t dk = tile_desc<D>(base + s * S::STAGE, 8 * D, 16), dq = tile_desc<D>(base + S::OFF_Q + m.q * S::Q, 8 * D, 16);
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                float c[4] = {0.f, 0.f, 0.f, 0.f};
-                const int row = kw + 8 * n + (kj ^ (4 * (n & 1)));
-#pragma unroll
-                for (int kp = 0; kp < D / 64; ++kp) {
-                    uint32_t b[4];
-                    ldsm_x4(b[0], b[1], b[2], b[3], sk + at<D>(row, 4 * kp + km));
-                    mma_e4m3(c, a[2 * kp], b[0], b[1]);
-                    mma_e4m3(c, a[2 * kp + 1], b[2], b[3]);
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) sc[n][e] = fmaf(fmaf(c[2 + e], 0.0625f, c[e]), fac, me.lv);
+                for (int k = 0; k < D / 32; ++k) mma_f8(tmem + (i & 1) * 16, desc_adv(dk, k * 32), desc_adv(dq, k * 32), kIdesc, k > 0);
+                mma_commit(&s_full[i & 1]);
             }
-            if (me.len < kw + 32) {
-#pragma unroll
-                for (int n = 0; n < 4; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if (kw + 8 * n + ((2 * t4 + e) ^ (4 * (n & 1))) >= me.len) sc[n][e] = -INFINITY;
-            }
-            float mx = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1])),
-                             fmaxf(fmaxf(sc[2][0], sc[2][1]), fmaxf(sc[3][0], sc[3][1])));
-            if (__any_sync(0xffffffffu, mx > m_run + 4.f)) {
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float m_new = fmaxf(m_run, mx);
-                const float alpha = m_new == m_run ? 1.f : exp2f(m_run - m_new);
-                m_run = m_new;
-                l_run *= alpha;
-#pragma unroll
-                for (int n = 0; n < D / 8; ++n) {
-                    acc[n][0] *= alpha;
-                    acc[n][1] *= alpha;
-                    acc[n][2] *= alpha;
-                    acc[n][3] *= alpha;
-                }
-            }
-            const float m_use = m_run == -INFINITY ? 0.f : m_run;   // no score yet but -inf (or NaN)
-            float ps = 0.f;
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    sc[n][e] = exp2f(sc[n][e] - m_use);
-                    ps += sc[n][e];
-                    sc[n][e] *= me.pv;
-                }
-            l_run = fmaf(ps, exp2f(-me.lv), l_run);
-            uint32_t pa[4];
-            split4(sc[0][0], sc[0][1], sc[1][0], sc[1][1], pa[0], pa[1]);
-            split4(sc[2][0], sc[2][1], sc[3][0], sc[3][1], pa[2], pa[3]);
-#pragma unroll
-            for (int w = 0; w < D / 16; ++w) {
-                uint32_t b[4];
-                ldsm_b8_t(b, sv + at<D>(vrow, w));
-                mma_e4m3(acc[2 * w], pa, b[0], b[2]);
-                mma_e4m3(acc[2 * w + 1], pa, b[1], b[3]);
-            }
-        }
-        if (!(me.flags & kLast)) {
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[s]);
-            continue;
-        }
-
-        // join the warps' states, in order; once all four have read it, the last block's stage takes the outputs
-        l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
-        l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
-        if (t4 == 0) {
-            sM[warp][g] = m_run;
-            sL[warp][g] = l_run;
-        }
-        named_bar_sync(1, 32 * kWarps);
-        float M = -INFINITY, L = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sM[w][g]);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w)               // an empty state is all zeros, one of NaN scores NaN
-            L += (sM[w][g] == -INFINITY ? 1.f : exp2f(sM[w][g] - M)) * sL[w][g];
-        const float f = m_run == -INFINITY ? 1.f : exp2f(m_run - M);
-        const bool whole = me.part < 0;
-        const float z = (whole ? (L == 0.f ? 0.f : f / L) : f) * 0.0625f;   // P carries 16
-        float *sO = reinterpret_cast<float *>(smem + s * S::STAGE);
-        const long long row = (long long)me.t * p.Hq + (long long)me.r * G;
-        if (g < G) {
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n)
-                *reinterpret_cast<float2 *>(sO + (warp * 8 + g) * S::OROW + n * 8 + 2 * t4) =
-                    make_float2(fmaf(acc[n][2], 0.0625f, acc[n][0]) * z, fmaf(acc[n][3], 0.0625f, acc[n][1]) * z);
-            if (warp == 0 && t4 == 0) {
-                if (whole) lse[row + g] = (M + log2f(L)) * kLn2;
-                else part_ml[me.part * 8 + g] = make_float2(M, L);
+            return true;
+        };
+        bool more = mbar_wait_warp(&full[0], 0, st, 147, &abort_flag) && scores(0);
+        for (int i = 0; more; ++i) {
+            // the next page's scores as soon as it is there, this page's products as soon as its probabilities are
+            bool ahead = false;
+            uint32_t polls = 0;
+            while (!__all_sync(0xffffffffu, mbar_test(&p_full[i & 1], (i >> 1) & 1))) {
+                if (!ahead && landed(i + 1)) {
+                    ahead = true;
+                    fence_after_sync();
+                    more = scores(i + 1);
+                }
+                if (++polls >= kSpinLimit || ((polls & 1023u) == 1023u && *(volatile int *)&abort_flag)) break;
             }
-        }
-        named_bar_sync(1, 32 * kWarps);
-        for (int idx = tid * 4; idx < G * D; idx += 32 * kWarps * 4) {
-            const float *src = sO + idx / D * S::OROW + idx % D;
-            float4 v = *reinterpret_cast<const float4 *>(src);
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) {
-                const float4 u = *reinterpret_cast<const float4 *>(src + w * 8 * S::OROW);
-                v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+            if (polls >= kSpinLimit || *(volatile int *)&abort_flag) {
+                if (polls >= kSpinLimit) report(st, kDevTimeout, 148, i);
+                abort_flag = 1;
+                break;
             }
-            if (whole) *reinterpret_cast<uint2 *>(o + row * D + idx) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-            else *reinterpret_cast<float4 *>(part_o + (long long)me.part * 8 * D + idx) = v;
+            fence_after_sync();
+            const int s = i % kStages;
+            const Meta m = meta[s];
+            if (lane == 0) {
+                const uint64_t dv = tile_desc<D>(base + s * S::STAGE + S::TILE, 8 * D, D == 128 ? 16 : 8 * D);
+                const uint64_t dp = tile_desc<128>(base + S::OFF_P + (i & 1) * S::P, 1024, 16);
+                for (int k = 0; k < max(1, (m.len + 31) / 32); ++k)
+                    mma_f8(tmem + 32, desc_adv(dv, k * 32 * D), desc_adv(dp, k * 32), kIdesc | kAMajorMN, k > 0 || !(m.flags & kFirst));
+                mma_commit(&empty[s]);
+                mma_commit(&pv_done[i & 1]);
+            }
+            __syncwarp();
+            if (!ahead) more = mbar_wait_warp(&full[(i + 1) % kStages], ((i + 1) / kStages) & 1, st, 149, &abort_flag) && scores(i + 1);
         }
-        if (!whole) __threadfence();                   // the state before the arrival
-        fence_proxy_async();                           // the stage goes back to the copies
-        named_bar_sync(1, 32 * kWarps);                // sM and sL are free again, too
-        if (lane == 0) mbar_arrive(&empty[s]);
-        if (whole) continue;
+        if (lane == 0) mma_commit(&drained);
+        __syncwarp();
+        mbar_wait_warp(&drained, 0, nullptr, 0, nullptr);
+    } else {
+        const uint32_t lanes = (uint32_t)warp * 32u << 16;   // this warp's quarter of TMEM
+        float m_ref[8], l[8], fq[8];
+        bool ok = true;                                // no wait of this thread has run out
+#pragma unroll
+        for (int h = 0; h < 8; ++h) m_ref[h] = -INFINITY, l[h] = fq[h] = 0.f;
+        for (int i = 0;; ++i) {
+            const int s = i % kStages;
+            ok = mbar_wait_warp(&s_full[i & 1], (i >> 1) & 1, st, 146, &abort_flag) && ok;
+            fence_after_sync();
+            const Meta me = meta[s];
+            uint32_t c[16];
+            tmem_ld16_nowait(tmem + lanes + (i & 1) * 16, c);
+            tmem_wait16(c);
+            const bool end = ok && (me.flags & kEnd), first = me.flags & kFirst;
+            if (first) {
+#pragma unroll
+                for (int h = 0; h < 8; ++h) m_ref[h] = -INFINITY, l[h] = 0.f, fq[h] = sQ[me.q][h];
+            }
+            float x[8];
+            bool grown = false;
+#pragma unroll
+            for (int h = 0; h < 8; ++h) {
+                x[h] = fmaf(fmaf(__uint_as_float(c[8 + h]), 0.0625f, __uint_as_float(c[h])), fq[h] * me.ks, me.lv);
+                if (tid >= me.len) x[h] = -INFINITY;
+                grown = grown || x[h] > m_ref[h] + 4.f;
+            }
+            // every thread passes the same barriers, also when a wait ran out
+            if (any_of((grown && !end) || !ok)) {
+                if (any_of(!ok)) break;
+#pragma unroll
+                for (int h = 0; h < 8; ++h) {
+                    const float m = warp_max(x[h]);
+                    if (lane == 0) sM[warp][h] = m;
+                }
+                named_bar_sync(1, 32 * kWarps);
+                float alpha[8];
+#pragma unroll
+                for (int h = 0; h < 8; ++h) {
+                    const float m = fmaxf(fmaxf(fmaxf(sM[0][h], sM[1][h]), fmaxf(sM[2][h], sM[3][h])), m_ref[h]);
+                    alpha[h] = m == m_ref[h] ? 1.f : ex2(m_ref[h] - m);
+                    m_ref[h] = m;
+                    l[h] *= alpha[h];
+                }
+                if (!first) {                          // what has been added up so far
+                    ok = mbar_wait_warp(&pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, st, 150, &abort_flag) && ok;
+                    fence_after_sync();
+                    uint32_t v[16];
+                    tmem_ld16_nowait(tmem + lanes + 32, v);
+                    tmem_wait16(v);
+#pragma unroll
+                    for (int h = 0; h < 16; ++h) v[h] = __float_as_uint(__uint_as_float(v[h]) * alpha[h & 7]);
+                    tmem_st16(tmem + lanes + 32, v);
+                    tmem_wait_st();
+                }
+            }
+            if (end) break;
+            const float il = ex2(-me.lv);
+#pragma unroll
+            for (int h = 0; h < 8; ++h) {
+                const float e = ex2(x[h] - (m_ref[h] == -INFINITY ? 0.f : m_ref[h]));   // no score yet but -inf (or NaN)
+                l[h] = fmaf(e, il, l[h]);
+                x[h] = e * me.pv;
+            }
+            if (i >= 2) ok = mbar_wait_warp(&pv_done[i & 1], ((i >> 1) - 1) & 1, st, 151, &abort_flag) && ok;
+            uint8_t *sp = smem + S::OFF_P + (i & 1) * S::P;
+            auto put = [&](int n, uint32_t code) { sp[at<128>(n, tid >> 4) + (tid & 15)] = (uint8_t)code; };
+#pragma unroll
+            for (int h = 0; h < 8; h += 2) {
+                const uint32_t hi = e4m3x2(x[h], x[h + 1]);
+                const float2 f = from_e4m3x2(hi);
+                const uint32_t lo = e4m3x2(16.f * (x[h] - f.x), 16.f * (x[h + 1] - f.y));
+                put(h, hi);
+                put(h + 1, hi >> 8);
+                put(8 + h, lo);
+                put(9 + h, lo >> 8);
+            }
+            // rows behind the last visible token: whatever they hold must not reach 0 * V
+            if (tid >= me.len && tid < max(1, (me.len + 31) / 32) * 32) {
+                uint4 *row = reinterpret_cast<uint4 *>(smem + s * S::STAGE + S::TILE + tid * D);
+#pragma unroll
+                for (int w = 0; w < D / 16; ++w) row[w] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_before_sync();
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[i & 1]);
+            if (!(me.flags & kLast)) continue;
 
-        // the last arrival of a cut row joins its pieces (and leaves the count at zero)
-        if (tid == 0) joins = atomicInc(&arrived[me.first], me.n - 1) == (unsigned)(me.n - 1);
-        named_bar_sync(1, 32 * kWarps);
-        if (!joins) continue;
-        __threadfence();
-        for (int idx = tid * 4; idx < G * D; idx += 32 * kWarps * 4) {
-            constexpr int U = 4;                       // pieces whose loads are in flight together
-            const int h = idx / D;
-            float Mj = -INFINITY, Lj = 0.f;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            // the piece's outputs: this thread's feature, 8 heads
+            float out[1];
+            lane_colsum<8>(l, lane, out);
+            if (lane < 8) sL[warp][lane] = out[0];
+            ok = mbar_wait_warp(&pv_done[i & 1], (i >> 1) & 1, st, 152, &abort_flag) && ok;
+            fence_after_sync();
+            uint32_t v[16];
+            tmem_ld16_nowait(tmem + lanes + 32, v);
+            tmem_wait16(v);
+            named_bar_sync(1, 32 * kWarps);
+            const bool whole = me.part < 0;
+            const long long row = (long long)me.t * p.Hq + (long long)me.r * G;
+#pragma unroll
+            for (int h = 0; h < 8; ++h) {
+                if (h >= G) break;
+                const float L = sL[0][h] + sL[1][h] + sL[2][h] + sL[3][h];
+                const float y = fmaf(__uint_as_float(v[8 + h]), 0.0625f, __uint_as_float(v[h])) * 0.0625f;   // P carries 16
+                if (whole) {
+                    if (tid < D) o[(row + h) * D + tid] = __float2bfloat16_rn(L == 0.f ? 0.f : y / L);
+                    if (tid == h) lse[row + h] = (m_ref[h] + log2f(L)) * kLn2;
+                } else {
+                    if (tid < D) part_o[((long long)me.part * 8 + h) * D + tid] = y;
+                    if (tid == h) part_ml[me.part * 8 + h] = make_float2(m_ref[h], L);
+                }
+            }
+            if (whole) continue;
+
+            // the last arrival of a cut row joins its pieces (and leaves the count at zero)
+            __threadfence();                           // the state before the arrival
+            named_bar_sync(1, 32 * kWarps);
+            if (tid == 0) joins = atomicInc(&arrived[me.first], me.n - 1) == (unsigned)(me.n - 1);
+            named_bar_sync(1, 32 * kWarps);
+            if (!joins) continue;
+            __threadfence();
+            constexpr int U = 4, E = 8 * D / (32 * kWarps * 4);   // pieces, and float4s of a thread, in flight together
+            float Mj[E], Lj[E];
+            float4 y[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) Mj[e] = -INFINITY, Lj[e] = 0.f, y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int i0 = 0; i0 < me.n; i0 += U) {
-                float2 ml[U];
-                float4 v[U];
+                float2 ml[E][U];
+                float4 u4[E][U];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int i = min(i0 + u, me.n - 1);
-                    const long long part = 2 * (me.first + i) + (i == 0 ? 1 : 0);
-                    ml[u] = __ldcg(part_ml + part * 8 + h);
-                    v[u] = __ldcg(reinterpret_cast<const float4 *>(part_o + part * 8 * D + idx));
-                }
-                float m = Mj;
+                for (int e = 0; e < E; ++e)
 #pragma unroll
-                for (int u = 0; u < U; ++u) m = fmaxf(m, ml[u].x);
-                const float keep = Mj == -INFINITY ? 1.f : exp2f(Mj - m);
-                Mj = m;
-                Lj *= keep;
-                x = make_float4(x.x * keep, x.y * keep, x.z * keep, x.w * keep);
+                    for (int u = 0; u < U; ++u) {
+                        const int idx = min((tid + e * 32 * kWarps) * 4, G * D - 4), j = min(i0 + u, me.n - 1);
+                        const long long part = 2 * (me.first + j) + (j == 0 ? 1 : 0);
+                        ml[e][u] = __ldcg(part_ml + part * 8 + idx / D);
+                        u4[e][u] = __ldcg(reinterpret_cast<const float4 *>(part_o + part * 8 * D + idx));
+                    }
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (i0 + u >= me.n) break;
-                    const float w = ml[u].x == -INFINITY ? 1.f : exp2f(ml[u].x - Mj);
-                    Lj += w * ml[u].y;
-                    x = make_float4(fmaf(w, v[u].x, x.x), fmaf(w, v[u].y, x.y), fmaf(w, v[u].z, x.z), fmaf(w, v[u].w, x.w));
+                for (int e = 0; e < E; ++e) {
+                    float m = Mj[e];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) m = fmaxf(m, ml[e][u].x);
+                    const float keep = Mj[e] == -INFINITY ? 1.f : exp2f(Mj[e] - m);   // an empty state is all zeros, one of NaN scores NaN
+                    Mj[e] = m;
+                    Lj[e] *= keep;
+                    y[e] = make_float4(y[e].x * keep, y[e].y * keep, y[e].z * keep, y[e].w * keep);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        if (i0 + u >= me.n) break;
+                        const float w = ml[e][u].x == -INFINITY ? 1.f : exp2f(ml[e][u].x - m);
+                        Lj[e] += w * ml[e][u].y;
+                        y[e] = make_float4(fmaf(w, u4[e][u].x, y[e].x), fmaf(w, u4[e][u].y, y[e].y), fmaf(w, u4[e][u].z, y[e].z),
+                                           fmaf(w, u4[e][u].w, y[e].w));
+                    }
                 }
             }
-            const float inv = Lj == 0.f ? 0.f : 1.f / Lj;
-            *reinterpret_cast<uint2 *>(o + row * D + idx) = make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
-            if (idx % D == 0) lse[row + h] = (Mj + log2f(Lj)) * kLn2;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int idx = (tid + e * 32 * kWarps) * 4;
+                if (idx >= G * D) break;
+                const float z = Lj[e] == 0.f ? 0.f : 1.f / Lj[e];
+                *reinterpret_cast<uint2 *>(o + row * D + idx) = make_uint2(pack_bf16(y[e].x * z, y[e].y * z), pack_bf16(y[e].z * z, y[e].w * z));
+                if (idx % D == 0) lse[row + idx / D] = (Mj[e] + log2f(Lj[e])) * kLn2;
+            }
         }
     }
+    __syncthreads();
+    if (warp == kWarps + 1) tmem_dealloc(tmem, kColumns);
 }
 
 // Whether rows are cut into equal stretches.  Not with many rows (the list is

@@ -89,11 +89,11 @@ def test_workspace_sizes(api):
     assert api.paged_workspace_size(sh, api.OP_PAGED_APPEND) == 256
     assert api.paged_workspace_size(sh, api.OP_PAGED_PLAN) == 512          # 16 bytes and 16 a request
     # attention: two states of a group's heads for each stretch, two to an SM, whatever the batch; none where rows are not cut
-    for kw in (GOOD, {**GOOD, "T": 512}, {**GOOD, "T": 1, "R": 1, "max_blocks": 8192}, {**GOOD, "max_blocks": 4, "topk": 5}):
+    for kw in (GOOD, {**GOOD, "T": 384}, {**GOOD, "T": 1, "R": 1, "max_blocks": 8192}, {**GOOD, "max_blocks": 4, "topk": 5}):
         s = api.PagedShape(**kw)
         n = api.paged_workspace_size(s, api.OP_PAGED_ATTN) - 256
         assert 0 < n <= 2 * 256 * (2 * 8 * (s.d + 2) * 4) + 4096
-    for kw in ({"T": 513}, {"max_blocks": 4, "topk": 4}):
+    for kw in ({"T": 385}, {"max_blocks": 4, "topk": 4}):
         assert api.paged_workspace_size(api.PagedShape(**{**GOOD, **kw}), api.OP_PAGED_ATTN) == 256
     with pytest.raises(api.MsaError):
         api.paged_workspace_size(sh, 15)
