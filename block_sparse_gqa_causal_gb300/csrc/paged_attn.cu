@@ -30,12 +30,13 @@
 //
 // The work is one long list of blocks, those of (row 0, group 0), then (row 0,
 // group 1) and so on, cut into equal stretches for the two CTAs that each SM
-// holds, whatever the rows' lengths.  A producer warp streams the stretch
-// through one ring of stages (K and V tiles of a page and head, contiguous and
-// swizzled by TMA) without a pause where a row ends and the next begins, and
-// lays down each row's queries; one warp issues the MMAs, the next page's S
-// before this page's P V; four warps, a token to a thread, turn scores into
-// probabilities.  A stretch cuts at most two rows; those pieces' states go to
+// holds, whatever the rows' lengths.  A planner warp walks the stretch a row
+// ahead (selection, block table and scales are three dependent loads, 2 us
+// that would empty the ring at every row) and lays down each row's queries; a
+// producer warp streams the pages through one ring of stages (K and V tiles of
+// a page and head, contiguous and swizzled by TMA); one warp issues the MMAs,
+// the next page's S before this page's P V; four warps, a token to a thread,
+// turn scores into probabilities.  A stretch cuts at most two rows; those pieces' states go to
 // the workspace, and the CTA that ends the last piece of a row joins them, in
 // their order along the row.
 #include <algorithm>
@@ -50,9 +51,9 @@ namespace {
 using namespace tc;
 
 constexpr int kWarps = 4;                       // softmax warps, a token of the page to a thread
-constexpr int kThreads = 32 * (kWarps + 2);     // then the producer and the MMA warp
+constexpr int kThreads = 32 * (kWarps + 3);     // then the producer, the MMA and the planner warp
 constexpr int kStages = 3;
-constexpr int kQueries = kStages + 1;           // rows whose queries are held: one more than steps in flight
+constexpr int kQueries = 4;                     // pieces whose queries are held
 constexpr int kColumns = 64;                    // TMEM: two S buffers and O, 16 columns each
 constexpr int kPrefixRows = 384;                // most rows whose blocks are cut evenly; above, whole rows are dealt out
 constexpr int kMinBlocks = 2;                   // a stretch has at least this many blocks
@@ -63,11 +64,19 @@ enum { kFirst = 1, kLast = 2, kEnd = 4 };       // of a piece; of the CTA's stre
 struct Meta {
     int len;        // visible tokens of the block
     float ks;       // the page's K scale for this head
-    float lv, pv;   // log2 of its V scale (-100 at least), and 16 x what that leaves of the scale (1)
+    float lv, il, pv;   // log2 of its V scale (-100 at least), 2^-lv, and 16 x what lv leaves of the scale (1)
     int flags;
-    int t, r, q;    // the piece's row and group, and where its queries lie
+    int t, r, q;    // the piece's row and group, and its number in the stretch
     int part;       // the piece's place among the partial states; -1: a whole row
     int first, n;   // a cut row's first stretch and the number of its pieces
+};
+
+// Up to 32 blocks of a piece, from the planner to the producer.
+struct Chunk {
+    int flags, t, r, q, part, first, n;
+    unsigned blocks;               // which entries are blocks
+    int page[32], len[32];         // len 0: no such page
+    float ks[32], vs[32];
 };
 
 template <int D>
@@ -75,10 +84,10 @@ struct AttnSmem {
     static constexpr int TILE = kPage * D;      // K or V codes of a page and head
     static constexpr int STAGE = 2 * TILE;
     static constexpr int Q = 16 * D;            // a row's queries: hi and lo terms of 8 heads
-    static constexpr int P = 16 * kPage;        // a page's probabilities
+    static constexpr int P = 16 * kPage;        // a page's probabilities, 16 bytes (hi and lo of 8 heads) to a token
     static constexpr int OFF_Q = kStages * STAGE;
     static constexpr int OFF_P = OFF_Q + kQueries * Q;
-    static constexpr int BYTES = OFF_P + 2 * P + 1024;   // + alignment
+    static constexpr int BYTES = OFF_P + 2 * P;
 };
 
 // byte offset of 16-byte word w of row r in a tile of D-byte rows, swizzled as TMA and the MMA descriptors do
@@ -102,6 +111,11 @@ __device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t group, uin
     d |= (uint64_t)(D == 128 ? 2 : 4) << 61;
     return d;
 }
+// MN-major without swizzle, 16 bytes of N to a row: eight rows of K in 128 bytes.
+__device__ __forceinline__ uint64_t rows16_desc(uint32_t addr)
+{
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 16 | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+}
 // instruction descriptor of kind::f8f6f4: e4m3 x e4m3, fp32 sums, 128 x 16
 constexpr uint32_t kIdesc = (1u << 4) | ((16u >> 3) << 17) | ((128u >> 4) << 24);
 
@@ -112,6 +126,13 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, 
         "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
         " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate));
+}
+
+__device__ __forceinline__ float lanes_max(float x)
+{
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(r) : "f"(x));   // passes NaN over
+    return r;
 }
 
 // Barrier 1 over the softmax warps; whether any thread brought `x`.
@@ -147,10 +168,6 @@ __device__ __forceinline__ void split4(float x0, float x1, float x2, float x3, u
     lo = e4m3x2(16.f * (x0 - f01.x), 16.f * (x1 - f01.y)) | (e4m3x2(16.f * (x2 - f23.x), 16.f * (x3 - f23.y)) << 16);
 }
 
-MSA_DEV void mbar_expect_tx(uint64_t *bar, uint32_t bytes)
-{
-    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
-}
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2)
 attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ CUtensorMap tm_k,
@@ -162,14 +179,16 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
 {
     using S = AttnSmem<D>;
     extern __shared__ __align__(1024) uint8_t raw[];
-    uint8_t *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);   // keeps shared addressing
-    __shared__ uint64_t full[kStages], empty[kStages], s_full[2], p_full[2], pv_done[2], drained;
+    uint8_t *smem = raw;
+    __shared__ uint64_t full[kStages], empty[kStages], c_full[2], c_empty[2], q_full[kQueries], q_empty[kQueries], s_full[2], p_full[2],
+        pv_done[2], drained;
     __shared__ Meta meta[kStages];
-    __shared__ float sQ[kQueries][8];           // logit factor of each head's queries, times log2 e
+    __shared__ Chunk chunk[2];
+    __shared__ float sQ[2 * kQueries][8];       // logit factor of each head's queries, times log2 e
     __shared__ float sM[kWarps][8], sL[kWarps][8];
     __shared__ uint32_t tmem_slot;
     __shared__ long long before[kPrefixRows + 1];   // blocks of the rows before each row, one group
-    __shared__ int abort_flag, joins;
+    __shared__ int abort_flag;
 
     chain_next();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = p.G;
@@ -186,6 +205,10 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
         }
         return sel ? p.topk : pos / kPage + 1;
     };
+    if (smem_u32(raw) & 1023u) {                // the swizzled tiles' alignment
+        if (tid == 0) report(st, kDevCheck, 157, (int)smem_u32(raw));
+        return;
+    }
     if (tid == 0) {
         abort_flag = 0;
         for (int i = 0; i < kStages; ++i) {
@@ -196,6 +219,12 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], kWarps);
             mbar_init(&pv_done[i], 1);
+            mbar_init(&c_full[i], 1);
+            mbar_init(&c_empty[i], 1);
+        }
+        for (int i = 0; i < kQueries; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);
         }
         mbar_init(&drained, 1);
         fence_mbar_init();
@@ -231,8 +260,8 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
     fence_after_sync();
     const uint32_t tmem = tmem_slot;
 
-    if (warp == kWarps) {
-        int step = 0, pieces = 0;
+    if (warp == kWarps + 2) {
+        int chunks = 0, pieces = 0;
         bool live = true;
         uint4 x[D / 32];                               // a quarter of head lane / 4's query row
         auto load_q = [&](int t, int r) {
@@ -240,7 +269,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) x[i] = lane / 4 < G ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
         };
-        // ... as hi and lo terms, once no step in flight reads the place any more
+        // ... as hi and lo terms
         auto lay_q = [&](int qi) {
             uint32_t top = 0;
 #pragma unroll
@@ -252,7 +281,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
             // not finite: NaN, and so are the scores
             const float sq = __uint_as_float(top >= 0x7F80u ? 0x7FC00000u : pow2_scale_bits(top)), inv = 1.f / sq;
-            uint8_t *dst = smem + S::OFF_Q + qi * S::Q;
+            uint8_t *dst = smem + S::OFF_Q + qi % kQueries * S::Q;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 const float2 a = unpack_bf16(x[i].x), b = unpack_bf16(x[i].y), c = unpack_bf16(x[i].z), d = unpack_bf16(x[i].w);
@@ -263,41 +292,19 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                 *reinterpret_cast<uint2 *>(dst + at<D>(lane / 4, f >> 4) + (f & 15)) = hi;
                 *reinterpret_cast<uint2 *>(dst + at<D>(8 + lane / 4, f >> 4) + (f & 15)) = lo;
             }
-            if (lane % 4 == 0) sQ[qi][lane / 4] = sq * (p.scale * kLog2e);
+            if (lane % 4 == 0) sQ[qi % (2 * kQueries)][lane / 4] = sq * (p.scale * kLog2e);
             fence_proxy_async();
             __syncwarp();
+            if (lane == 0) mbar_arrive(&q_full[qi % kQueries]);
         };
-        // Waits for the next stage and starts its copies.  The arrival that completes the phase comes with the
-        // block's Meta, so that the copies do not wait for the scales.
-        auto start = [&](int page, int r, int len) {
-            const int s = step % kStages;
-            if (step >= kStages && !mbar_wait_warp(&empty[s], (step / kStages - 1) & 1, st, 144, &abort_flag)) {
-                live = false;
-                return;
-            }
-            if (lane == 0) {
-                const int boxes = (len + 31) / 32;             // 32-token boxes, none past the row
-                if (boxes) mbar_expect_tx(&full[s], boxes * 64 * D);
-                uint8_t *dst = smem + s * S::STAGE;
-                for (int x = 0; x < boxes; ++x)
-                    tma_load_3d(dst + x * 32 * D, &tm_k, &full[s], 0, x * 32, page * p.Hkv + r);
-                for (int x = 0; x < boxes; ++x)
-                    tma_load_3d(dst + S::TILE + x * 32 * D, &tm_v, &full[s], 0, x * 32, page * p.Hkv + r);
-            }
-        };
-        auto publish = [&](const Meta &m) {
-            const int s = step % kStages;
-            if (lane == 0) {
-                meta[s] = m;
-                mbar_arrive(&full[s]);
-            }
-            ++step;
+        auto slot_free = [&]() {
+            return chunks < 2 || mbar_wait_warp(&c_empty[chunks & 1], ((chunks >> 1) - 1) & 1, st, 158, &abort_flag);
         };
         // blocks (a selection: slots) j0 .. j1 - 1 of group r of row t
         auto piece = [&](int t, int r, int req, int pos, int j0, int j1, int part, int first_cut, int n_cut) {
-            const int c0 = pos / kPage, qi = pieces++ % kQueries;
+            const int c0 = pos / kPage, qi = pieces++;
             load_q(t, r);
-            for (int base = j0; base < j1 && live; base += 32) {
+            for (int base = j0; base < j1; base += 32) {
                 int c = -1;
                 if (sel) {
                     // selected blocks ascend; an entry that does not, or lies past the row's own block, is no block
@@ -318,7 +325,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                     c = base + lane;
                 }
                 int page = -1, len = 0;
-                float ks = 0.f, vscale = 0.f;
+                float ks = 0.f, vscale = 1.f;
                 if (c >= 0) {
                     page = block_table[(long long)req * p.max_blocks + c];
                     if ((unsigned)page >= (unsigned)p.n_pages) {
@@ -329,34 +336,34 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                         vscale = v_scale[(long long)page * p.Hkv + r];
                     }
                 }
-                // a block without a page is an empty step, and so is a piece without any block
-                unsigned todo = __ballot_sync(0xffffffffu, c >= 0);
-                if (sel && !todo) todo = 1;
-                bool first = base == j0;
-                while (todo && live) {
-                    const int l = __ffs(todo) - 1;
-                    todo &= todo - 1;
-                    const int blen = __shfl_sync(0xffffffffu, len, l);
-                    start(__shfl_sync(0xffffffffu, page, l), r, blen);
-                    if (!live) break;
-                    if (first) lay_q(qi);
-                    Meta m;
-                    m.len = blen;
-                    m.ks = __shfl_sync(0xffffffffu, ks, l);
-                    const float vs = __shfl_sync(0xffffffffu, vscale, l);
-                    m.lv = fmaxf(log2f(vs), -100.f);
-                    m.pv = 16.f * (vs * exp2f(-m.lv));
-                    m.flags = (first ? kFirst : 0) | (!todo && (sel || base + 32 >= j1) ? kLast : 0);
-                    m.t = t;
-                    m.r = r;
-                    m.q = qi;
-                    m.part = part;
-                    m.first = first_cut;
-                    m.n = n_cut;
-                    first = false;
-                    publish(m);
+                if (!slot_free()) {
+                    live = false;
+                    return;
                 }
-                if (sel) break;                        // at most 32 slots: one round
+                Chunk &ch = chunk[chunks & 1];
+                ch.page[lane] = page;
+                ch.len[lane] = len;
+                ch.ks[lane] = ks;
+                ch.vs[lane] = vscale;
+                // a block without a page is an empty step, and so is a piece without any block
+                const unsigned blocks = __ballot_sync(0xffffffffu, c >= 0);
+                const bool last = sel || base + 32 >= j1;      // at most 32 slots: one round
+                if (lane == 0) {
+                    ch.flags = (base == j0 ? kFirst : 0) | (last ? kLast : 0);
+                    ch.t = t, ch.r = r, ch.q = qi, ch.part = part, ch.first = first_cut, ch.n = n_cut;
+                    ch.blocks = sel && !blocks ? 1u : blocks;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c_full[chunks & 1]);
+                ++chunks;
+                if (base == j0) {
+                    if (qi >= kQueries && !mbar_wait_warp(&q_empty[qi % kQueries], (qi / kQueries - 1) & 1, st, 159, &abort_flag)) {
+                        live = false;
+                        return;
+                    }
+                    lay_q(qi);
+                }
+                if (last) break;
             }
         };
         const int me = blockIdx.x;
@@ -396,20 +403,70 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                 if (nt) piece(t, (int)(i % p.Hkv), req, pos, 0, nt, -1, 0, 0);
             }
         }
-        const int copied = step;
-        if (live) {
-            const int s = step % kStages;
-            if (step < kStages || mbar_wait_warp(&empty[s], (step / kStages - 1) & 1, st, 144, &abort_flag)) {
+        if (live && slot_free() && lane == 0) {
+            chunk[chunks & 1].flags = kEnd;
+            mbar_arrive(&c_full[chunks & 1]);
+        }
+    } else if (warp == kWarps) {
+        int step = 0;
+        bool live = true, ended = false;
+        auto copy = [&](const CUtensorMap *tm, uint8_t *dst, uint64_t *bar, int tile, int len) {
+            for (int i = 0; i < (len + 31) / 32; ++i)          // 32-token boxes, none past the row
+                tma_load_3d(dst + i * 32 * D, tm, bar, 0, i * 32, tile);
+        };
+        auto stage_free = [&]() {
+            return step < kStages || mbar_wait_warp(&empty[step % kStages], (step / kStages - 1) & 1, st, 144, &abort_flag);
+        };
+        for (int i = 0; live; ++i) {
+            if (!mbar_wait_warp(&c_full[i & 1], (i >> 1) & 1, st, 160, &abort_flag)) break;
+            const Chunk &ch = chunk[i & 1];
+            Meta m;
+            const int flags = ch.flags;
+            m.t = ch.t, m.r = ch.r, m.q = ch.q, m.part = ch.part, m.first = ch.first, m.n = ch.n;
+            unsigned todo = ch.blocks;
+            const int page = ch.page[lane], len = ch.len[lane];
+            const float ks = ch.ks[lane], vs = ch.vs[lane];
+            const float lv = fmaxf(log2f(vs), -100.f), il = exp2f(-lv), pv = 16.f * (vs * il);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c_empty[i & 1]);
+            if (flags & kEnd) {
+                ended = stage_free();
+                if (ended && lane == 0) {
+                    meta[step % kStages].flags = kEnd;
+                    meta[step % kStages].len = 0;
+                    mbar_arrive(&full[step % kStages]);
+                }
+                break;
+            }
+            bool first = flags & kFirst;
+            while (todo) {
+                const int l = __ffs(todo) - 1, s = step % kStages;
+                todo &= todo - 1;
+                m.len = __shfl_sync(0xffffffffu, len, l);
+                m.ks = __shfl_sync(0xffffffffu, ks, l);
+                m.lv = __shfl_sync(0xffffffffu, lv, l);
+                m.il = __shfl_sync(0xffffffffu, il, l);
+                m.pv = __shfl_sync(0xffffffffu, pv, l);
+                m.flags = (first ? kFirst : 0) | (!todo && (flags & kLast) ? kLast : 0);
+                first = false;
+                const int tile = __shfl_sync(0xffffffffu, page, l) * p.Hkv + m.r;
+                if (!stage_free()) {
+                    live = false;
+                    break;
+                }
                 if (lane == 0) {
-                    meta[s].flags = kEnd;
-                    meta[s].len = 0;
-                    mbar_arrive(&full[s]);
+                    meta[s] = m;
+                    const int boxes = (m.len + 31) / 32;
+                    if (boxes) mbar_arrive_expect_tx(&full[s], boxes * 64 * D);
+                    else mbar_arrive(&full[s]);
+                    copy(&tm_k, smem + s * S::STAGE, &full[s], tile, m.len);
+                    copy(&tm_v, smem + s * S::STAGE + S::TILE, &full[s], tile, m.len);
                 }
                 ++step;
             }
         }
-        // stay until the last copies have landed (the stage of the end mark has been read)
-        for (int k = max(0, step - kStages); k < copied; ++k) mbar_wait_warp(&full[k % kStages], (k / kStages) & 1, st, 145, nullptr);
+        // stay until the last copies have landed (the end mark's stage has been read)
+        for (int k = max(0, step - kStages + (ended ? 1 : 0)); k < step; ++k) mbar_wait_warp(&full[k % kStages], (k / kStages) & 1, st, 145, nullptr);
     } else if (warp == kWarps + 1) {
         const uint32_t base = smem_u32(smem);
         auto landed = [&](int i) { return __all_sync(0xffffffffu, mbar_test(&full[i % kStages], (i / kStages) & 1)); };
@@ -421,11 +478,14 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                 if (lane == 0) mbar_arrive(&s_full[i & 1]);
                 return false;
             }
+            if ((m.flags & kFirst) && !mbar_wait_warp(&q_full[m.q % kQueries], (m.q / kQueries) & 1, st, 161, &abort_flag)) return false;
+            fence_after_sync();
             if (lane == 0) {
-                const uint64_t dk = tile_desc<D>(base + s * S::STAGE, 8 * D, 16), dq = tile_desc<D>(base + S::OFF_Q + m.q * S::Q, 8 * D, 16);
+                const uint64_t dk = tile_desc<D>(base + s * S::STAGE, 8 * D, 16), dq = tile_desc<D>(base + S::OFF_Q + m.q % kQueries * S::Q, 8 * D, 16);
 #pragma unroll
                 for (int k = 0; k < D / 32; ++k) mma_f8(tmem + (i & 1) * 16, desc_adv(dk, k * 32), desc_adv(dq, k * 32), kIdesc, k > 0);
                 mma_commit(&s_full[i & 1]);
+                if (m.flags & kLast) mma_commit(&q_empty[m.q % kQueries]);
             }
             __syncwarp();
             return true;
@@ -438,7 +498,6 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
             while (!__all_sync(0xffffffffu, mbar_test(&p_full[i & 1], (i >> 1) & 1))) {
                 if (!ahead && landed(i + 1)) {
                     ahead = true;
-                    fence_after_sync();
                     more = scores(i + 1);
                 }
                 if (++polls >= kSpinLimit || ((polls & 1023u) == 1023u && *(volatile int *)&abort_flag)) break;
@@ -448,14 +507,14 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                 abort_flag = 1;
                 break;
             }
-            fence_after_sync();
             const int s = i % kStages;
+            fence_after_sync();
             const Meta m = meta[s];
             if (lane == 0) {
                 const uint64_t dv = tile_desc<D>(base + s * S::STAGE + S::TILE, 8 * D, D == 128 ? 16 : 8 * D);
-                const uint64_t dp = tile_desc<128>(base + S::OFF_P + (i & 1) * S::P, 1024, 16);
+                const uint64_t dp = rows16_desc(base + S::OFF_P + (i & 1) * S::P);
                 for (int k = 0; k < max(1, (m.len + 31) / 32); ++k)
-                    mma_f8(tmem + 32, desc_adv(dv, k * 32 * D), desc_adv(dp, k * 32), kIdesc | kAMajorMN, k > 0 || !(m.flags & kFirst));
+                    mma_f8(tmem + 32, desc_adv(dv, k * 32 * D), desc_adv(dp, k * 32 * 16), kIdesc | kAMajorMN | kBMajorMN, k > 0 || !(m.flags & kFirst));
                 mma_commit(&empty[s]);
                 mma_commit(&pv_done[i & 1]);
             }
@@ -468,9 +527,68 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
     } else {
         const uint32_t lanes = (uint32_t)warp * 32u << 16;   // this warp's quarter of TMEM
         float m_ref[8], l[8], fq[8];
-        bool ok = true;                                // no wait of this thread has run out
+        bool ok = true, live = true;                   // no wait of this thread, of any has run out
+        // a cut row whose piece has been handed in, and how many had been before it (thread 0)
+        unsigned before_me = 0;
+        int cut_n = 0, cut_first = 0;
+        long long cut_row = 0;
 #pragma unroll
         for (int h = 0; h < 8; ++h) m_ref[h] = -INFINITY, l[h] = fq[h] = 0.f;
+
+        // The last CTA to hand in a piece of a cut row joins them all (and has left the count at zero).  The count
+        // comes back while the next page is worked on.
+        auto join = [&]() {
+            const int n = cut_n;
+            cut_n = 0;
+            if (!any_of(tid == 0 && before_me == (unsigned)n - 1)) return;
+            __threadfence();
+            constexpr int U = 4, E = 8 * D / (32 * kWarps * 4);   // pieces, and float4s of a thread, in flight together
+            float M[E], L[E];
+            float4 y[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) M[e] = -INFINITY, L[e] = 0.f, y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i0 = 0; i0 < n; i0 += U) {
+                float2 ml[E][U];
+                float4 x[E][U];
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int idx = min((tid + e * 32 * kWarps) * 4, G * D - 4), j = min(i0 + u, n - 1);
+                        const long long part = 2 * (cut_first + j) + (j == 0 ? 1 : 0);
+                        ml[e][u] = __ldcg(part_ml + part * 8 + idx / D);
+                        x[e][u] = __ldcg(reinterpret_cast<const float4 *>(part_o + part * 8 * D + idx));
+                    }
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    float m = M[e];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) m = fmaxf(m, ml[e][u].x);
+                    const float keep = M[e] == -INFINITY ? 1.f : ex2(M[e] - m);   // an empty state is all zeros, one of NaN scores NaN
+                    M[e] = m;
+                    L[e] *= keep;
+                    y[e] = make_float4(y[e].x * keep, y[e].y * keep, y[e].z * keep, y[e].w * keep);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        if (i0 + u >= n) break;
+                        const float f = ml[e][u].x == -INFINITY ? 1.f : ex2(ml[e][u].x - m);
+                        L[e] = fmaf(f, ml[e][u].y, L[e]);
+                        y[e] = make_float4(fmaf(f, x[e][u].x, y[e].x), fmaf(f, x[e][u].y, y[e].y), fmaf(f, x[e][u].z, y[e].z),
+                                           fmaf(f, x[e][u].w, y[e].w));
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int idx = (tid + e * 32 * kWarps) * 4;
+                if (idx >= G * D) break;
+                const float z = L[e] == 0.f ? 0.f : 1.f / L[e];
+                *reinterpret_cast<uint2 *>(o + cut_row * D + idx) =
+                    make_uint2(pack_bf16(y[e].x * z, y[e].y * z), pack_bf16(y[e].z * z, y[e].w * z));
+                if (idx % D == 0) lse[cut_row + idx / D] = (M[e] + log2f(L[e])) * kLn2;
+            }
+        };
+
         for (int i = 0;; ++i) {
             const int s = i % kStages;
             ok = mbar_wait_warp(&s_full[i & 1], (i >> 1) & 1, st, 146, &abort_flag) && ok;
@@ -482,22 +600,24 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
             const bool end = ok && (me.flags & kEnd), first = me.flags & kFirst;
             if (first) {
 #pragma unroll
-                for (int h = 0; h < 8; ++h) m_ref[h] = -INFINITY, l[h] = 0.f, fq[h] = sQ[me.q][h];
+                for (int h = 0; h < 8; ++h) m_ref[h] = -INFINITY, l[h] = 0.f, fq[h] = sQ[me.q % (2 * kQueries)][h];
             }
-            float x[8];
-            bool grown = false;
+            float x[8], over = -INFINITY;
 #pragma unroll
             for (int h = 0; h < 8; ++h) {
                 x[h] = fmaf(fmaf(__uint_as_float(c[8 + h]), 0.0625f, __uint_as_float(c[h])), fq[h] * me.ks, me.lv);
                 if (tid >= me.len) x[h] = -INFINITY;
-                grown = grown || x[h] > m_ref[h] + 4.f;
+                over = fmaxf(over, x[h] == -INFINITY ? -INFINITY : x[h] - m_ref[h]);
             }
             // every thread passes the same barriers, also when a wait ran out
-            if (any_of((grown && !end) || !ok)) {
-                if (any_of(!ok)) break;
+            if (any_of((over > 4.f && !end) || !ok)) {
+                if (any_of(!ok)) {
+                    live = false;
+                    break;
+                }
 #pragma unroll
                 for (int h = 0; h < 8; ++h) {
-                    const float m = warp_max(x[h]);
+                    const float m = lanes_max(x[h]);
                     if (lane == 0) sM[warp][h] = m;
                 }
                 named_bar_sync(1, 32 * kWarps);
@@ -522,28 +642,26 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                 }
             }
             if (end) break;
-            const float il = ex2(-me.lv);
 #pragma unroll
             for (int h = 0; h < 8; ++h) {
-                const float e = ex2(x[h] - (m_ref[h] == -INFINITY ? 0.f : m_ref[h]));   // no score yet but -inf (or NaN)
-                l[h] = fmaf(e, il, l[h]);
+                // no score yet but -inf (or NaN): -inf - -inf must not be
+                const float e = ex2(m_ref[h] == -INFINITY ? x[h] : x[h] - m_ref[h]);
+                l[h] = fmaf(e, me.il, l[h]);
                 x[h] = e * me.pv;
             }
-            if (i >= 2) ok = mbar_wait_warp(&pv_done[i & 1], ((i >> 1) - 1) & 1, st, 151, &abort_flag) && ok;
-            uint8_t *sp = smem + S::OFF_P + (i & 1) * S::P;
-            auto put = [&](int n, uint32_t code) { sp[at<128>(n, tid >> 4) + (tid & 15)] = (uint8_t)code; };
+            uint32_t hi[4], lo[4];
 #pragma unroll
             for (int h = 0; h < 8; h += 2) {
-                const uint32_t hi = e4m3x2(x[h], x[h + 1]);
-                const float2 f = from_e4m3x2(hi);
-                const uint32_t lo = e4m3x2(16.f * (x[h] - f.x), 16.f * (x[h + 1] - f.y));
-                put(h, hi);
-                put(h + 1, hi >> 8);
-                put(8 + h, lo);
-                put(9 + h, lo >> 8);
+                hi[h / 2] = e4m3x2(x[h], x[h + 1]);
+                const float2 f = from_e4m3x2(hi[h / 2]);
+                lo[h / 2] = e4m3x2(16.f * (x[h] - f.x), 16.f * (x[h + 1] - f.y));
             }
+            if (i >= 2) ok = mbar_wait_warp(&pv_done[i & 1], ((i >> 1) - 1) & 1, st, 151, &abort_flag) && ok;
+            *reinterpret_cast<uint4 *>(smem + S::OFF_P + (i & 1) * S::P + tid * 16) =
+                make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
             // rows behind the last visible token: whatever they hold must not reach 0 * V
-            if (tid >= me.len && tid < max(1, (me.len + 31) / 32) * 32) {
+            const int rows = max(1, (me.len + 31) / 32) * 32;
+            if (tid >= me.len && tid < rows) {
                 uint4 *row = reinterpret_cast<uint4 *>(smem + s * S::STAGE + S::TILE + tid * D);
 #pragma unroll
                 for (int w = 0; w < D / 16; ++w) row[w] = make_uint4(0u, 0u, 0u, 0u);
@@ -552,87 +670,48 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[i & 1]);
+            if (cut_n) join();
             if (!(me.flags & kLast)) continue;
 
             // the piece's outputs: this thread's feature, 8 heads
-            float out[1];
-            lane_colsum<8>(l, lane, out);
-            if (lane < 8) sL[warp][lane] = out[0];
+            float sum[1];
+            lane_colsum<8>(l, lane, sum);
+            if (lane < 8) sL[warp][lane] = sum[0];
+            named_bar_sync(1, 32 * kWarps);
+            const int hl = lane & 7;                   // the head whose sum and reference this lane keeps
+            const float L = sL[0][hl] + sL[1][hl] + sL[2][hl] + sL[3][hl];
+            float ml = m_ref[0];
+#pragma unroll
+            for (int h = 1; h < 8; ++h) ml = hl == h ? m_ref[h] : ml;
+            const bool whole = me.part < 0;
+            const float z = 0.0625f * (!whole ? 1.f : L == 0.f ? 0.f : 1.f / L);   // P carries 16
+            const long long row = (long long)me.t * p.Hq + (long long)me.r * G;
+            if (warp == 0 && lane < G) {
+                if (whole) lse[row + lane] = (ml + log2f(L)) * kLn2;
+                else part_ml[me.part * 8 + lane] = make_float2(ml, L);
+            }
             ok = mbar_wait_warp(&pv_done[i & 1], (i >> 1) & 1, st, 152, &abort_flag) && ok;
             fence_after_sync();
             uint32_t v[16];
             tmem_ld16_nowait(tmem + lanes + 32, v);
             tmem_wait16(v);
-            named_bar_sync(1, 32 * kWarps);
-            const bool whole = me.part < 0;
-            const long long row = (long long)me.t * p.Hq + (long long)me.r * G;
 #pragma unroll
             for (int h = 0; h < 8; ++h) {
-                if (h >= G) break;
-                const float L = sL[0][h] + sL[1][h] + sL[2][h] + sL[3][h];
-                const float y = fmaf(__uint_as_float(v[8 + h]), 0.0625f, __uint_as_float(v[h])) * 0.0625f;   // P carries 16
-                if (whole) {
-                    if (tid < D) o[(row + h) * D + tid] = __float2bfloat16_rn(L == 0.f ? 0.f : y / L);
-                    if (tid == h) lse[row + h] = (m_ref[h] + log2f(L)) * kLn2;
-                } else {
-                    if (tid < D) part_o[((long long)me.part * 8 + h) * D + tid] = y;
-                    if (tid == h) part_ml[me.part * 8 + h] = make_float2(m_ref[h], L);
-                }
+                const float zh = __shfl_sync(0xffffffffu, z, h);
+                if (h >= G || tid >= D) continue;
+                const float y = fmaf(__uint_as_float(v[8 + h]), 0.0625f, __uint_as_float(v[h])) * zh;
+                if (whole) o[(row + h) * D + tid] = __float2bfloat16_rn(y);
+                else part_o[((long long)me.part * 8 + h) * D + tid] = y;
             }
             if (whole) continue;
-
-            // the last arrival of a cut row joins its pieces (and leaves the count at zero)
-            __threadfence();                           // the state before the arrival
+            __threadfence();                           // the state before the count
             named_bar_sync(1, 32 * kWarps);
-            if (tid == 0) joins = atomicInc(&arrived[me.first], me.n - 1) == (unsigned)(me.n - 1);
-            named_bar_sync(1, 32 * kWarps);
-            if (!joins) continue;
-            __threadfence();
-            constexpr int U = 4, E = 8 * D / (32 * kWarps * 4);   // pieces, and float4s of a thread, in flight together
-            float Mj[E], Lj[E];
-            float4 y[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) Mj[e] = -INFINITY, Lj[e] = 0.f, y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int i0 = 0; i0 < me.n; i0 += U) {
-                float2 ml[E][U];
-                float4 u4[E][U];
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int idx = min((tid + e * 32 * kWarps) * 4, G * D - 4), j = min(i0 + u, me.n - 1);
-                        const long long part = 2 * (me.first + j) + (j == 0 ? 1 : 0);
-                        ml[e][u] = __ldcg(part_ml + part * 8 + idx / D);
-                        u4[e][u] = __ldcg(reinterpret_cast<const float4 *>(part_o + part * 8 * D + idx));
-                    }
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    float m = Mj[e];
-#pragma unroll
-                    for (int u = 0; u < U; ++u) m = fmaxf(m, ml[e][u].x);
-                    const float keep = Mj[e] == -INFINITY ? 1.f : exp2f(Mj[e] - m);   // an empty state is all zeros, one of NaN scores NaN
-                    Mj[e] = m;
-                    Lj[e] *= keep;
-                    y[e] = make_float4(y[e].x * keep, y[e].y * keep, y[e].z * keep, y[e].w * keep);
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        if (i0 + u >= me.n) break;
-                        const float w = ml[e][u].x == -INFINITY ? 1.f : exp2f(ml[e][u].x - m);
-                        Lj[e] += w * ml[e][u].y;
-                        y[e] = make_float4(fmaf(w, u4[e][u].x, y[e].x), fmaf(w, u4[e][u].y, y[e].y), fmaf(w, u4[e][u].z, y[e].z),
-                                           fmaf(w, u4[e][u].w, y[e].w));
-                    }
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int idx = (tid + e * 32 * kWarps) * 4;
-                if (idx >= G * D) break;
-                const float z = Lj[e] == 0.f ? 0.f : 1.f / Lj[e];
-                *reinterpret_cast<uint2 *>(o + row * D + idx) = make_uint2(pack_bf16(y[e].x * z, y[e].y * z), pack_bf16(y[e].z * z, y[e].w * z));
-                if (idx % D == 0) lse[row + idx / D] = (Mj[e] + log2f(Lj[e])) * kLn2;
-            }
+            if (tid == 0) before_me = atomicInc(&arrived[me.first], me.n - 1);
+            cut_n = me.n;
+            cut_first = me.first;
+            cut_row = row;
         }
+        if (cut_n && live) join();
     }
     __syncthreads();
     if (warp == kWarps + 1) tmem_dealloc(tmem, kColumns);
