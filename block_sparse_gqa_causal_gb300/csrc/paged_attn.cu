@@ -31,8 +31,8 @@
 // The work is one long list of blocks, those of (row 0, group 0), then (row 0,
 // group 1) and so on, cut into equal stretches for the two CTAs that each SM
 // holds, whatever the rows' lengths.  A planner warp walks the stretch a row
-// ahead (selection, block table and scales are three dependent loads, 2 us
-// that would empty the ring at every row) and lays down each row's queries; a
+// ahead (row, selection and block table are dependent loads, 2 us that would
+// empty the ring at every row) and lays down each row's queries; a
 // producer warp streams the pages through one ring of stages (K and V tiles of
 // a page and head, contiguous and swizzled by TMA); one warp issues the MMAs,
 // the next page's S before this page's P V; four warps, a token to a thread,
@@ -76,7 +76,6 @@ struct Chunk {
     int flags, t, r, q, part, first, n;
     unsigned blocks;               // which entries are blocks
     int page[32], len[32];         // len 0: no such page
-    float ks[32], vs[32];
 };
 
 template <int D>
@@ -166,6 +165,11 @@ __device__ __forceinline__ void split4(float x0, float x1, float x2, float x3, u
     const float2 f01 = from_e4m3x2(h01), f23 = from_e4m3x2(h23);
     hi = h01 | (h23 << 16);
     lo = e4m3x2(16.f * (x0 - f01.x), 16.f * (x1 - f01.y)) | (e4m3x2(16.f * (x2 - f23.x), 16.f * (x3 - f23.y)) << 16);
+}
+
+MSA_DEV void mbar_expect_tx(uint64_t *bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 
 template <int D>
@@ -325,15 +329,12 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                     c = base + lane;
                 }
                 int page = -1, len = 0;
-                float ks = 0.f, vscale = 1.f;
                 if (c >= 0) {
                     page = block_table[(long long)req * p.max_blocks + c];
                     if ((unsigned)page >= (unsigned)p.n_pages) {
                         report(st, kDevCheck, 143, page);
                     } else {
                         len = min(kPage, pos - c * kPage + 1);
-                        ks = k_scale[(long long)page * p.Hkv + r];
-                        vscale = v_scale[(long long)page * p.Hkv + r];
                     }
                 }
                 if (!slot_free()) {
@@ -343,8 +344,6 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                 Chunk &ch = chunk[chunks & 1];
                 ch.page[lane] = page;
                 ch.len[lane] = len;
-                ch.ks[lane] = ks;
-                ch.vs[lane] = vscale;
                 // a block without a page is an empty step, and so is a piece without any block
                 const unsigned blocks = __ballot_sync(0xffffffffu, c >= 0);
                 const bool last = sel || base + 32 >= j1;      // at most 32 slots: one round
@@ -420,16 +419,8 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
         for (int i = 0; live; ++i) {
             if (!mbar_wait_warp(&c_full[i & 1], (i >> 1) & 1, st, 160, &abort_flag)) break;
             const Chunk &ch = chunk[i & 1];
-            Meta m;
             const int flags = ch.flags;
-            m.t = ch.t, m.r = ch.r, m.q = ch.q, m.part = ch.part, m.first = ch.first, m.n = ch.n;
-            unsigned todo = ch.blocks;
-            const int page = ch.page[lane], len = ch.len[lane];
-            const float ks = ch.ks[lane], vs = ch.vs[lane];
-            const float lv = fmaxf(log2f(vs), -100.f), il = exp2f(-lv), pv = 16.f * (vs * il);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&c_empty[i & 1]);
-            if (flags & kEnd) {
+            if (flags & kEnd) {                        // a chunk of nothing else: its entries hold anything
                 ended = stage_free();
                 if (ended && lane == 0) {
                     meta[step % kStages].flags = kEnd;
@@ -438,15 +429,20 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                 }
                 break;
             }
+            Meta m;
+            m.t = ch.t, m.r = ch.r, m.q = ch.q, m.part = ch.part, m.first = ch.first, m.n = ch.n;
+            unsigned todo = ch.blocks;
+            const int page = ch.page[lane], len = ch.len[lane];
+            // the scales come while the first copies are under way
+            const long long ph = len ? (long long)page * p.Hkv + m.r : 0;
+            const float ks = len ? k_scale[ph] : 0.f, vs = len ? v_scale[ph] : 1.f;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c_empty[i & 1]);
             bool first = flags & kFirst;
             while (todo) {
                 const int l = __ffs(todo) - 1, s = step % kStages;
                 todo &= todo - 1;
                 m.len = __shfl_sync(0xffffffffu, len, l);
-                m.ks = __shfl_sync(0xffffffffu, ks, l);
-                m.lv = __shfl_sync(0xffffffffu, lv, l);
-                m.il = __shfl_sync(0xffffffffu, il, l);
-                m.pv = __shfl_sync(0xffffffffu, pv, l);
                 m.flags = (first ? kFirst : 0) | (!todo && (flags & kLast) ? kLast : 0);
                 first = false;
                 const int tile = __shfl_sync(0xffffffffu, page, l) * p.Hkv + m.r;
@@ -454,13 +450,19 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                     live = false;
                     break;
                 }
-                if (lane == 0) {
-                    meta[s] = m;
-                    const int boxes = (m.len + 31) / 32;
-                    if (boxes) mbar_arrive_expect_tx(&full[s], boxes * 64 * D);
-                    else mbar_arrive(&full[s]);
+                if (lane == 0 && m.len) {
+                    mbar_expect_tx(&full[s], (m.len + 31) / 32 * 64 * D);
                     copy(&tm_k, smem + s * S::STAGE, &full[s], tile, m.len);
                     copy(&tm_v, smem + s * S::STAGE + S::TILE, &full[s], tile, m.len);
+                }
+                const float lane_vs = __shfl_sync(0xffffffffu, vs, l);
+                m.ks = __shfl_sync(0xffffffffu, ks, l);
+                m.lv = fmaxf(log2f(lane_vs), -100.f);
+                m.il = exp2f(-m.lv);
+                m.pv = 16.f * (lane_vs * m.il);
+                if (lane == 0) {
+                    meta[s] = m;
+                    mbar_arrive(&full[s]);
                 }
                 ++step;
             }

@@ -83,7 +83,8 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedProblem p, PlanArgs a, 
                                                     DeviceStatus *st)
 {
     __shared__ Sums warp_sum[32];
-    __shared__ int bad;
+    __shared__ int bad, n_ended;
+    __shared__ int3 ended[1024];
     chain_next();
     chain_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, nwarp = nthr >> 5;
@@ -182,21 +183,25 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedProblem p, PlanArgs a, 
             if (!why) reinterpret_cast<int4 *>(scratch)[1 + r] = make_int4((int)at.take, (int)at.segs, q.old, q.held);
         }
         // pages of ended requests go behind the free ones, a warp to a request
-        unsigned todo = __ballot_sync(0xffffffffu, !why && q.s.gone > 0);
-        while (todo) {
-            const int l = __ffs(todo) - 1;
-            todo &= todo - 1;
-            const int n = __shfl_sync(0xffffffffu, (int)q.s.gone, l), b = __shfl_sync(0xffffffffu, (int)at.gone, l);
-            const int32_t *row = a.block_table + (long long)(base + (warp << 5) + l) * p.max_blocks;
-            constexpr int U = 16;                                // loads in flight before the stores they may not pass
-            for (int j0 = lane; j0 < n; j0 += 32 * U) {
-                int32_t page[U];
+        if (!why && total.gone > 0) {
+            if (tid == 0) n_ended = 0;
+            __syncthreads();
+            if (q.s.gone > 0) ended[atomicAdd(&n_ended, 1)] = make_int3(r, (int)q.s.gone, (int)at.gone);
+            __syncthreads();
+            for (int i = warp; i < n_ended; i += nwarp) {
+                const int3 e = ended[i];
+                const int32_t *row = a.block_table + (long long)e.x * p.max_blocks;
+                constexpr int U = 16;                            // loads in flight before the stores they may not pass
+                for (int j0 = lane; j0 < e.y; j0 += 32 * U) {
+                    int32_t page[U];
 #pragma unroll
-                for (int i = 0; i < U; ++i) page[i] = j0 + 32 * i < n ? row[j0 + 32 * i] : 0;
+                    for (int u = 0; u < U; ++u) page[u] = j0 + 32 * u < e.y ? row[j0 + 32 * u] : 0;
 #pragma unroll
-                for (int i = 0; i < U; ++i)
-                    if (j0 + 32 * i < n) a.free_pages[((long long)head + count + b + j0 + 32 * i) % p.n_pages] = page[i];
+                    for (int u = 0; u < U; ++u)
+                        if (j0 + 32 * u < e.y) a.free_pages[((long long)head + count + e.z + j0 + 32 * u) % p.n_pages] = page[u];
+                }
             }
+            __syncthreads();
         }
     }
     if (tid == 0) {
@@ -228,7 +233,7 @@ cudaError_t launch_paged_plan(const PagedProblem &p, const PlanArgs &a, int32_t 
 {
     const int S = paged_segments(p);
     const bool fused = p.T <= kFusedRows;
-    const int want = std::max(p.R, fused ? p.T : 1);
+    const int want = a.ended ? 1024 : std::max(p.R, fused ? p.T : 1);
     const int threads = std::min(1024, std::max(64, (want + 31) / 32 * 32));
     cudaError_t e = launch_chained("paged_plan_kernel", plan_kernel, dim3(1), threads, 0, s, p, a, scratch, S, fused ? 1 : 0, st);
     if (e != cudaSuccess || fused) return e;

@@ -28,19 +28,27 @@ __device__ __forceinline__ unsigned long long merged(unsigned long long best, un
     return merge_desc64(best > o ? best : o, lane);
 }
 
-// descending bitonic sort of one 32-bit value per lane
-__device__ __forceinline__ uint32_t sort_desc32(uint32_t v, int lane)
+// descending bitonic sort of one value per lane
+template <class T>
+__device__ __forceinline__ T sort_desc(T v, int lane)
 {
 #pragma unroll
     for (int size = 2; size <= 32; size <<= 1) {
 #pragma unroll
         for (int stride = size >> 1; stride > 0; stride >>= 1) {
-            const uint32_t o = __shfl_xor_sync(0xffffffffu, v, stride);
+            const T o = __shfl_xor_sync(0xffffffffu, v, stride);
             const bool desc = (lane & size) == 0 || size == 32;
             v = ((lane & stride) == 0) == desc ? max(v, o) : min(v, o);
         }
     }
     return v;
+}
+
+// the score of a ranking key; -inf of none
+__device__ __forceinline__ float worst(unsigned long long key)
+{
+    const uint32_t u = (uint32_t)(key >> 32);
+    return key == 0 ? -INFINITY : __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
 }
 
 // W: warps of a row; R: rows of a CTA
@@ -50,7 +58,7 @@ topk_kernel(PagedProblem p, const float *__restrict__ scores, const int32_t *__r
             int32_t *__restrict__ sel, DeviceStatus *st)
 {
     static_assert(W == 1 || R == 1, "a row's warps fill the CTA");
-    __shared__ int list[W * R][kTile];                        // the blocks of a tile that reach the bound, ascending
+    __shared__ int list[W * R][kTile];                        // the blocks of a tile that reach the bound
     __shared__ unsigned long long lists[W][32];
     chain_next();
     chain_wait();
@@ -69,29 +77,26 @@ topk_kernel(PagedProblem p, const float *__restrict__ scores, const int32_t *__r
     if (c0 >= k && k > 1) {
         int *mine = list[warp];
         for (int base = (W == 1 ? 0 : warp) * kTile; base < c0; base += W * kTile) {
-            uint32_t v[kPer], top = 0;                        // 0 below every score's key
-            const int n = min(kTile, c0 - base);
+            const int n = min(kTile, c0 - base), mine_n = (n - lane + 31) / 32;   // this lane's: blocks base + lane + 32 i
+            float v[kPer], top = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                v[i] = 0;
-                if (i * 32 < n && i * 32 + lane < n) {
-                    const float s = sc[base + i * 32 + lane];
-                    v[i] = float_key(s != s ? -INFINITY : s);  // a NaN ranks last
-                }
+            for (int i = 0; i < kPer; ++i) v[i] = i < mine_n ? sc[base + i * 32 + lane] : -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) top = fmaxf(top, v[i]);   // passes NaN over
+            const float bound = fmaxf(__shfl_sync(0xffffffffu, sort_desc(top, lane), k - 2), worst(shfl64(best, k - 2)));
+            uint32_t in = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) in |= (fmaxf(v[i], -INFINITY) >= bound ? 1u : 0u) << i;   // a NaN ranks last
+            in &= mine_n >= 32 ? ~0u : mine_n > 0 ? (1u << mine_n) - 1 : 0u;
+            int at = __popc(in), m = at;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, at, d);
+                if (lane >= d) at += o;
             }
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) top = max(top, v[i]);
-            const uint32_t bound = max(__shfl_sync(0xffffffffu, sort_desc32(top, lane), k - 2),
-                                       (uint32_t)(shfl64(best, k - 2) >> 32));
-            int m = 0;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                if (i * 32 >= n) break;
-                const bool in = v[i] >= bound && v[i] != 0;
-                const uint32_t b = __ballot_sync(0xffffffffu, in);
-                if (in) mine[m + __popc(b & ((1u << lane) - 1))] = base + i * 32 + lane;
-                m += __popc(b);
-            }
+            m = __shfl_sync(0xffffffffu, at, 31);
+            at -= __popc(in);
+            for (; in; in &= in - 1) mine[at++] = base + lane + 32 * (__ffs(in) - 1);
             __syncwarp();
             for (int i = 0; i < m; i += 32) {
                 unsigned long long key = 0;
@@ -128,7 +133,7 @@ topk_kernel(PagedProblem p, const float *__restrict__ scores, const int32_t *__r
     } else if (lane == k - 1) {
         c = 0xFFFFFFFFu - (uint32_t)c0;
     }
-    c = sort_desc32(c, lane);
+    c = sort_desc(c, lane);
     if (lane < k) sel[row * k + lane] = c ? (int32_t)(0xFFFFFFFFu - c) : -1;
 }
 
