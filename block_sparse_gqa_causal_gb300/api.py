@@ -462,8 +462,9 @@ def _stream_on(dev) -> int:
     return _raw_stream(dev.index) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
-def _paged_call(fn, shape: PagedShape, op: int, dev, tensors, workspace) -> None:
-    """Checks the tensors against the call's specs, all on one CUDA device, and makes the call."""
+def _paged_call(fn, shape: PagedShape, op: int, dev, tensors, made, workspace) -> None:
+    """Checks the tensors against the call's specs, all on one CUDA device, and makes the call; `made` are the last
+    arguments, where this module has just allocated them."""
     ptrs = []
     for (name, shp, dtype, optional), t in zip(shape._specs[op], tensors):
         if t is None:
@@ -474,6 +475,8 @@ def _paged_call(fn, shape: PagedShape, op: int, dev, tensors, workspace) -> None
         if t.dtype is not dtype or t.shape != shp or t.device != dev or not t.is_contiguous():
             raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {shp} on {dev}, "
                              f"got {t.dtype} {tuple(t.shape)} contiguous={t.is_contiguous()} on {t.device}")
+        ptrs.append(t.data_ptr())
+    for t in made:
         ptrs.append(t.data_ptr())
     if dev.type != "cuda":
         raise ValueError(f"need CUDA tensors, got {dev}")
@@ -510,12 +513,14 @@ def paged_plan(shape: PagedShape, new_lens, lens, block_table, free_pages, free_
     if place is not None:
         with place:
             return paged_plan(s, new_lens, lens, block_table, free_pages, free_state, ended=ended, out=out, workspace=workspace)
+    given, made = out or (), ()
     if out is None:
-        row = torch.empty(s.T, dtype=torch.int32, device=dev)
-        out = PagedPlan(torch.empty_like(lens), torch.empty_like(free_state), torch.empty(s.R + 1, dtype=torch.int32, device=dev),
-                        row, torch.empty_like(row), torch.empty_like(row), torch.empty(s.n_segs + 1, dtype=torch.int32, device=dev))
+        new = lambda n: torch.empty(n, dtype=torch.int32, device=dev)  # noqa: E731
+        row = new(s.T)
+        made = out = PagedPlan(torch.empty_like(lens), torch.empty_like(free_state), new(s.R + 1), row, torch.empty_like(row),
+                               torch.empty_like(row), new(s.n_segs + 1))
     _paged_call((_lib or lib()).msa_paged_plan, s, OP_PAGED_PLAN, dev,
-                (new_lens, lens, ended, block_table, free_pages, free_state, *out), workspace)
+                (new_lens, lens, ended, block_table, free_pages, free_state, *given), made, workspace)
     return out
 
 
@@ -531,7 +536,7 @@ def paged_append(shape: PagedShape, k_new, v_new, k_idx_new, slots, segs, k8, v8
         with place:
             return paged_append(shape, k_new, v_new, k_idx_new, slots, segs, k8, v8, k_scale, v_scale, k_idx, workspace=workspace)
     _paged_call((_lib or lib()).msa_paged_append, shape, OP_PAGED_APPEND, dev,
-                (k_new, v_new, k_idx_new, slots, segs, k8, v8, k_scale, v_scale, k_idx), workspace)
+                (k_new, v_new, k_idx_new, slots, segs, k8, v8, k_scale, v_scale, k_idx), (), workspace)
 
 
 def paged_block_scores(shape: PagedShape, q_idx, k_idx, block_table, q_starts, row_req, row_pos, *, block_scores=None,
@@ -543,10 +548,12 @@ def paged_block_scores(shape: PagedShape, q_idx, k_idx, block_table, q_starts, r
     if place is not None:
         with place:
             return paged_block_scores(s, q_idx, k_idx, block_table, q_starts, row_req, row_pos, block_scores=block_scores, workspace=workspace)
+    given, made = (block_scores,), ()
     if block_scores is None:
         block_scores = torch.empty((s.T, s.Hkv, s.max_blocks), dtype=torch.float32, device=dev)
+        given, made = (), (block_scores,)
     _paged_call((_lib or lib()).msa_paged_block_scores, s, OP_PAGED_BLOCK_SCORES, dev,
-                (q_idx, k_idx, block_table, q_starts, row_req, row_pos, block_scores), workspace)
+                (q_idx, k_idx, block_table, q_starts, row_req, row_pos, *given), made, workspace)
     return block_scores
 
 
@@ -557,9 +564,11 @@ def paged_block_topk(shape: PagedShape, block_scores, row_pos, *, sel_idx=None, 
     if place is not None:
         with place:
             return paged_block_topk(s, block_scores, row_pos, sel_idx=sel_idx, workspace=workspace)
+    given, made = (sel_idx,), ()
     if sel_idx is None:
         sel_idx = torch.empty((s.T, s.Hkv, s.topk), dtype=torch.int32, device=dev)
-    _paged_call((_lib or lib()).msa_paged_block_topk, s, OP_PAGED_BLOCK_TOPK, dev, (block_scores, row_pos, sel_idx), workspace)
+        given, made = (), (sel_idx,)
+    _paged_call((_lib or lib()).msa_paged_block_topk, s, OP_PAGED_BLOCK_TOPK, dev, (block_scores, row_pos, *given), made, workspace)
     return sel_idx
 
 
@@ -572,10 +581,15 @@ def paged_attn(shape: PagedShape, q, k8, v8, k_scale, v_scale, block_table, row_
     if place is not None:
         with place:
             return paged_attn(s, q, k8, v8, k_scale, v_scale, block_table, row_req, row_pos, sel_idx=sel_idx, o=o, lse=lse, workspace=workspace)
-    o = torch.empty_like(q) if o is None else o
-    lse = torch.empty((s.T, s.Hq), dtype=torch.float32, device=dev) if lse is None else lse
+    if o is None and lse is None:
+        o, lse = torch.empty((s.T, s.Hq, s.d), dtype=torch.bfloat16, device=dev), torch.empty((s.T, s.Hq), dtype=torch.float32, device=dev)
+        given, made = (), (o, lse)
+    else:
+        o = torch.empty((s.T, s.Hq, s.d), dtype=torch.bfloat16, device=dev) if o is None else o
+        lse = torch.empty((s.T, s.Hq), dtype=torch.float32, device=dev) if lse is None else lse
+        given, made = (o, lse), ()
     _paged_call((_lib or lib()).msa_paged_attn, s, OP_PAGED_ATTN, dev,
-                (q, k8, v8, k_scale, v_scale, block_table, row_req, row_pos, sel_idx, o, lse), workspace)
+                (q, k8, v8, k_scale, v_scale, block_table, row_req, row_pos, sel_idx, *given), made, workspace)
     return o, lse
 
 

@@ -22,13 +22,14 @@ namespace {
 
 constexpr int kFusedRows = 4096;
 constexpr int kFillThreads = 256;
+constexpr int kCopied = 2048;            // requests whose first rows a CTA copies
 
 // scratch: {ring head, segments, -, -}, then per request {first page taken,
 // first segment, length before, pages held before}
 __device__ __forceinline__ int pages_of(int n) { return (n + kPage - 1) / kPage; }
 
 __device__ __forceinline__ void fill_entry(const PagedProblem &p, const PlanArgs &a, const int32_t *scratch, int S,
-                                           int n_rows, int n_segs, int head, int i, DeviceStatus *st)
+                                           const int32_t *starts, int n_rows, int n_segs, int head, int i, DeviceStatus *st)
 {
     if (i >= n_segs && i <= S) a.segs[i] = n_rows;
     if (i >= p.T) return;
@@ -41,11 +42,11 @@ __device__ __forceinline__ void fill_entry(const PagedProblem &p, const PlanArgs
     int lo = 0, hi = p.R;                       // the last r with q_starts[r] <= i
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (a.q_starts[mid] <= i) lo = mid;
+        if (starts[mid] <= i) lo = mid;
         else hi = mid;
     }
     const int4 rq = reinterpret_cast<const int4 *>(scratch)[1 + lo];
-    const int q0 = a.q_starts[lo];
+    const int q0 = starts[lo];
     const int pos = rq.z + (i - q0), blk = pos / kPage, off = pos % kPage;
     int32_t *entry = a.block_table + (long long)lo * p.max_blocks + blk;
     int page;
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedProblem p, PlanArgs a, 
     __syncthreads();
     const int n = max(p.T, S + 1);
     for (int i = tid; i < n; i += nthr)
-        fill_entry(p, a, scratch, S, (int)total.rows, (int)total.segs, head, i, st);
+        fill_entry(p, a, scratch, S, a.q_starts, (int)total.rows, (int)total.segs, head, i, st);
 }
 
 __global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(PagedProblem p, PlanArgs a, const int32_t *scratch, int S,
@@ -221,8 +222,14 @@ __global__ void __launch_bounds__(kFillThreads) plan_fill_kernel(PagedProblem p,
 {
     chain_next();
     chain_wait();
+    // the bisection's steps depend on one another: a copy in shared memory answers them ten times sooner
+    __shared__ int32_t copy[kCopied + 1];
+    const bool small = p.R <= kCopied;
+    if (small)
+        for (int r = threadIdx.x; r <= p.R; r += kFillThreads) copy[r] = a.q_starts[r];
+    __syncthreads();
     const int i = blockIdx.x * kFillThreads + threadIdx.x;
-    fill_entry(p, a, scratch, S, a.q_starts[p.R], scratch[1], scratch[0], i, st);
+    fill_entry(p, a, scratch, S, small ? copy : a.q_starts, a.q_starts[p.R], scratch[1], scratch[0], i, st);
 }
 
 }  // namespace

@@ -646,3 +646,75 @@ def test_cache_offsets_past_32_bits(api):
         res.append((k8[at], v8[at], ki[at], ks[at], bs, o, lse))
     for a, b in zip(*res):
         assert torch.equal(a.view(torch.uint8) if a.dtype is torch.float8_e4m3fn else a, b)
+
+
+def test_steps_without_rows(api):
+    """Every request idle, or no row that belongs to one: nothing is written and nothing recorded."""
+    import torch
+    sv = Server(api, R=3, nb=4, n_pages=8, Hq=8, Hkv=2, d=64, di=64, k=2, T=5, seed=1)
+    x = sv.rows()
+    for new in ([0, 0, 0], [2, 0, 3], [0, 0, 0]):
+        before = [t.clone() for t in (sv.table, sv.ring, sv.ks, sv.ki)]
+        plan, bs, sel, o, lse = sv.step(i32(new), None, {n: v[0] for n, v in x.items()})
+        for ws in sv.ws.values():
+            status_ok(api, ws)
+        if sum(new) == 0:
+            assert not plan.q_starts.any() and (plan.row_req == -1).all()
+            assert all(torch.equal(a, b) for a, b in zip(before, (sv.table, sv.ring, sv.ks, sv.ki)))
+    assert sv.lens.tolist() == [2, 0, 3] and sv.free.tolist()[1] == 6
+
+
+def test_two_streams_at_once(api):
+    """Two callers on two streams, each with its own workspace and outputs, over the same cache."""
+    import torch
+    cases = [attn_case(api, lens=[3000 + 50 * i for i in range(20)], q=[1] * 20, Hq=16, Hkv=2, d=128, k=16, sparse=True, seed=s) for s in (0, 1)]
+    want = [api.paged_attn(sh, *args, sel_idx=i32(sel)) for sh, args, sel, r in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    spaces = [api.new_paged_workspace(c[0], api.OP_PAGED_ATTN) for c in cases]
+    sels = [i32(c[2]) for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [api.paged_attn(c[0], *c[1], sel_idx=s, workspace=w, stream=st) for c, s, w, st in zip(cases, sels, spaces, streams)]
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
+def test_workspace_shared_by_graphs_replayed_in_turn(api):
+    """Two graphs over one workspace, one after the other on a stream, as the workspace rule allows."""
+    import torch
+    (sh, args, sel, _), (sh2, args2, _, _) = (attn_case(api, lens=[2500, 900, 4000], q=[1, 1, 1], Hq=16, Hkv=2, d=128, k=16, sparse=sp, seed=7) for sp in (True, False))
+    sel = i32(sel)
+    want, want2 = api.paged_attn(sh, *args, sel_idx=sel), api.paged_attn(sh2, *args2)
+    ws = api.new_paged_workspace(sh, api.OP_PAGED_ATTN)
+    graphs, outs = [], []
+    for call in (lambda: api.paged_attn(sh, *args, sel_idx=sel, workspace=ws), lambda: api.paged_attn(sh2, *args2, workspace=ws)):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(call())
+        graphs.append(g)
+    for i in range(30):
+        graphs[i % 2].replay()
+        graphs[(i + i // 3) % 2].replay()
+    torch.cuda.synchronize()
+    for got, w in zip(outs, (want, want2)):
+        assert torch.equal(got[0], w[0]) and torch.equal(got[1], w[1])
+    status_ok(api, ws)
+
+
+def test_outputs_on_a_given_stream_are_not_reused_early(api):
+    """Outputs and workspaces that a call allocates belong to the stream it runs on: calls on a side stream, their results
+    dropped and memory asked for again on the current stream meanwhile."""
+    import torch
+    sh, args, sel, _ = attn_case(api, lens=[5000] * 16, q=[1] * 16, Hq=16, Hkv=2, d=128, k=16, sparse=True)
+    sel = i32(sel)
+    want = api.paged_attn(sh, *args, sel_idx=sel)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(30):
+        o, lse = api.paged_attn(sh, *args, sel_idx=sel, stream=side)       # its own workspace, freed on return
+        junk = [torch.full((1 << 18,), 7, dtype=torch.int32, device="cuda") for _ in range(8)]
+        side.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        del o, lse, junk
