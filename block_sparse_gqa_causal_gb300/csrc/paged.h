@@ -47,7 +47,15 @@ cudaError_t make_tmap_u8_3d(CUtensorMap *map, const void *base, unsigned long lo
 // set up in turn (chain_next) and waits for the predecessor's end, its writes
 // visible, before it touches global memory (chain_wait).  After any other
 // kernel this is an ordinary launch.
-MSA_DEV void chain_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+// The pointers given take on new values, as far as the compiler can tell, so that no load through them
+// (loads of const __restrict__ data may pass a memory clobber) is moved above the wait.
+template <class... P>
+MSA_DEV void chain_wait(P &...ptrs)
+{
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    auto renew = [](auto &p) { asm volatile("" : "+l"(p)::"memory"); };
+    (renew(ptrs), ...);
+}
 MSA_DEV void chain_next() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
 template <class... P, class... A>

@@ -15,9 +15,9 @@
 //
 // The tiles' pages, one tile after another, are cut into equal stretches for
 // the two CTAs that each SM holds, whatever the requests' lengths: at four
-// caches of 131,072 to 1,048,576 tokens 97 us against 100 for a grid of
-// (tile, share) CTAs.  With more rows than kPrefixRows, whole tiles are dealt
-// out.
+// caches of 131,072 to 1,048,576 tokens (605 MB) 93 us, 96% of the copy rate,
+// against 100 for a grid of (tile, share) CTAs.  With more rows than
+// kPrefixRows, whole tiles are dealt out.
 #include <algorithm>
 #include <type_traits>
 
@@ -75,7 +75,7 @@ scores_kernel(PagedProblem p, const bf16 *__restrict__ q_idx, const __grid_const
         }
         fence_mbar_init();
     }
-    chain_wait();
+    chain_wait(q_idx, block_table, q_starts, row_req, row_pos);
 
     // the rows of the tile that row t begins (a tile is up to rows_per_tile rows of one request); 0: t begins none
     auto tile_rows = [&](int t) {

@@ -360,6 +360,7 @@ msa_status msa_kv_append(const msa_shape *shape, const void *k_new, const void *
  * call on it, and again after msa_check_device_status() reported a timeout.
  * What device memory says (lengths, pages, selections) is checked on the
  * device: an entry out of range is left out and recorded in the status word.
+ * Outputs do not overlap inputs or one another, but where a call says so.
  */
 typedef struct {
     int R, T, max_blocks, n_pages, Hq, Hkv, d, d_idx, topk;
