@@ -2,13 +2,16 @@
 
 Argument marshalling only: it checks dtypes and layouts, allocates outputs
 and workspaces with torch (device memory), and passes raw pointers and the
-current CUDA stream to the library.  Every step of the computation runs in
+current CUDA stream to the library (the paged calls through _paged_binding.so,
+which does the same natively).  Every step of the computation runs in
 the library's kernels; there is no fallback.  If libmsa.so has not been
 built, the first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import importlib.util
 import math
 import os
 import threading
@@ -130,36 +133,36 @@ class PagedShape:
         return _CPagedShape(self.R, self.T, self.max_blocks, self.n_pages, self.Hq, self.Hkv, self.d, self.d_idx,
                             self.topk, self.scale, self.scale_idx)
 
-    @cached_property
-    def _ref(self):
-        return ctypes.byref(self.c())
+    def __getstate__(self):
+        return {n: getattr(self, n) for n in self.__dataclass_fields__}     # copies and pickles leave the handles behind
 
     @cached_property
-    def _specs(self) -> dict:
-        """What each call takes: (name, shape, dtype, may be None) of its tensors, in the order of the C arguments."""
-        i32, f32, bf, f8 = torch.int32, torch.float32, torch.bfloat16, torch.float8_e4m3fn
-        table = ("block_table", (self.R, self.max_blocks), i32, False)
-        rows = [(n, (self.T,), i32, False) for n in ("row_req", "row_pos")]
-        cache = [(n, (self.n_pages, self.Hkv, PAGE, self.d), f8, False) for n in ("k8", "v8")]
-        scales = [(n, (self.n_pages, self.Hkv), f32, False) for n in ("k_scale", "v_scale")]
-        k_idx = ("k_idx", (self.n_pages, PAGE, self.d_idx), bf, False)
-        new = [(n, (self.T, self.Hkv, self.d), bf, True) for n in ("k_new", "v_new")] + [("k_idx_new", (self.T, self.d_idx), bf, True)]
-        sel = (self.T, self.Hkv, self.topk)
-        scores = (self.T, self.Hkv, self.max_blocks)
-        plan = [("lens", (self.R,)), ("free_state", (2,)), ("q_starts", (self.R + 1,)), ("row_req", (self.T,)), ("row_pos", (self.T,)),
-                ("slots", (self.T,)), ("segs", (self.n_segs + 1,))]
-        return {
-            OP_PAGED_PLAN: [("new_lens", (self.R,), i32, False), ("lens", (self.R,), i32, False), ("ended", (self.R,), i32, True), table,
-                            ("free_pages", (self.n_pages,), i32, False), ("free_state", (2,), i32, False)]
-            + [(n, s, i32, False) for n, s in plan],
-            OP_PAGED_APPEND: new + [("slots", (self.T,), i32, False), ("segs", (self.n_segs + 1,), i32, False)]
-            + [(n, s, t, True) for n, s, t, _ in cache + scales + [k_idx]],
-            OP_PAGED_BLOCK_SCORES: [("q_idx", (self.T, self.Hkv, self.d_idx), bf, False), k_idx, table, ("q_starts", (self.R + 1,), i32, False)]
-            + rows + [("block_scores", scores, f32, False)],
-            OP_PAGED_BLOCK_TOPK: [("block_scores", scores, f32, False), rows[1], ("sel_idx", sel, i32, False)],
-            OP_PAGED_ATTN: [("q", (self.T, self.Hq, self.d), bf, False)] + cache + scales + [table] + rows
-            + [("sel_idx", sel, i32, True), ("o", (self.T, self.Hq, self.d), bf, False), ("lse", (self.T, self.Hq), f32, False)],
+    def _calls(self) -> dict:
+        """By op, the binding's handle of the call: the shape and (name, shape, dtype, kind) of each tensor in the order of
+        the C arguments."""
+        i32, f32, bf, f8 = 0, 1, 2, 3                  # dtypes
+        need, maybe, out = 0, 1, 2                     # kinds; an `out` that is None is allocated
+        R, T, H, N, D = self.R, self.T, self.Hkv, self.n_pages, self.d
+        row = lambda *names: [(n, (T,), i32, need) for n in names]  # noqa: E731
+        table, starts = ("block_table", (R, self.max_blocks), i32, need), ("q_starts", (R + 1,), i32, need)
+        cache = lambda kind: ([(n, (N, H, PAGE, D), f8, kind) for n in ("k8", "v8")]  # noqa: E731
+                              + [(n, (N, H), f32, kind) for n in ("k_scale", "v_scale")])
+        k_idx, sel, scores = (N, PAGE, self.d_idx), (T, H, self.topk), (T, H, self.max_blocks)
+        specs = {
+            OP_PAGED_PLAN: [("new_lens", (R,), i32, need), ("lens", (R,), i32, need), ("ended", (R,), i32, maybe), table,
+                            ("free_pages", (N,), i32, need), ("free_state", (2,), i32, need), ("lens", (R,), i32, out),
+                            ("free_state", (2,), i32, out), ("q_starts", (R + 1,), i32, out), ("row_req", (T,), i32, out),
+                            ("row_pos", (T,), i32, out), ("slots", (T,), i32, out), ("segs", (self.n_segs + 1,), i32, out)],
+            OP_PAGED_APPEND: [("k_new", (T, H, D), bf, maybe), ("v_new", (T, H, D), bf, maybe), ("k_idx_new", (T, self.d_idx), bf, maybe),
+                              *row("slots"), ("segs", (self.n_segs + 1,), i32, need), *cache(maybe), ("k_idx", k_idx, bf, maybe)],
+            OP_PAGED_BLOCK_SCORES: [("q_idx", (T, H, self.d_idx), bf, need), ("k_idx", k_idx, bf, need), table, starts,
+                                    *row("row_req", "row_pos"), ("block_scores", scores, f32, out)],
+            OP_PAGED_BLOCK_TOPK: [("block_scores", scores, f32, need), *row("row_pos"), ("sel_idx", sel, i32, out)],
+            OP_PAGED_ATTN: [("q", (T, self.Hq, D), bf, need), *cache(need), table, *row("row_req", "row_pos"),
+                            ("sel_idx", sel, i32, maybe), ("o", (T, self.Hq, D), bf, out), ("lse", (T, self.Hq), f32, out)],
         }
+        fields = (R, T, self.max_blocks, N, self.Hq, H, D, self.d_idx, self.topk, self.scale, self.scale_idx)
+        return {op: binding().prepare(op, fields, args) for op, args in specs.items()}
 
 
 class PagedPlan(NamedTuple):
@@ -212,11 +215,9 @@ def lib() -> ctypes.CDLL:
             GS = ctypes.POINTER(_CPagedShape)
             L.msa_paged_workspace_size.argtypes = [GS, ctypes.c_int]
             L.msa_paged_workspace_size.restype = sz
-            L.msa_paged_plan.argtypes = [GS] + [P] * 14 + [sz, P]
-            L.msa_paged_append.argtypes = [GS] + [P] * 11 + [sz, P]
-            L.msa_paged_block_scores.argtypes = [GS] + [P] * 8 + [sz, P]
-            L.msa_paged_block_topk.argtypes = [GS] + [P] * 4 + [sz, P]
-            L.msa_paged_attn.argtypes = [GS] + [P] * 12 + [sz, P]
+            for fn, ptrs in (("msa_paged_plan", 14), ("msa_paged_append", 11), ("msa_paged_block_scores", 8),
+                             ("msa_paged_block_topk", 4), ("msa_paged_attn", 12)):
+                getattr(L, fn).argtypes = [GS] + [P] * ptrs + [sz, P]
             L.msa_selftest_wait_timeout.argtypes = [P, ctypes.c_uint, P]
             for fn in ("msa_index_select", "msa_sparse_attn_fwd", "msa_kl_fwd", "msa_fused_bwd", "msa_fused_bwd_kl",
                        "msa_train_step", "msa_train_step_staged", "msa_check_device_status", "msa_block_mask",
@@ -233,6 +234,25 @@ def lib() -> ctypes.CDLL:
             L.msa_kernel_timing_report.restype = sz
             _lib = L
         return _lib
+
+
+_binding = None
+
+
+def binding():
+    """Load _paged_binding.so, the paged calls' marshalling (fails loudly if it is missing)."""
+    global _binding
+    lib()                                   # libmsa.so, which the binding is linked with
+    with _lock:
+        if _binding is None:
+            path = os.path.join(_HERE, "_paged_binding.so")
+            if not os.path.exists(path):
+                raise RuntimeError(f"{path} is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`")
+            spec = importlib.util.spec_from_file_location("block_sparse_gqa_causal_gb300._paged_binding", path)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            _binding = module
+        return _binding
 
 
 def _check(code: int) -> None:
@@ -441,54 +461,8 @@ def kv_append(shape: Shape, k_new, v_new, k_idx_new, k, v, k_idx, *, stream=None
                                _ptr(k_idx), _stream(stream)))
 
 
-def _place(dev, stream):
-    """None where the tensors' device is the current one and no stream is given;
-    else the context in which a paged call allocates and launches (the stream, so
-    that what is allocated there is not handed out again before the call's
-    kernels are done with it)."""
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-        return torch.cuda.stream(stream)
-    return torch.cuda.device(dev) if dev.type == "cuda" and dev.index != torch.cuda.current_device() else None
-
-
-# The current stream's handle of a device; the public call builds a Stream object first, which
-# costs as much as half of a small kernel's launch.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _stream_on(dev) -> int:
-    return _raw_stream(dev.index) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
-
-
-def _paged_call(fn, shape: PagedShape, op: int, dev, tensors, made, workspace) -> None:
-    """Checks the tensors against the call's specs, all on one CUDA device, and makes the call; `made` are the last
-    arguments, where this module has just allocated them."""
-    ptrs = []
-    for (name, shp, dtype, optional), t in zip(shape._specs[op], tensors):
-        if t is None:
-            if not optional:
-                raise ValueError(f"{name} is None")
-            ptrs.append(None)
-            continue
-        if t.dtype is not dtype or t.shape != shp or t.device != dev or not t.is_contiguous():
-            raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {shp} on {dev}, "
-                             f"got {t.dtype} {tuple(t.shape)} contiguous={t.is_contiguous()} on {t.device}")
-        ptrs.append(t.data_ptr())
-    for t in made:
-        ptrs.append(t.data_ptr())
-    if dev.type != "cuda":
-        raise ValueError(f"need CUDA tensors, got {dev}")
-    if workspace is None:
-        workspace = new_paged_workspace(shape, op, dev)
-    elif workspace.device != dev or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
-        raise ValueError(f"workspace: need a contiguous uint8 tensor on {dev}, got {workspace.dtype} on {workspace.device}")
-    _check(fn(shape._ref, *ptrs, workspace.data_ptr(), workspace.numel(), _stream_on(dev)))
-
-
 def paged_workspace_size(shape: PagedShape, op: int) -> int:
-    n = lib().msa_paged_workspace_size(shape._ref, op)
+    n = lib().msa_paged_workspace_size(ctypes.byref(shape.c()), op)
     if n == 0:
         _check(1)
     return int(n)
@@ -501,6 +475,26 @@ def new_paged_workspace(shape: PagedShape, op: int, device=None) -> torch.Tensor
     return ws
 
 
+def _paged(shape: PagedShape, op: int, workspace, stream, *tensors):
+    """A paged call through the binding, which checks the tensors, on their device and its current stream; the outputs."""
+    if stream is not None:
+        # outputs and workspace are allocated on the stream as well, so that they are not handed out again before the
+        # call's kernels are done with them
+        dev = next(t.device for t in tensors if t is not None)
+        if stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        with torch.cuda.stream(stream):
+            return _paged(shape, op, workspace, None, *tensors)
+    if workspace is None:
+        dev = next(t.device for t in tensors if t is not None)
+        with torch.cuda.device(dev) if dev.type == "cuda" else contextlib.nullcontext():
+            workspace = new_paged_workspace(shape, op, dev)
+    r = (_binding or binding()).call(shape._calls[op], workspace, *tensors)
+    if type(r) is int:
+        _check(r)
+    return r
+
+
 def paged_plan(shape: PagedShape, new_lens, lens, block_table, free_pages, free_state, *, ended=None, out=None,
                workspace=None, stream=None) -> PagedPlan:
     """msa_paged_plan: the step's pages, block tables and slot maps from the
@@ -508,20 +502,8 @@ def paged_plan(shape: PagedShape, new_lens, lens, block_table, free_pages, free_
     [R, max_blocks] and free_pages [n_pages] int32 are updated in place.  Returns a
     PagedPlan (pass `out` to reuse its tensors; its lens and free_state may be
     the tensors passed in)."""
-    s, dev = shape, new_lens.device
-    place = _place(dev, stream)
-    if place is not None:
-        with place:
-            return paged_plan(s, new_lens, lens, block_table, free_pages, free_state, ended=ended, out=out, workspace=workspace)
-    given, made = out or (), ()
-    if out is None:
-        new = lambda n: torch.empty(n, dtype=torch.int32, device=dev)  # noqa: E731
-        row = new(s.T)
-        made = out = PagedPlan(torch.empty_like(lens), torch.empty_like(free_state), new(s.R + 1), row, torch.empty_like(row),
-                               torch.empty_like(row), new(s.n_segs + 1))
-    _paged_call((_lib or lib()).msa_paged_plan, s, OP_PAGED_PLAN, dev,
-                (new_lens, lens, ended, block_table, free_pages, free_state, *given), made, workspace)
-    return out
+    return PagedPlan(*_paged(shape, OP_PAGED_PLAN, workspace, stream, new_lens, lens, ended, block_table, free_pages, free_state,
+                             *(out or (None,) * 7)))
 
 
 def paged_append(shape: PagedShape, k_new, v_new, k_idx_new, slots, segs, k8, v8, k_scale, v_scale, k_idx, *,
@@ -530,67 +512,27 @@ def paged_append(shape: PagedShape, k_new, v_new, k_idx_new, slots, segs, k8, v8
     (bf16) into the caches k8, v8 [n_pages, Hkv, 128, d] (float8_e4m3fn) with
     k_scale, v_scale [n_pages, Hkv] (fp32), and k_idx [n_pages, 128, d_idx] (bf16),
     at a plan's slots and segs.  The K and V group, or the K_idx pair, may be None."""
-    dev = slots.device
-    place = _place(dev, stream)
-    if place is not None:
-        with place:
-            return paged_append(shape, k_new, v_new, k_idx_new, slots, segs, k8, v8, k_scale, v_scale, k_idx, workspace=workspace)
-    _paged_call((_lib or lib()).msa_paged_append, shape, OP_PAGED_APPEND, dev,
-                (k_new, v_new, k_idx_new, slots, segs, k8, v8, k_scale, v_scale, k_idx), (), workspace)
+    _paged(shape, OP_PAGED_APPEND, workspace, stream, k_new, v_new, k_idx_new, slots, segs, k8, v8, k_scale, v_scale, k_idx)
 
 
 def paged_block_scores(shape: PagedShape, q_idx, k_idx, block_table, q_starts, row_req, row_pos, *, block_scores=None,
                        workspace=None, stream=None):
     """msa_paged_block_scores: [T, Hkv, max_blocks] fp32 of q_idx [T, Hkv, d_idx] and
     the pages k_idx [n_pages, 128, d_idx] (bf16)."""
-    s, dev = shape, q_idx.device
-    place = _place(dev, stream)
-    if place is not None:
-        with place:
-            return paged_block_scores(s, q_idx, k_idx, block_table, q_starts, row_req, row_pos, block_scores=block_scores, workspace=workspace)
-    given, made = (block_scores,), ()
-    if block_scores is None:
-        block_scores = torch.empty((s.T, s.Hkv, s.max_blocks), dtype=torch.float32, device=dev)
-        given, made = (), (block_scores,)
-    _paged_call((_lib or lib()).msa_paged_block_scores, s, OP_PAGED_BLOCK_SCORES, dev,
-                (q_idx, k_idx, block_table, q_starts, row_req, row_pos, *given), made, workspace)
-    return block_scores
+    return _paged(shape, OP_PAGED_BLOCK_SCORES, workspace, stream, q_idx, k_idx, block_table, q_starts, row_req, row_pos,
+                  block_scores)[0]
 
 
 def paged_block_topk(shape: PagedShape, block_scores, row_pos, *, sel_idx=None, workspace=None, stream=None):
     """msa_paged_block_topk: sel_idx [T, Hkv, topk] int32 of block_scores [T, Hkv, max_blocks]."""
-    s, dev = shape, block_scores.device
-    place = _place(dev, stream)
-    if place is not None:
-        with place:
-            return paged_block_topk(s, block_scores, row_pos, sel_idx=sel_idx, workspace=workspace)
-    given, made = (sel_idx,), ()
-    if sel_idx is None:
-        sel_idx = torch.empty((s.T, s.Hkv, s.topk), dtype=torch.int32, device=dev)
-        given, made = (), (sel_idx,)
-    _paged_call((_lib or lib()).msa_paged_block_topk, s, OP_PAGED_BLOCK_TOPK, dev, (block_scores, row_pos, *given), made, workspace)
-    return sel_idx
+    return _paged(shape, OP_PAGED_BLOCK_TOPK, workspace, stream, block_scores, row_pos, sel_idx)[0]
 
 
 def paged_attn(shape: PagedShape, q, k8, v8, k_scale, v_scale, block_table, row_req, row_pos, *, sel_idx=None, o=None,
                lse=None, workspace=None, stream=None):
     """msa_paged_attn: (o [T, Hq, d] bf16, lse [T, Hq] fp32) of q [T, Hq, d] bf16 over
     the 8-bit cache: the blocks of sel_idx [T, Hkv, topk], or all of them when it is None."""
-    s, dev = shape, q.device
-    place = _place(dev, stream)
-    if place is not None:
-        with place:
-            return paged_attn(s, q, k8, v8, k_scale, v_scale, block_table, row_req, row_pos, sel_idx=sel_idx, o=o, lse=lse, workspace=workspace)
-    if o is None and lse is None:
-        o, lse = torch.empty((s.T, s.Hq, s.d), dtype=torch.bfloat16, device=dev), torch.empty((s.T, s.Hq), dtype=torch.float32, device=dev)
-        given, made = (), (o, lse)
-    else:
-        o = torch.empty((s.T, s.Hq, s.d), dtype=torch.bfloat16, device=dev) if o is None else o
-        lse = torch.empty((s.T, s.Hq), dtype=torch.float32, device=dev) if lse is None else lse
-        given, made = (o, lse), ()
-    _paged_call((_lib or lib()).msa_paged_attn, s, OP_PAGED_ATTN, dev,
-                (q, k8, v8, k_scale, v_scale, block_table, row_req, row_pos, sel_idx, *given), made, workspace)
-    return o, lse
+    return _paged(shape, OP_PAGED_ATTN, workspace, stream, q, k8, v8, k_scale, v_scale, block_table, row_req, row_pos, sel_idx, o, lse)
 
 
 def check_device_status(workspace, stream=None) -> None:

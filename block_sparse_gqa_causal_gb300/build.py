@@ -1,7 +1,9 @@
-"""Build libmsa.so (the CUDA library) in-tree with nvcc for sm_103a.
+"""Build libmsa.so (the CUDA library) in-tree with nvcc for sm_103a, and
+_paged_binding.so (the paged calls' Python binding) with the host compiler.
 
 Each .cu under csrc/ compiles to an object in parallel; the objects link
-into block_sparse_gqa_causal_gb300/libmsa.so.  No torch involvement.
+into block_sparse_gqa_causal_gb300/libmsa.so, without torch.  The binding is
+compiled against the torch that is installed and linked with libmsa.so.
 """
 from __future__ import annotations
 
@@ -9,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -16,6 +19,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmsa.so")
+BINDING = os.path.join(HERE, "_paged_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I" + os.path.join(ROOT, "include"), "-I" + CSRC]
@@ -39,6 +43,24 @@ def _stale(out: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _binding_commands(out: str):
+    """The object of the binding (named by the versions it is compiled for) and the commands that make and link it."""
+    import torch
+    at = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    inc = [os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include"), os.path.join(ROOT, "include")]
+    src = os.path.join(CSRC, "paged_binding.cpp")
+    obj = os.path.join(BUILD, f"paged_binding-{torch.__version__}-py{sysconfig.get_python_version()}.o")
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={abi}", *["-I" + i for i in inc], "-c", src, "-o", obj]
+    libs = os.path.join(at, "lib")
+    link = [cxx, "-shared", "-o", out, obj, LIB, "-Wl,-rpath,$ORIGIN", "-L" + libs, "-Wl,-rpath," + libs, "-ltorch_python", "-ltorch",
+            "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    return src, obj, compile_, link
+
+
 def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
@@ -54,20 +76,28 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) 
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
 
+    bsrc, bobj, bcompile, blink = _binding_commands(BINDING + ".tmp")
+    bstale = force or _stale(bobj, [bsrc, headers[-1]])
+    if bstale:
+        jobs.append(bcompile)
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0 or verbose or ptxas_info:
             sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {cmd[-3]}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed for {cmd[-3]}")
 
     if jobs:
         with ThreadPoolExecutor(min(len(jobs), os.cpu_count() or 4)) as ex:
             list(ex.map(run, jobs))
     if force or jobs or _stale(LIB, objs):
         tmp = LIB + ".tmp"
-        run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs])
+        run([nvcc(), *ARCH, "-shared", "-Xlinker", "-soname", "-Xlinker", os.path.basename(LIB), "-o", tmp, *objs])
         os.replace(tmp, LIB)
+    if bstale or _stale(BINDING, [bobj, LIB]):
+        run(blink)
+        os.replace(BINDING + ".tmp", BINDING)
     return LIB
 
 

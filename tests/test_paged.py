@@ -119,6 +119,29 @@ def test_binding_refuses_host_tensors_shapes_and_types(api):
         api.paged_attn(sh, torch.zeros(8, 8, 64, dtype=torch.bfloat16), None, None, None, None, None, None, None)
 
 
+def test_shapes_are_copied_without_their_handles(api):
+    import copy
+    import pickle
+    sh = api.PagedShape(**GOOD)
+    assert set(sh._calls) == set(range(16, 21))
+    for other in (copy.deepcopy(sh), pickle.loads(pickle.dumps(sh))):
+        assert other == sh and "_calls" not in vars(other) and other._calls.keys() == sh._calls.keys()
+
+
+def test_binding_names_what_it_refuses(api):
+    import torch
+    sh = api.PagedShape(**GOOD)
+    call, h = api.binding().call, sh._calls[api.OP_PAGED_BLOCK_TOPK]
+    ws, s, p = torch.zeros(256, dtype=torch.uint8), torch.zeros(8, 2, 16), torch.zeros(8, dtype=torch.int32)
+    for args, what in (((s, None, None), "row_pos is None"), ((s.double(), p, None), "block_scores: need a contiguous Float"),
+                       ((s.transpose(0, 1).contiguous().transpose(0, 1), p, None), "contiguous=0"), ((3, p, None), "block_scores: need a tensor"),
+                       ((s, p[:7], None), r"row_pos.*\[8\].*\[7\]"), ((s, p, None), "need CUDA tensors, got cpu")):
+        with pytest.raises(ValueError, match=what):
+            call(h, ws, *args)
+    with pytest.raises(TypeError, match="3 tensors expected"):
+        call(h, ws, s, p)
+
+
 # ------------------------------------------------------------------ the reference's pins
 def test_e4m3_reference_against_torch():
     import torch
