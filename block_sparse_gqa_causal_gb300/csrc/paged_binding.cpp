@@ -161,12 +161,34 @@ PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t nargs)
 
     const at::DeviceGuard guard(*dev);
     at::Tensor fresh[kMostArgs];
-    if (made)
-        for (size_t i = 0; i < n; ++i)
-            if (c->args[i].kind == kOutput && args[2 + i] == Py_None) {
-                fresh[i] = at::empty(c->args[i].shape, at::TensorOptions().dtype(c->args[i].dtype).device(*dev));
-                ptr[i] = fresh[i].data_ptr();
+    if (made) {
+        // several outputs of one type share an allocation (a plan has seven, and allocating them took longer than the plan)
+        bool together = made > 1;
+        int64_t total = 0, start[kMostArgs];
+        const Arg *one = nullptr;
+        for (size_t i = 0; i < n; ++i) {
+            const Arg &a = c->args[i];
+            if (a.kind != kOutput || args[2 + i] != Py_None) continue;
+            if (!one) one = &a;
+            together = together && a.dtype == one->dtype;
+            start[i] = total;
+            total += (c10::multiply_integers(a.shape) + 63) / 64 * 64;
+        }
+        at::Tensor all;
+        if (together) all = at::empty({total}, at::TensorOptions().dtype(one->dtype).device(*dev));
+        for (size_t i = 0; i < n; ++i) {
+            const Arg &a = c->args[i];
+            if (a.kind != kOutput || args[2 + i] != Py_None) continue;
+            if (together) {
+                fresh[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+                fresh[i].unsafeGetTensorImpl()->set_storage_offset(start[i]);
+                fresh[i].unsafeGetTensorImpl()->set_sizes_contiguous(a.shape);
+            } else {
+                fresh[i] = at::empty(a.shape, at::TensorOptions().dtype(a.dtype).device(*dev));
             }
+            ptr[i] = fresh[i].data_ptr();
+        }
+    }
     const int status = launch(*c, ptr, ws.data_ptr(), (size_t)ws.numel(), c10::cuda::getCurrentCUDAStream(dev->index()).stream());
     if (status != MSA_OK) return PyLong_FromLong(status);
     PyObject *out = PyTuple_New(outputs);

@@ -127,12 +127,18 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedProblem p, PlanArgs a, 
         __syncthreads();
         if (lane == 31) warp_sum[warp] = inc;
         __syncthreads();
-        Sums before{}, all{};
-        for (int w = 0; w < nwarp; ++w) {
-            if (w < warp) before = before + warp_sum[w];
-            all = all + warp_sum[w];
+        if (warp == 0) {                                         // the warps' sums, summed up in turn
+            Sums w = lane < nwarp ? warp_sum[lane] : Sums{};
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const Sums o = shfl_up(w, d);
+                if (lane >= d) w = w + o;
+            }
+            warp_sum[lane] = w;
         }
-        total = all;
+        __syncthreads();
+        const Sums before = warp ? warp_sum[warp - 1] : Sums{};
+        total = warp_sum[31];
         return Sums{before.rows + inc.rows - x.rows, before.take + inc.take - x.take, before.gone + inc.gone - x.gone,
                     before.segs + inc.segs - x.segs};
     };
