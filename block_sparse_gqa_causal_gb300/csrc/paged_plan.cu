@@ -11,8 +11,8 @@
 // One CTA sums (the work is a few thousand integers; latency is all there is)
 // and decides whether the step fits before anything is written.  Rows are
 // independent after that: a row finds its request by bisection of q_starts.
-// Up to kFusedRows rows the same CTA fills them, a launch fewer; above that a
-// second kernel does.  64 decoding requests take 3 us; 256 requests with
+// Up to kFusedRows rows (one to a thread) the same CTA fills them, a launch
+// fewer; above that a second kernel does (4,000 rows: 5 us against 8).  64 decoding requests take 3 us; 256 requests with
 // 32,768 new tokens in tables of 1,024 columns, some ending, 16 us.
 #include <algorithm>
 
@@ -21,7 +21,7 @@
 namespace msa {
 namespace {
 
-constexpr int kFusedRows = 4096;
+constexpr int kFusedRows = 1024;
 constexpr int kFillThreads = 256;
 constexpr int kCopied = 2048;            // requests whose first rows a CTA copies
 
@@ -52,7 +52,8 @@ __device__ __forceinline__ void fill_entry(const PagedProblem &p, const PlanArgs
     int32_t *entry = a.block_table + (long long)lo * p.max_blocks + blk;
     int page;
     if (blk >= rq.w) {
-        page = a.free_pages[((long long)head + rq.x + (blk - rq.w)) % p.n_pages];
+        const int at = head + rq.x + (blk - rq.w);   // under twice the ring: its takes are at most its pages
+        page = a.free_pages[at < p.n_pages ? at : at - p.n_pages];
         if (off == 0) *entry = page;            // every page taken is opened by one row of the step
     } else {
         page = *entry;                          // the partly filled last page
@@ -199,6 +200,8 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedProblem p, PlanArgs a, 
             for (int i = warp; i < n_ended; i += nwarp) {
                 const int3 e = ended[i];
                 const int32_t *row = a.block_table + (long long)e.x * p.max_blocks;
+                const int first = (int)(((long long)head + count + e.z) % p.n_pages);
+                auto place = [&](int j) { return first + j < p.n_pages ? first + j : first + j - p.n_pages; };
                 constexpr int U = 16;                            // loads in flight before the stores they may not pass
                 for (int j0 = lane; j0 < e.y; j0 += 32 * U) {
                     int32_t page[U];
@@ -206,7 +209,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedProblem p, PlanArgs a, 
                     for (int u = 0; u < U; ++u) page[u] = j0 + 32 * u < e.y ? row[j0 + 32 * u] : 0;
 #pragma unroll
                     for (int u = 0; u < U; ++u)
-                        if (j0 + 32 * u < e.y) a.free_pages[((long long)head + count + e.z + j0 + 32 * u) % p.n_pages] = page[u];
+                        if (j0 + 32 * u < e.y) a.free_pages[place(j0 + 32 * u)] = page[u];
                 }
             }
             __syncthreads();
