@@ -74,6 +74,7 @@ cudaError_t launch_chained(const char *name, void (*kernel)(P...), dim3 grid, in
     TimedLaunch timed_(name, s);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
     if (e == cudaSuccess) note_launch();
+    else cudaGetLastError();                 // reported by this call: not left for the next one to find
     return e;
 }
 
@@ -88,6 +89,7 @@ cudaError_t allow_smem(K *kernel, int bytes, std::atomic<unsigned long long> &do
     if (bit & done.load(std::memory_order_acquire)) return cudaSuccess;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess && bit) done.fetch_or(bit, std::memory_order_release);
+    if (e != cudaSuccess) cudaGetLastError();
     return e;
 }
 

@@ -2,18 +2,19 @@
 // per (row, group) the row's own block and the topk - 1 earlier ones of
 // largest score, ties to the lower block.
 //
-// Candidates are ranked by 64-bit keys (score, then lower block), all
-// distinct, so the order is total and the result does not depend on how the
-// work is split.  A warp takes 1,024 blocks at a time, 32 to a lane, in
-// registers.  The (topk-1)-th largest of the 32 lanes' maxima is a lower bound
-// of the (topk-1)-th best score, and only about twenty of 1,024 scores in
-// random order reach it: these alone are listed, sorted across the lanes and
-// merged into the warp's 32 best.  (Scores that tie make the list longer, not
-// wrong.)  Every score is read once; what is left is a few hundred
-// instructions a row.  Rows of more than 1,024 blocks are cut over a CTA's
-// warps, whose lists the first warp merges.  8,000 rows over 1,024 blocks take
-// 9 us (the sorting networks' shuffles; reading the scores takes 2.5), 512 rows
-// of 256 blocks 3 us.
+// The order is total (score, then lower block), so the result does not depend
+// on how the work is split.  A warp takes 1,024 blocks at a time, 32 to a lane,
+// in registers.  The (topk-1)-th largest of the 32 lanes' maxima is a lower
+// bound of the (topk-1)-th best score, and only about twenty of 1,024 scores in
+// random order reach it: these alone are listed.  Where they are at most 32,
+// one to a lane, and the row has no other tile, one sort of their scores gives
+// the last score that is in, and the equals of it that fit are found apart.
+// Else (scores that tie make the list longer, not wrong) they are ranked by
+// 64-bit keys and merged into the warp's 32 best, and rows of more than 1,024
+// blocks are cut over a CTA's warps, whose lists the first warp merges.  8,000
+// rows over 1,024 blocks take 8 us (the sorting networks' shuffles; reading
+// the scores takes 2.5; 9 with a 64-bit sort of every list), 512 rows of 256
+// blocks 3 us.
 #include <algorithm>
 
 #include "paged.h"
@@ -76,19 +77,36 @@ topk_kernel(PagedProblem p, const float *__restrict__ scores, const int32_t *__r
     }
     const float *sc = scores + row * p.max_blocks;
     unsigned long long best = 0;                              // this lane's of the warp's 32 best; 0: none
+    uint32_t picked = 0;                                      // or the selection itself, 2^32 - 1 - block; 0: none
+    bool done = false;
     if (c0 >= k && k > 1) {
         int *mine = list[warp];
         for (int base = (W == 1 ? 0 : warp) * kTile; base < c0; base += W * kTile) {
             const int n = min(kTile, c0 - base), mine_n = (n - lane + 31) / 32;   // this lane's: blocks base + lane + 32 i
             float v[kPer], top = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) v[i] = i < mine_n ? sc[base + i * 32 + lane] : -INFINITY;
+            for (int g = 0; g < kPer; g += 8) {
+                if (g * 32 < n) {                             // the warp's eights that hold blocks at all
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) top = fmaxf(top, v[i]);   // passes NaN over
+                    for (int i = g; i < g + 8; ++i) v[i] = i < mine_n ? sc[base + i * 32 + lane] : -INFINITY;
+                }
+            }
+#pragma unroll
+            for (int g = 0; g < kPer; g += 8)
+                if (g * 32 < n) {
+#pragma unroll
+                    for (int i = g; i < g + 8; ++i) top = fmaxf(top, v[i]);   // passes NaN over
+                }
             const float bound = fmaxf(__shfl_sync(0xffffffffu, sort_desc(top, lane), k - 2), worst(shfl64(best, k - 2)));
             uint32_t in = 0;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) in |= (fmaxf(v[i], -INFINITY) >= bound ? 1u : 0u) << i;   // a NaN ranks last
+            for (int g = 0; g < kPer; g += 8)
+                if (g * 32 < n) {
+#pragma unroll
+                    for (int i = g; i < g + 8; ++i)
+                        if (v[i] >= bound) in |= 1u << i;
+                }
+            if (bound == -INFINITY) in = ~0u;                 // a NaN ranks last: with -inf
             in &= mine_n >= 32 ? ~0u : mine_n > 0 ? (1u << mine_n) - 1 : 0u;
             int at = __popc(in), m = at;
 #pragma unroll
@@ -100,6 +118,26 @@ topk_kernel(PagedProblem p, const float *__restrict__ scores, const int32_t *__r
             at -= __popc(in);
             for (; in; in &= in - 1) mine[at++] = base + lane + 32 * (__ffs(in) - 1);
             __syncwarp();
+            if (W == 1 && m <= 32 && c0 <= kTile) {
+                // all of the row's candidates, one to a lane: those above the (topk-1)-th score, and of its equals the
+                // lowest blocks
+                int c = lane < m ? mine[lane] : 0;
+                float x = lane < m ? fmaxf(sc[c], -INFINITY) : -INFINITY;
+                const float last = __shfl_sync(0xffffffffu, sort_desc(x, lane), k - 2);
+                bool take = lane < m && x > last;
+                const bool equal = lane < m && x == last;
+                const int room = k - 1 - __popc(__ballot_sync(0xffffffffu, take));
+                if (__popc(__ballot_sync(0xffffffffu, equal)) > room) {
+                    const uint32_t order = sort_desc(equal ? 0xFFFFFFFFu - (uint32_t)c : 0u, lane);
+                    const uint32_t least = __shfl_sync(0xffffffffu, order, room - 1);
+                    take = take || (equal && 0xFFFFFFFFu - (uint32_t)c >= least);
+                } else {
+                    take = take || equal;
+                }
+                picked = take ? 0xFFFFFFFFu - (uint32_t)c : 0u;
+                done = true;
+                break;
+            }
             for (int i = 0; i < m; i += 32) {
                 unsigned long long key = 0;
                 if (i + lane < m) {
@@ -130,12 +168,12 @@ topk_kernel(PagedProblem p, const float *__restrict__ scores, const int32_t *__r
     uint32_t c = 0;
     if (c0 < k) {
         if (lane <= c0) c = 0xFFFFFFFFu - (uint32_t)lane;
-    } else if (lane < k - 1) {
-        c = (uint32_t)best;                                   // a key's low half
-    } else if (lane == k - 1) {
-        c = 0xFFFFFFFFu - (uint32_t)c0;
+    } else {
+        // the row's own block is the last: it needs no place in the sort
+        c = done ? picked : lane < k - 1 ? (uint32_t)best : 0u;   // a key's low half
     }
     c = sort_desc(c, lane);
+    if (c0 >= k && lane == k - 1) c = 0xFFFFFFFFu - (uint32_t)c0;
     if (lane < k) sel[row * k + lane] = c ? (int32_t)(0xFFFFFFFFu - c) : -1;
 }
 
