@@ -38,7 +38,8 @@
 // the next page's S before this page's P V; four warps, a token to a thread,
 // turn scores into probabilities.  A stretch cuts at most two rows; those pieces' states go to
 // the workspace, and the CTA that ends the last piece of a row joins them, in
-// their order along the row.
+// their order along the row (more than kOneGo by eights: one request of 65,536
+// tokens attending to everything, 38 pieces a row, 40 us in one go, 34 so).
 //
 // At 64 rows x 8 groups x 16 blocks of d = 128 (264 MB) 53 us: it streams at
 // the copy rate for 40, the first page is there after 6, and the last CTA ends
@@ -62,7 +63,11 @@ constexpr int kQueries = 4;                     // pieces whose queries are held
 constexpr int kColumns = 64;                    // TMEM: two S buffers and O, 16 columns each
 constexpr int kPrefixRows = 384;                // most rows whose blocks are cut evenly; above, whole rows are dealt out
 constexpr int kMinBlocks = 2;                   // a stretch has at least this many blocks
-constexpr int kArrivedWords = (4096 - kStatusBytes) / 4;   // the workspace's counts, one to a stretch
+// The workspace's counts, three to a stretch: of the row that it cuts off, of eight pieces from it on that another
+// stretch's row has, and of the first eight of its own.
+constexpr int kArrivedWords = (4096 - kStatusBytes) / 4;
+constexpr int kMostCtas = kArrivedWords / 3;
+constexpr int kOneGo = 16;                      // pieces of a row that are joined in one go
 constexpr int kWholeBlocks = 4;                 // rows of up to so many blocks are not cut
 
 enum { kFirst = 1, kLast = 2, kEnd = 4 };       // of a piece; of the CTA's stretch
@@ -203,7 +208,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = p.G;
     const bool even = arrived != nullptr;         // stretches of equal length; else whole rows are dealt out
 
-    // blocks that a group of row t has to look at; 0: not a row (entries of a selection may sit in any of its slots)
+    // blocks (of a selection: slots, as many as the row can fill) that a group of row t has to look at; 0: not a row
     auto blocks_of = [&](int t, int &req, int &pos) {
         req = row_req[t];
         pos = row_pos[t];
@@ -212,7 +217,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
             report(st, kDevCheck, 141, req >= p.R ? req : pos);
             return 0;
         }
-        return sel ? p.topk : pos / kPage + 1;
+        return sel ? min(p.topk, pos / kPage + 1) : pos / kPage + 1;
     };
     if (smem_u32(raw) & 1023u) {                // the swizzled tiles' alignment
         if (tid == 0) report(st, kDevCheck, 157, (int)smem_u32(raw));
@@ -316,7 +321,8 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
             for (int base = j0; base < j1; base += 32) {
                 int c = -1;
                 if (sel) {
-                    // selected blocks ascend; an entry that does not, or lies past the row's own block, is no block
+                    // selected blocks ascend; an entry that does not, lies past the row's own block, or behind the slots
+                    // that the row's blocks can fill, is no block
                     c = lane < p.topk ? sel[((long long)t * p.Hkv + r) * p.topk + lane] : -1;
                     int most = c;
 #pragma unroll
@@ -325,7 +331,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                         if (lane >= d) most = max(most, v);
                     }
                     most = __shfl_up_sync(0xffffffffu, most, 1);
-                    if (c >= 0 && (c > c0 || (lane > 0 && c <= most))) {
+                    if (c >= 0 && (c > c0 || lane > c0 || (lane > 0 && c <= most))) {
                         report(st, kDevCheck, 142, c);
                         c = -1;
                     }
@@ -542,57 +548,81 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
 #pragma unroll
         for (int h = 0; h < 8; ++h) m_ref[h] = -INFINITY, l[h] = fq[h] = 0.f;
 
-        // The last CTA to hand in a piece of a cut row joins them all (and has left the count at zero).  The count
-        // comes back while the next page is worked on.
+        // The last CTA to hand in a piece of a row joins them; of many pieces, first the eight next to each other, and the
+        // last to do that for a row the eights (each leaves its count at zero).  The first count comes back while the
+        // next page is worked on.
         auto join = [&]() {
-            const int n = cut_n;
+            const int n = cut_n, eights = n <= kOneGo ? 1 : (n + 7) / 8, mine = n <= kOneGo ? 0 : ((int)blockIdx.x - cut_first) / 8;
             cut_n = 0;
-            if (!any_of(tid == 0 && before_me == (unsigned)n - 1)) return;
-            __threadfence();
-            constexpr int U = 4, E = 8 * D / (32 * kWarps * 4);   // pieces, and float4s of a thread, in flight together
-            float M[E], L[E];
-            float4 y[E];
+            int start = cut_first + 8 * mine, stride = 1, count = n <= kOneGo ? n : min(8, n - 8 * mine);
+            if (!any_of(tid == 0 && before_me == (unsigned)count - 1)) return;
+            for (;;) {
+                __threadfence();
+                constexpr int U = 4, E = 8 * D / (32 * kWarps * 4);   // states, and float4s of a thread, in flight together
+                float M[E], L[E];
+                float4 y[E];
+                auto part = [&](int j) { return 2LL * (start + j * stride) + (start + j * stride == cut_first ? 1 : 0); };
 #pragma unroll
-            for (int e = 0; e < E; ++e) M[e] = -INFINITY, L[e] = 0.f, y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int i0 = 0; i0 < n; i0 += U) {
-                float2 ml[E][U];
-                float4 x[E][U];
+                for (int e = 0; e < E; ++e) M[e] = -INFINITY, L[e] = 0.f, y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int i0 = 0; i0 < count; i0 += U) {
+                    float2 ml[E][U];
+                    float4 x[E][U];
 #pragma unroll
-                for (int e = 0; e < E; ++e)
+                    for (int e = 0; e < E; ++e)
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int idx = min((tid + e * 32 * kWarps) * 4, G * D - 4), j = min(i0 + u, n - 1);
-                        const long long part = 2 * (cut_first + j) + (j == 0 ? 1 : 0);
-                        ml[e][u] = __ldcg(part_ml + part * 8 + idx / D);
-                        x[e][u] = __ldcg(reinterpret_cast<const float4 *>(part_o + part * 8 * D + idx));
-                    }
+                        for (int u = 0; u < U; ++u) {
+                            const int idx = min((tid + e * 32 * kWarps) * 4, G * D - 4);
+                            const long long at = part(min(i0 + u, count - 1));
+                            ml[e][u] = __ldcg(part_ml + at * 8 + idx / D);
+                            x[e][u] = __ldcg(reinterpret_cast<const float4 *>(part_o + at * 8 * D + idx));
+                        }
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    float m = M[e];
+                    for (int e = 0; e < E; ++e) {
+                        float m = M[e];
 #pragma unroll
-                    for (int u = 0; u < U; ++u) m = fmaxf(m, ml[e][u].x);
-                    const float keep = M[e] == -INFINITY ? 1.f : ex2(M[e] - m);   // an empty state is all zeros, one of NaN scores NaN
-                    M[e] = m;
-                    L[e] *= keep;
-                    y[e] = make_float4(y[e].x * keep, y[e].y * keep, y[e].z * keep, y[e].w * keep);
+                        for (int u = 0; u < U; ++u) m = fmaxf(m, ml[e][u].x);
+                        const float keep = M[e] == -INFINITY ? 1.f : ex2(M[e] - m);   // an empty state is all zeros, one of NaN scores NaN
+                        M[e] = m;
+                        L[e] *= keep;
+                        y[e] = make_float4(y[e].x * keep, y[e].y * keep, y[e].z * keep, y[e].w * keep);
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        if (i0 + u >= n) break;
-                        const float f = ml[e][u].x == -INFINITY ? 1.f : ex2(ml[e][u].x - m);
-                        L[e] = fmaf(f, ml[e][u].y, L[e]);
-                        y[e] = make_float4(fmaf(f, x[e][u].x, y[e].x), fmaf(f, x[e][u].y, y[e].y), fmaf(f, x[e][u].z, y[e].z),
-                                           fmaf(f, x[e][u].w, y[e].w));
+                        for (int u = 0; u < U; ++u) {
+                            if (i0 + u >= count) break;
+                            const float f = ml[e][u].x == -INFINITY ? 1.f : ex2(ml[e][u].x - m);
+                            L[e] = fmaf(f, ml[e][u].y, L[e]);
+                            y[e] = make_float4(fmaf(f, x[e][u].x, y[e].x), fmaf(f, x[e][u].y, y[e].y), fmaf(f, x[e][u].z, y[e].z),
+                                               fmaf(f, x[e][u].w, y[e].w));
+                        }
                     }
                 }
-            }
+                const bool all = eights == 1 || stride == 8;
+                const long long to = part(0);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int idx = (tid + e * 32 * kWarps) * 4;
-                if (idx >= G * D) break;
-                const float z = L[e] == 0.f ? 0.f : 1.f / L[e];
-                *reinterpret_cast<uint2 *>(o + cut_row * D + idx) =
-                    make_uint2(pack_bf16(y[e].x * z, y[e].y * z), pack_bf16(y[e].z * z, y[e].w * z));
-                if (idx % D == 0) lse[cut_row + idx / D] = (M[e] + log2f(L[e])) * kLn2;
+                for (int e = 0; e < E; ++e) {
+                    const int idx = (tid + e * 32 * kWarps) * 4;
+                    if (idx >= G * D) break;
+                    if (all) {
+                        const float z = L[e] == 0.f ? 0.f : 1.f / L[e];
+                        *reinterpret_cast<uint2 *>(o + cut_row * D + idx) =
+                            make_uint2(pack_bf16(y[e].x * z, y[e].y * z), pack_bf16(y[e].z * z, y[e].w * z));
+                        if (idx % D == 0) lse[cut_row + idx / D] = (M[e] + log2f(L[e])) * kLn2;
+                    } else {                           // where the first of the eight was; every thread has read what it replaces
+                        *reinterpret_cast<float4 *>(part_o + to * 8 * D + idx) = y[e];
+                    }
+                }
+                if (all) return;
+                named_bar_sync(1, 32 * kWarps);        // the sums of the first have been read by all
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int idx = (tid + e * 32 * kWarps) * 4;
+                    if (idx < G * D && idx % D == 0) part_ml[to * 8 + idx / D] = make_float2(M[e], L[e]);
+                }
+                __threadfence();
+                named_bar_sync(1, 32 * kWarps);
+                if (!any_of(tid == 0 && atomicInc(&arrived[cut_first], eights - 1) == (unsigned)eights - 1)) return;
+                start = cut_first;
+                stride = 8;
+                count = eights;
             }
         };
 
@@ -713,7 +743,12 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
             if (whole) continue;
             __threadfence();                           // the state before the count
             named_bar_sync(1, 32 * kWarps);
-            if (tid == 0) before_me = atomicInc(&arrived[me.first], me.n - 1);
+            if (tid == 0) {
+                // the count of the piece's eight, or of the row where it has few
+                const int eight = ((int)blockIdx.x - me.first) / 8;
+                const int at = me.n <= kOneGo ? me.first : (eight == 0 ? 2 : 1) * kMostCtas + me.first + 8 * eight;
+                before_me = atomicInc(&arrived[at], (me.n <= kOneGo ? me.n : min(8, me.n - 8 * eight)) - 1);
+            }
             cut_n = me.n;
             cut_first = me.first;
             cut_row = row;
@@ -733,7 +768,7 @@ bool cuts_rows(const PagedProblem &p, bool sparse)
 // Two CTAs to an SM, fewer where that leaves stretches under kMinBlocks.
 int attn_ctas(const PagedProblem &p, bool sparse)
 {
-    const long long rows = (long long)p.T * p.Hkv, most = std::min(2 * p.num_sms, kArrivedWords);
+    const long long rows = (long long)p.T * p.Hkv, most = std::min(2 * p.num_sms, kMostCtas);
     return (int)std::min(most, cuts_rows(p, sparse) ? rows * (sparse ? p.topk : p.max_blocks) / kMinBlocks : rows);
 }
 
@@ -751,7 +786,7 @@ cudaError_t launch_paged_attn(const PagedProblem &p, const bf16 *q, const uint8_
                               float *scratch, DeviceStatus *st, cudaStream_t s)
 {
     const int ctas = attn_ctas(p, sel != nullptr);
-    // one count per stretch, zero between calls, then the partial outputs and (reference, sum) pairs
+    // the counts, zero between calls, then the partial outputs and (reference, sum) pairs
     unsigned *arrived = cuts_rows(p, sel != nullptr) ? reinterpret_cast<unsigned *>(scratch) : nullptr;
     float *part_o = scratch + kArrivedWords;
     float2 *part_ml = reinterpret_cast<float2 *>(part_o + (size_t)2 * p.num_sms * 2 * 8 * p.d);

@@ -449,8 +449,10 @@ msa_status msa_paged_block_topk(const msa_paged_shape *shape, const float *block
  *   l_j = scale * <q[t, h, :], k_j>,  o = sum_j softmax(l)_j v_j,
  *   lse[t, h] = log sum_j exp(l_j).
  * q, o [T, Hq, d] bf16, lse [T, Hq] fp32, sel_idx [T, Hkv, topk] int32,
- * distinct and ascending with -1 anywhere; an entry that does not ascend or
- * lies past the row's own block is left out and recorded in the status word.
+ * distinct and ascending, then -1 (a -1 in between is passed over); an entry
+ * that does not ascend, lies past the row's own block c0, or sits behind the
+ * min(topk, c0 + 1) entries that the row can have, is left out and recorded in
+ * the status word.
  * A row without any block has o = 0 and lse = -inf.  Queries and
  * probabilities enter the products with 8 significant bits or more, sums are
  * fp32.  Deterministic.

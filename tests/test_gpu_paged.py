@@ -390,6 +390,9 @@ CASES = [
     dict(lens=[6000], q=[1], Hq=8, Hkv=8, d=128, k=16), dict(lens=[5000, 4097], q=[2, 1], Hq=8, Hkv=4, d=64, k=32),
     dict(lens=[300], q=[1], Hq=8, Hkv=1, d=64, k=1, max_blocks=50),
     dict(lens=[2100 + 37 * i for i in range(40)], q=[1] * 40, Hq=16, Hkv=8, d=64, k=16, max_blocks=40),       # rows of several CTAs, CTAs of several rows
+    dict(lens=[400, 130, 5, 1300], q=[1, 2, 1, 1], Hq=16, Hkv=2, d=128, k=16),                            # fewer blocks than slots
+    dict(lens=[38500], q=[1], Hq=8, Hkv=1, d=128, k=32),                                                 # a row in many pieces
+    dict(lens=[21000, 40000], q=[1, 1], Hq=4, Hkv=1, d=64, k=32),
     dict(lens=[400, 330], q=[300, 310], Hq=2, Hkv=1, d=64, k=2, pad=7),                                   # more rows than are cut
     dict(lens=[3000, 100, 7], q=[1, 1, 1], Hq=64, Hkv=8, d=128, k=16, max_blocks=200)]
 
@@ -429,6 +432,12 @@ def test_attention_leaves_out_bad_entries(api):
         with pytest.raises(api.MsaError):
             api.check_device_status(ws)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    short, a2, _, _ = attn_case(api, lens=[200], q=[1], Hq=4, Hkv=1, d=64, k=4, sparse=True)      # two blocks: two slots
+    ws = api.new_paged_workspace(short, api.OP_PAGED_ATTN)
+    got, want = (api.paged_attn(short, *a2, sel_idx=i32(np.array(s).reshape(1, 1, 4)), workspace=w) for s, w in (([-1, 0, 1, -1], ws), ([-1, 0, -1, -1], None)))
+    with pytest.raises(api.MsaError):
+        api.check_device_status(ws)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     for page in (-1, sh.n_pages, 2 ** 31 - 1):
         table = args[5].clone()
         table[0, 7] = page
