@@ -68,6 +68,10 @@ constexpr int kMinBlocks = 2;                   // a stretch has at least this m
 constexpr int kArrivedWords = (4096 - kStatusBytes) / 4;
 constexpr int kMostCtas = kArrivedWords / 3;
 constexpr int kOneGo = 16;                      // pieces of a row that are joined in one go
+// What a group of a row costs next to its blocks, in blocks (its queries, its outputs): 64 rows of up to 8 blocks x 8
+// groups 34 us without, 27 so.  Left out where a stretch would not get kMinBlocks without it.
+constexpr int kPieceCost = 1;
+constexpr int kCountShift = 48;                 // before[]: blocks below, rows that have any above
 constexpr int kWholeBlocks = 4;                 // rows of up to so many blocks are not cut
 
 enum { kFirst = 1, kLast = 2, kEnd = 4 };       // of a piece; of the CTA's stretch
@@ -201,7 +205,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
     __shared__ float sQ[2 * kQueries][8];       // logit factor of each head's queries, times log2 e
     __shared__ float sM[kWarps][8], sL[kWarps][8];
     __shared__ uint32_t tmem_slot;
-    __shared__ long long before[kPrefixRows + 1];   // blocks of the rows before each row, one group
+    __shared__ long long before[kPrefixRows + 1];   // blocks, and count, of the rows before each row, one group
     __shared__ int abort_flag;
 
     chain_next();
@@ -251,7 +255,8 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
     if (even)
         for (int t = tid; t < p.T; t += kThreads) {
             int req, pos;
-            before[t] = blocks_of(t, req, pos);
+            const int n = blocks_of(t, req, pos);
+            before[t] = n ? n | 1LL << kCountShift : 0;
         }
     __syncthreads();
     if (even && warp == 0) {
@@ -378,7 +383,11 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
         };
         const int me = blockIdx.x;
         if (even) {
-            const long long W = before[p.T] * p.Hkv;
+            constexpr long long kBlocks = (1LL << kCountShift) - 1;
+            const int cost = (before[p.T] & kBlocks) * p.Hkv / kMinBlocks > (long long)gridDim.x ? kPieceCost : 0;
+            // where row t starts in the list
+            auto begin = [&](int t) { return ((before[t] & kBlocks) + cost * (before[t] >> kCountShift)) * p.Hkv; };
+            const long long W = begin(p.T);
             const long long n = max(1LL, min((long long)gridDim.x, W / kMinBlocks));
             long long x = me < n ? W * me / n : 0;
             const long long x1 = me < n ? W * (me + 1) / n : 0;
@@ -388,22 +397,24 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                 int hi = p.T;
                 while (hi - t > 1) {
                     const int mid = (t + hi) >> 1;
-                    if (before[mid] * p.Hkv <= x) t = mid;
+                    if (begin(mid) <= x) t = mid;
                     else hi = mid;
                 }
             }
             while (x < x1 && live) {
-                const int nt = (int)(before[t + 1] - before[t]);
-                const long long y = x - before[t] * p.Hkv;
-                if (y >= (long long)nt * p.Hkv) {
+                if (x >= begin(t + 1)) {
                     ++t;
                     continue;
                 }
-                const int r = (int)(y / nt), j0 = (int)(y % nt), j1 = (int)min((long long)nt, j0 + (x1 - x));
+                const int nt = (int)((before[t + 1] - before[t]) & kBlocks), r = (int)((x - begin(t)) / (nt + cost));
+                const long long x0 = begin(t) + (long long)r * (nt + cost) + cost;   // where the group's blocks start
+                x = max(x, x0);
+                if (x >= x1) break;
+                const int j0 = (int)(x - x0), j1 = (int)min((long long)nt, x1 - x0);
                 const bool whole = j0 == 0 && j1 == nt;
-                const int f = whole ? 0 : holder(x - j0), last = whole ? 0 : holder(x - j0 + nt - 1);
+                const int f = whole ? 0 : holder(x0), last = whole ? 0 : holder(x0 + nt - 1);
                 piece(t, r, row_req[t], row_pos[t], j0, j1, whole ? -1 : 2 * me + (j0 > 0 ? 0 : 1), f, last - f + 1);
-                x += j1 - j0;
+                x = x0 + j1;
             }
         } else {
             const long long pairs = (long long)p.T * p.Hkv;

@@ -393,6 +393,7 @@ CASES = [
     dict(lens=[400, 130, 5, 1300], q=[1, 2, 1, 1], Hq=16, Hkv=2, d=128, k=16),                            # fewer blocks than slots
     dict(lens=[38500], q=[1], Hq=8, Hkv=1, d=128, k=32),                                                 # a row in many pieces
     dict(lens=[21000, 40000], q=[1, 1], Hq=4, Hkv=1, d=64, k=32),
+    dict(lens=[2 + 97 * i % 900 for i in range(120)], q=[1 + (i % 7 == 0) for i in range(120)], Hq=16, Hkv=4, d=64, k=8, pad=5),   # many short rows
     dict(lens=[400, 330], q=[300, 310], Hq=2, Hkv=1, d=64, k=2, pad=7),                                   # more rows than are cut
     dict(lens=[3000, 100, 7], q=[1, 1, 1], Hq=64, Hkv=8, d=128, k=16, max_blocks=200)]
 
