@@ -12,6 +12,10 @@ namespace msa {
 
 constexpr int kPage = 128;   // tokens of a page: one MSA block
 
+// The workspace's head: the status word, then the attention's arrival counts, zero between its calls.  No other call writes
+// there, so that the calls may share a workspace.
+constexpr size_t kHeadBytes = 4096;
+
 struct PagedProblem {
     int R, T, max_blocks, n_pages, Hq, Hkv, G, d, d_idx, topk;
     float scale, scale_idx;

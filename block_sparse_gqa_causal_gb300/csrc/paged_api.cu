@@ -73,7 +73,7 @@ msa_status make_paged(const msa_paged_shape *s, PagedProblem &p)
 size_t scratch_bytes(const PagedProblem &p, int op)
 {
     switch (op) {
-    case MSA_OP_PAGED_PLAN: return paged_plan_scratch_ints(p) * 4;
+    case MSA_OP_PAGED_PLAN: return kHeadBytes - kStatusBytes + paged_plan_scratch_ints(p) * 4;
     case MSA_OP_PAGED_ATTN: return paged_attn_scratch_floats(p) * 4;
     default: return 0;
     }
@@ -111,8 +111,6 @@ msa_status done(cudaError_t e, const char *what)
     return e == cudaSuccess ? MSA_OK : refuse(MSA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-template <class T>
-T *scratch(void *ws) { return reinterpret_cast<T *>(static_cast<char *>(ws) + kStatusBytes); }
 DeviceStatus *status(void *ws) { return static_cast<DeviceStatus *>(ws); }
 const bf16 *b16(const void *x) { return static_cast<const bf16 *>(x); }
 
@@ -147,7 +145,8 @@ msa_status msa_paged_plan(const msa_paged_shape *shape, const int32_t *new_lens,
     if ((uintptr_t)ended % 4) return refuse(MSA_ERR_INVALID_ARGUMENT, "ended is not 4-byte aligned");
     const PlanArgs a{new_lens, lens_in, ended, free_in, block_table, free_pages, lens_out, free_out, q_starts, row_req,
                      row_pos, slots, segs};
-    return done(launch_paged_plan(p, a, scratch<int32_t>(workspace), status(workspace), static_cast<cudaStream_t>(stream)),
+    int32_t *scratch = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + kHeadBytes);
+    return done(launch_paged_plan(p, a, scratch, status(workspace), static_cast<cudaStream_t>(stream)),
                 "paged_plan launch");
 }
 
@@ -220,7 +219,8 @@ msa_status msa_paged_attn(const msa_paged_shape *shape, const void *q, const voi
     if ((uintptr_t)sel_idx % 4) return refuse(MSA_ERR_INVALID_ARGUMENT, "sel_idx is not 4-byte aligned");
     return done(launch_paged_attn(p, b16(q), static_cast<const uint8_t *>(k8), static_cast<const uint8_t *>(v8), k_scale,
                                   v_scale, block_table, row_req, row_pos, sel_idx, static_cast<bf16 *>(o), lse,
-                                  scratch<float>(workspace), status(workspace), static_cast<cudaStream_t>(stream)),
+                                  reinterpret_cast<float *>(static_cast<char *>(workspace) + kStatusBytes), status(workspace),
+                                  static_cast<cudaStream_t>(stream)),
                 "paged_attn launch");
 }
 

@@ -29,17 +29,19 @@
 // of the largest weight.
 //
 // The work is one long list of blocks, those of (row 0, group 0), then (row 0,
-// group 1) and so on, cut into equal stretches for the two CTAs that each SM
-// holds, whatever the rows' lengths.  A planner warp walks the stretch a row
-// ahead (row, selection and block table are dependent loads, 2 us that would
-// empty the ring at every row) and lays down each row's queries; a
-// producer warp streams the pages through one ring of stages (K and V tiles of
-// a page and head, contiguous and swizzled by TMA); one warp issues the MMAs,
-// the next page's S before this page's P V; four warps, a token to a thread,
-// turn scores into probabilities.  A stretch cuts at most two rows; those pieces' states go to
-// the workspace, and the CTA that ends the last piece of a row joins them, in
-// their order along the row (more than kOneGo by eights: one request of 65,536
-// tokens attending to everything, 38 pieces a row, 40 us in one go, 34 so).
+// group 1) and so on, each group's led by kPieceCost that stands for what it
+// costs besides, cut into equal stretches for the two CTAs that each SM holds,
+// whatever the rows' lengths.  A planner warp walks the stretch a row ahead
+// (row, selection and block table are dependent loads, 2 us that would empty
+// the ring at every row) and lays down each row's queries; a producer warp
+// streams the pages through one ring of stages (K and V tiles of a page and
+// head, contiguous and swizzled by TMA); one warp issues the MMAs, the next
+// page's S before this page's P V; four warps, a token to a thread, turn scores
+// into probabilities.  A stretch cuts at most two rows; those pieces' states go
+// to the workspace, and the CTA that ends the last piece of a row joins them,
+// in their order along the row (more than kOneGo by eights: one request of
+// 65,536 tokens attending to everything, 38 pieces a row, 40 us in one go, 34
+// so).
 //
 // At 64 rows x 8 groups x 16 blocks of d = 128 (264 MB) 53 us: it streams at
 // the copy rate for 40, the first page is there after 6, and the last CTA ends
@@ -65,7 +67,7 @@ constexpr int kPrefixRows = 384;                // most rows whose blocks are cu
 constexpr int kMinBlocks = 2;                   // a stretch has at least this many blocks
 // The workspace's counts, three to a stretch: of the row that it cuts off, of eight pieces from it on that another
 // stretch's row has, and of the first eight of its own.
-constexpr int kArrivedWords = (4096 - kStatusBytes) / 4;
+constexpr int kArrivedWords = (kHeadBytes - kStatusBytes) / 4;
 constexpr int kMostCtas = kArrivedWords / 3;
 constexpr int kOneGo = 16;                      // pieces of a row that are joined in one go
 // What a group of a row costs next to its blocks, in blocks (its queries, its outputs): 64 rows of up to 8 blocks x 8
@@ -566,6 +568,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
             const int n = cut_n, eights = n <= kOneGo ? 1 : (n + 7) / 8, mine = n <= kOneGo ? 0 : ((int)blockIdx.x - cut_first) / 8;
             cut_n = 0;
             int start = cut_first + 8 * mine, stride = 1, count = n <= kOneGo ? n : min(8, n - 8 * mine);
+            if (tid == 0 && before_me >= (unsigned)count) report(st, kDevCheck, 164, (int)before_me);   // not zero before the call
             if (!any_of(tid == 0 && before_me == (unsigned)count - 1)) return;
             for (;;) {
                 __threadfence();

@@ -357,7 +357,9 @@ msa_status msa_kv_append(const msa_shape *shape, const void *k_new, const void *
  * and code arrays, 4-byte of the others.  Every call takes a workspace of
  * msa_paged_workspace_size bytes with the status word of the other calls; its
  * first 4,096 bytes (all of a smaller one) have to be zero before the first
- * call on it, and again after msa_check_device_status() reported a timeout.
+ * call on it, and again after msa_check_device_status() reported a timeout or
+ * after a call that is not of these five (which may leave anything behind byte
+ * 256); these five may share one, ordered on one stream.
  * What device memory says (lengths, pages, selections) is checked on the
  * device: an entry out of range is left out and recorded in the status word.
  * Outputs do not overlap inputs or one another, but where a call says so.

@@ -691,6 +691,22 @@ def test_two_streams_at_once(api):
             assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
 
 
+def test_one_workspace_for_every_call(api):
+    """The five calls in turn on one workspace, rows cut between CTAs: as on workspaces of their own."""
+    import torch
+    sizes = dict(R=3, nb=20, n_pages=60, Hq=16, Hkv=2, d=128, di=64, k=16, T=64, seed=3)
+    own, one = Server(api, **sizes), Server(api, **sizes)
+    most = max(w.numel() for w in one.ws.values())
+    space = torch.zeros(most, dtype=torch.uint8, device="cuda")
+    one.ws = {op: space for op in one.ws}
+    x = own.rows()
+    for new in [[30, 0, 34], [1, 60, 1]] * 12:
+        a, b = (s.step(i32(new), None, {n: v[0] for n, v in x.items()}) for s in (own, one))
+        status_ok(api, space)
+        n = sum(new)
+        assert torch.equal(a[3][:n], b[3][:n]) and torch.equal(a[4][:n], b[4][:n]) and torch.equal(a[2][:n], b[2][:n])
+
+
 def test_workspace_shared_by_graphs_replayed_in_turn(api):
     """Two graphs over one workspace, one after the other on a stream, as the workspace rule allows."""
     import torch

@@ -87,7 +87,7 @@ def test_append_wants_whole_groups(api):
 def test_workspace_sizes(api):
     sh = api.PagedShape(**GOOD)
     assert api.paged_workspace_size(sh, api.OP_PAGED_APPEND) == 256
-    assert api.paged_workspace_size(sh, api.OP_PAGED_PLAN) == 512          # 16 bytes and 16 a request
+    assert api.paged_workspace_size(sh, api.OP_PAGED_PLAN) == 4096 + 256   # behind the attention's counts: 16 bytes and 16 a request
     # attention: two states of a group's heads for each stretch, two to an SM, whatever the batch; none where rows are not cut
     for kw in (GOOD, {**GOOD, "T": 384}, {**GOOD, "T": 1, "R": 1, "max_blocks": 8192}, {**GOOD, "max_blocks": 4, "topk": 5}):
         s = api.PagedShape(**kw)
