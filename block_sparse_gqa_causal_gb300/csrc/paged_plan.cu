@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedProblem p, PlanArgs a, 
         }
         return q;
     };
-    // exclusive sum over the CTA's requests of this round; the round's total too
+    // exclusive sum over the CTA's requests of one pass; the pass's total too
     auto scan = [&](const Sums &x, Sums &total) {
         Sums inc = x;
 #pragma unroll
