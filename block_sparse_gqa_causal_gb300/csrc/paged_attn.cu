@@ -14,19 +14,29 @@
 // Sixteen columns are twice the heads, so the other operand is split in two
 // e4m3 terms: columns 0-7 hold the heads' leading terms hi = rn(x), columns
 // 8-15 lo = rn(16 (x - hi)), and hi + lo / 16 carries the 8 significant bits
-// of a bf16 query exactly, down to 2^-23 of the row's largest feature (queries
-// are scaled by a power of two to fill the range), and the probabilities with
-// the precision that bf16 gives them.  (mma.sync takes e4m3 too, but the
+// of a bf16 query exactly, features below 2^-14 of the row's largest to 2^-22 of
+// it (queries are scaled by a power of two to fill the range).  (mma.sync takes e4m3 too, but the
 // compiler turns each into two 16-bit MMAs and conversions: 800 instructions a
 // warp and page, which held the pages back.)
 //
 // With t_j = l_j log2 e + log2 vs, the weight of token j's codes is 2^t_j and
 // that of the sum 2^t_j / vs, so one reference m per head bounds both and the
 // products P V add up in TMEM across pages of different scales.  m is the
-// largest t so far, or up to 4 less: P = 16 * 2^(t - m) stays within 256 and
-// the sums are only rescaled when t has outgrown m by more than that, which
-// after a row's first page is rare.  P's small terms are off by at most 2^-18
-// of the largest weight.
+// largest t so far, or up to kLag = 3 less: P = 32 * 2^(t - m) stays within 256
+// and the sums are only rescaled when t has outgrown m by more than that, which
+// after a row's first page is rare.
+//
+// Two terms hold P = hi + lo / 32 to 8 significant bits from 256 down to 2^-7,
+// 12 binades below the reference.  That is not enough: thousands of tokens under
+// an attention sink weigh less than that each and more than the sink together.
+// So there are three levels, 2^15 apart, each with an O of its own in TMEM; a
+// probability has its terms in the level where it keeps its 8 bits and zeros in
+// the others, and the levels are joined when a row's outputs are written.  8 bits
+// are kept down to 2^-42 of the reference; a token below is off by 2^-50 of it.
+// A lower level's product is issued for those 32 tokens only (a warp's, a step of
+// the MMA) that have any there: near-uniform rows pay a vote, and under a sink
+// the dense case below takes 188 us instead of 184.  A page's probabilities take
+// the place of its K tile once its scores are there.
 //
 // The work is one long list of blocks, those of (row 0, group 0), then (row 0,
 // group 1) and so on, each group's led by kPieceCost that stands for what it
@@ -43,10 +53,10 @@
 // 65,536 tokens attending to everything, 38 pieces a row, 40 us in one go, 34
 // so).
 //
-// At 64 rows x 8 groups x 16 blocks of d = 128 (264 MB) 53 us: it streams at
+// At 64 rows x 8 groups x 16 blocks of d = 128 (264 MB) 54 us: it streams at
 // the copy rate for 40, the first page is there after 6, and the last CTA ends
 // 4 to 5 after the median one.  Every block of eight requests of up to 131,072
-// tokens (1.2 GB): 181 us, 98% of the copy rate.
+// tokens (1.2 GB): 183 us, 97% of the copy rate.
 #include <algorithm>
 #include <type_traits>
 
@@ -62,7 +72,15 @@ constexpr int kWarps = 4;                       // softmax warps, a token of the
 constexpr int kThreads = 32 * (kWarps + 3);     // then the producer, the MMA and the planner warp
 constexpr int kStages = 3;
 constexpr int kQueries = 4;                     // pieces whose queries are held
-constexpr int kColumns = 64;                    // TMEM: two S buffers and O, 16 columns each
+constexpr int kLevels = 3;                      // magnitudes of probabilities that are summed up apart
+constexpr float kLag = 3.f;                     // log2 of what a probability may outgrow its reference by
+constexpr float kOne = 32.f;                    // what the reference's probability is held as: all up to 2^kLag times that
+constexpr float kLo = 32.f;                     // scale of the low term: the high one is off by 8 at most (up to 256)
+constexpr float kLevelEnd = 1.f / 128;          // the least value of a level: there its two terms' 8 bits end
+constexpr float kLevelStep = 1 << 15;           // from one level's end to the next one's
+constexpr int kO = 32;                          // TMEM: two S buffers, then a level's O behind the other, 16 columns each
+constexpr int kColumns = 128;
+static_assert(kO + kLevels * 16 <= kColumns, "TMEM columns");
 constexpr int kPrefixRows = 384;                // most rows whose blocks are cut evenly; above, whole rows are dealt out
 constexpr int kMinBlocks = 2;                   // a stretch has at least this many blocks
 // The workspace's counts, three to a stretch: of the row that it cuts off, of eight pieces from it on that another
@@ -80,7 +98,7 @@ enum { kFirst = 1, kLast = 2, kEnd = 4 };       // of a piece; of the CTA's stre
 struct Meta {
     int len;        // visible tokens of the block
     float ks;       // the page's K scale for this head
-    float lv, il, pv;   // log2 of its V scale (-100 at least), 2^-lv, and 16 x what lv leaves of the scale (1)
+    float lv, il, pv;   // log2 of its V scale (-100 at least), 2^-lv, and kOne x what lv leaves of the scale (1)
     int flags;
     int t, r, q;    // the piece's row and group, and its number in the stretch
     int part;       // the piece's place among the partial states; -1: a whole row
@@ -101,8 +119,9 @@ struct AttnSmem {
     static constexpr int Q = 16 * D;            // a row's queries: hi and lo terms of 8 heads
     static constexpr int P = 16 * kPage;        // a page's probabilities, 16 bytes (hi and lo of 8 heads) to a token
     static constexpr int OFF_Q = kStages * STAGE;
-    static constexpr int OFF_P = OFF_Q + kQueries * Q;
-    static constexpr int BYTES = OFF_P + 2 * P;
+    static constexpr int BYTES = OFF_Q + kQueries * Q;
+    // a page's probabilities, a level behind the other, in its K tile
+    static_assert(kLevels * P <= TILE, "probabilities outgrow a K tile");
 };
 
 // byte offset of 16-byte word w of row r in a tile of D-byte rows, swizzled as TMA and the MMA descriptors do
@@ -174,13 +193,14 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t two)
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(h) : "h"((uint16_t)two));
     return __half22float2(*reinterpret_cast<__half2 *>(&h));
 }
-// x = hi + lo / 16 for four values within +-448
+// x = hi + lo / S for four values within +-448
+template <int S>
 __device__ __forceinline__ void split4(float x0, float x1, float x2, float x3, uint32_t &hi, uint32_t &lo)
 {
     const uint32_t h01 = e4m3x2(x0, x1), h23 = e4m3x2(x2, x3);
     const float2 f01 = from_e4m3x2(h01), f23 = from_e4m3x2(h23);
     hi = h01 | (h23 << 16);
-    lo = e4m3x2(16.f * (x0 - f01.x), 16.f * (x1 - f01.y)) | (e4m3x2(16.f * (x2 - f23.x), 16.f * (x3 - f23.y)) << 16);
+    lo = e4m3x2(S * (x0 - f01.x), S * (x1 - f01.y)) | (e4m3x2(S * (x2 - f23.x), S * (x3 - f23.y)) << 16);
 }
 
 MSA_DEV void mbar_expect_tx(uint64_t *bar, uint32_t bytes)
@@ -206,6 +226,8 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
     __shared__ Chunk chunk[2];
     __shared__ float sQ[2 * kQueries][8];       // logit factor of each head's queries, times log2 e
     __shared__ float sM[kWarps][8], sL[kWarps][8];
+    __shared__ uint32_t sLevels[2];             // levels below the first that a page has, a byte to a warp, a bit to a level
+    static_assert(kWarps == 4, "a byte to a warp");
     __shared__ uint32_t tmem_slot;
     __shared__ long long before[kPrefixRows + 1];   // blocks, and count, of the rows before each row, one group
     __shared__ int abort_flag;
@@ -307,8 +329,8 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
             for (int i = 0; i < D / 32; ++i) {
                 const float2 a = unpack_bf16(x[i].x), b = unpack_bf16(x[i].y), c = unpack_bf16(x[i].z), d = unpack_bf16(x[i].w);
                 uint2 hi, lo;
-                split4(a.x * inv, a.y * inv, b.x * inv, b.y * inv, hi.x, lo.x);
-                split4(c.x * inv, c.y * inv, d.x * inv, d.y * inv, hi.y, lo.y);
+                split4<16>(a.x * inv, a.y * inv, b.x * inv, b.y * inv, hi.x, lo.x);
+                split4<16>(c.x * inv, c.y * inv, d.x * inv, d.y * inv, hi.y, lo.y);
                 const int f = lane % 4 * (D / 4) + 8 * i;
                 *reinterpret_cast<uint2 *>(dst + at<D>(lane / 4, f >> 4) + (f & 15)) = hi;
                 *reinterpret_cast<uint2 *>(dst + at<D>(8 + lane / 4, f >> 4) + (f & 15)) = lo;
@@ -483,7 +505,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                 m.ks = __shfl_sync(0xffffffffu, ks, l);
                 m.lv = fmaxf(log2f(lane_vs), -100.f);
                 m.il = exp2f(-m.lv);
-                m.pv = 16.f * (lane_vs * m.il);
+                m.pv = kOne * (lane_vs * m.il);
                 if (lane == 0) {
                     meta[s] = m;
                     mbar_arrive(&full[s]);
@@ -506,7 +528,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
             }
             if ((m.flags & kFirst) && !mbar_wait_warp(&q_full[m.q % kQueries], (m.q / kQueries) & 1, st, 161, &abort_flag)) return false;
             fence_after_sync();
-            if (lane == 0) {
+            if (elect_one()) {
                 const uint64_t dk = tile_desc<D>(base + s * S::STAGE, 8 * D, 16), dq = tile_desc<D>(base + S::OFF_Q + m.q % kQueries * S::Q, 8 * D, 16);
 #pragma unroll
                 for (int k = 0; k < D / 32; ++k) mma_f8(tmem + (i & 1) * 16, desc_adv(dk, k * 32), desc_adv(dq, k * 32), kIdesc, k > 0);
@@ -536,18 +558,24 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
             const int s = i % kStages;
             fence_after_sync();
             const Meta m = meta[s];
-            if (lane == 0) {
+            uint32_t below = sLevels[i & 1];
+            if (elect_one()) {
                 const uint64_t dv = tile_desc<D>(base + s * S::STAGE + S::TILE, 8 * D, D == 128 ? 16 : 8 * D);
-                const uint64_t dp = rows16_desc(base + S::OFF_P + (i & 1) * S::P);
+                const uint64_t dp = rows16_desc(base + s * S::STAGE);
                 for (int k = 0; k < max(1, (m.len + 31) / 32); ++k)
-                    mma_f8(tmem + 32, desc_adv(dv, k * 32 * D), desc_adv(dp, k * 32 * 16), kIdesc | kAMajorMN | kBMajorMN, k > 0 || !(m.flags & kFirst));
+                    mma_f8(tmem + kO, desc_adv(dv, k * 32 * D), desc_adv(dp, k * 32 * 16), kIdesc | kAMajorMN | kBMajorMN, k > 0 || !(m.flags & kFirst));
+#pragma unroll 1
+                for (; below; below &= below - 1) {
+                    const int bit = __ffs(below) - 1, k = bit >> 3, v = bit & 7;   // warp k's 32 tokens, level v
+                    mma_f8(tmem + kO + 16 * v, desc_adv(dv, k * 32 * D), desc_adv(dp, v * S::P + k * 32 * 16), kIdesc | kAMajorMN | kBMajorMN, true);
+                }
                 mma_commit(&empty[s]);
                 mma_commit(&pv_done[i & 1]);
             }
             __syncwarp();
             if (!ahead) more = mbar_wait_warp(&full[(i + 1) % kStages], ((i + 1) / kStages) & 1, st, 149, &abort_flag) && scores(i + 1);
         }
-        if (lane == 0) mma_commit(&drained);
+        if (elect_one()) mma_commit(&drained);
         __syncwarp();
         mbar_wait_warp(&drained, 0, nullptr, 0, nullptr);
     } else {
@@ -652,6 +680,9 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
             if (first) {
 #pragma unroll
                 for (int h = 0; h < 8; ++h) m_ref[h] = -INFINITY, l[h] = 0.f, fq[h] = sQ[me.q % (2 * kQueries)][h];
+                uint32_t none[16] = {};                // only the first level's products replace what was there
+#pragma unroll
+                for (int v = 1; v < kLevels; ++v) tmem_st16(tmem + lanes + kO + 16 * v, none);
             }
             float x[8], over = -INFINITY;
 #pragma unroll
@@ -661,7 +692,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                 over = fmaxf(over, x[h] == -INFINITY ? -INFINITY : x[h] - m_ref[h]);
             }
             // every thread passes the same barriers, also when a wait ran out
-            if (any_of((over > 4.f && !end) || !ok)) {
+            if (any_of((over > kLag && !end) || !ok)) {
                 if (any_of(!ok)) {
                     live = false;
                     break;
@@ -683,12 +714,15 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                 if (!first) {                          // what has been added up so far
                     ok = mbar_wait_warp(&pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, st, 150, &abort_flag) && ok;
                     fence_after_sync();
-                    uint32_t v[16];
-                    tmem_ld16_nowait(tmem + lanes + 32, v);
-                    tmem_wait16(v);
+#pragma unroll 1
+                    for (int at = kO; at < kO + 16 * kLevels; at += 16) {
+                        uint32_t v[16];
+                        tmem_ld16_nowait(tmem + lanes + at, v);
+                        tmem_wait16(v);
 #pragma unroll
-                    for (int h = 0; h < 16; ++h) v[h] = __float_as_uint(__uint_as_float(v[h]) * alpha[h & 7]);
-                    tmem_st16(tmem + lanes + 32, v);
+                        for (int h = 0; h < 16; ++h) v[h] = __float_as_uint(__uint_as_float(v[h]) * alpha[h & 7]);
+                        tmem_st16(tmem + lanes + at, v);
+                    }
                     tmem_wait_st();
                 }
             }
@@ -700,16 +734,44 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
                 l[h] = fmaf(e, me.il, l[h]);
                 x[h] = e * me.pv;
             }
-            uint32_t hi[4], lo[4];
+            float least = x[0];
 #pragma unroll
-            for (int h = 0; h < 8; h += 2) {
-                hi[h / 2] = e4m3x2(x[h], x[h + 1]);
-                const float2 f = from_e4m3x2(hi[h / 2]);
-                lo[h / 2] = e4m3x2(16.f * (x[h] - f.x), 16.f * (x[h + 1] - f.y));
+            for (int h = 1; h < 8; ++h) least = fminf(least, x[h]);
+            uint8_t *dst = smem + s * S::STAGE + tid * 16;
+            // a probability has its terms in the level that fits it, zeros in the others
+            const bool some = __any_sync(0xffffffffu, tid < me.len && least < kLevelEnd);
+            uint32_t l1[2] = {}, l2[2] = {};           // the heads below the first, the second level, a byte each
+            uint32_t below = 0;                        // the levels that the warp's tokens have
+            if (some) {
+                below = 2;
+                if (__any_sync(0xffffffffu, tid < me.len && least < kLevelEnd / kLevelStep)) {
+                    below = 6;
+#pragma unroll
+                    for (int h = 0; h < 8; ++h)
+                        if (x[h] < kLevelEnd / kLevelStep) {
+                            x[h] *= kLevelStep;
+                            l2[h / 4] |= 0xFFu << (h % 4 * 8);
+                        }
+                }
+#pragma unroll
+                for (int h = 0; h < 8; ++h)
+                    if (x[h] < kLevelEnd) {
+                        x[h] *= kLevelStep;
+                        l1[h / 4] |= 0xFFu << (h % 4 * 8);
+                    }
             }
+            uint32_t hi[2], lo[2];                     // e4m3 terms, four heads to a word
+#pragma unroll
+            for (int w = 0; w < 2; ++w) split4<(int)kLo>(x[4 * w], x[4 * w + 1], x[4 * w + 2], x[4 * w + 3], hi[w], lo[w]);
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0] & ~l1[0], hi[1] & ~l1[1], lo[0] & ~l1[0], lo[1] & ~l1[1]);
+            if (some) {
+                const uint32_t f0 = l1[0] & ~l2[0], f1 = l1[1] & ~l2[1];
+                *reinterpret_cast<uint4 *>(dst + S::P) = make_uint4(hi[0] & f0, hi[1] & f1, lo[0] & f0, lo[1] & f1);
+                if (below == 6) *reinterpret_cast<uint4 *>(dst + 2 * S::P) = make_uint4(hi[0] & l2[0], hi[1] & l2[1], lo[0] & l2[0], lo[1] & l2[1]);
+            }
+            // (every phase of pv_done is waited for: its parity tells two of them apart, not three)
             if (i >= 2) ok = mbar_wait_warp(&pv_done[i & 1], ((i >> 1) - 1) & 1, st, 151, &abort_flag) && ok;
-            *reinterpret_cast<uint4 *>(smem + S::OFF_P + (i & 1) * S::P + tid * 16) =
-                make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+            if (lane == 0) reinterpret_cast<uint8_t *>(&sLevels[i & 1])[warp] = (uint8_t)below;
             // rows behind the last visible token: whatever they hold must not reach 0 * V
             const int rows = max(1, (me.len + 31) / 32) * 32;
             if (tid >= me.len && tid < rows) {
@@ -717,6 +779,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
 #pragma unroll
                 for (int w = 0; w < D / 16; ++w) row[w] = make_uint4(0u, 0u, 0u, 0u);
             }
+            if (first) tmem_wait_st();
             fence_before_sync();
             fence_proxy_async();
             __syncwarp();
@@ -735,7 +798,7 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
 #pragma unroll
             for (int h = 1; h < 8; ++h) ml = hl == h ? m_ref[h] : ml;
             const bool whole = me.part < 0;
-            const float z = 0.0625f * (!whole ? 1.f : L == 0.f ? 0.f : 1.f / L);   // P carries 16
+            const float z = (!whole ? 1.f : L == 0.f ? 0.f : 1.f / L) / kOne;
             const long long row = (long long)me.t * p.Hq + (long long)me.r * G;
             if (warp == 0 && lane < G) {
                 if (whole) lse[row + lane] = (ml + log2f(L)) * kLn2;
@@ -743,14 +806,21 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
             }
             ok = mbar_wait_warp(&pv_done[i & 1], (i >> 1) & 1, st, 152, &abort_flag) && ok;
             fence_after_sync();
-            uint32_t v[16];
-            tmem_ld16_nowait(tmem + lanes + 32, v);
-            tmem_wait16(v);
+            float sum_o[8] = {};
+#pragma unroll
+            for (int k = kLevels - 1; k >= 0; --k) {   // the smallest first
+                uint32_t v[16];
+                tmem_ld16_nowait(tmem + lanes + kO + 16 * k, v);
+                tmem_wait16(v);
+#pragma unroll
+                for (int h = 0; h < 8; ++h)
+                    sum_o[h] = fmaf(sum_o[h], 1.f / kLevelStep, fmaf(__uint_as_float(v[8 + h]), 1.f / kLo, __uint_as_float(v[h])));
+            }
 #pragma unroll
             for (int h = 0; h < 8; ++h) {
                 const float zh = __shfl_sync(0xffffffffu, z, h);
                 if (h >= G || tid >= D) continue;
-                const float y = fmaf(__uint_as_float(v[8 + h]), 0.0625f, __uint_as_float(v[h])) * zh;
+                const float y = sum_o[h] * zh;
                 if (whole) o[(row + h) * D + tid] = __float2bfloat16_rn(y);
                 else part_o[((long long)me.part * 8 + h) * D + tid] = y;
             }

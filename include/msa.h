@@ -455,9 +455,12 @@ msa_status msa_paged_block_topk(const msa_paged_shape *shape, const float *block
  * that does not ascend, lies past the row's own block c0, or sits behind the
  * min(topk, c0 + 1) entries that the row can have, is left out and recorded in
  * the status word.
- * A row without any block has o = 0 and lse = -inf.  Queries and
- * probabilities enter the products with 8 significant bits or more, sums are
- * fp32.  Deterministic.
+ * A row without any block has o = 0 and lse = -inf.  Queries enter the
+ * products with 8 significant bits, features below 2^-14 of their row's and
+ * head's largest off by 2^-22 of it at most.  Probabilities enter with
+ * 8 significant bits down to 2^-42 of the largest p * v_scale of their row and
+ * head; a token below that is off by 2^-50 of it at most.  Sums are fp32.
+ * Deterministic.
  */
 msa_status msa_paged_attn(const msa_paged_shape *shape, const void *q, const void *k8, const void *v8, const float *k_scale,
                           const float *v_scale, const int32_t *block_table, const int32_t *row_req, const int32_t *row_pos,
