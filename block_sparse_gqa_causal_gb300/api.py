@@ -33,7 +33,7 @@ STATUS = {0: "MSA_OK", 1: "MSA_ERR_INVALID_ARGUMENT", 2: "MSA_ERR_UNSUPPORTED", 
 EXPORTS = ("msa_workspace_size", "msa_index_select", "msa_sparse_attn_fwd", "msa_kl_fwd", "msa_fused_bwd",
            "msa_fused_bwd_kl", "msa_train_step", "msa_train_step_staged", "msa_block_mask", "msa_warmup_kl",
            "msa_index_proj_workspace_size", "msa_index_proj_fwd", "msa_index_proj_bwd", "msa_kv_append",
-           "msa_paged_workspace_size", "msa_paged_plan", "msa_paged_append", "msa_paged_block_scores",
+           "msa_paged_workspace_size", "msa_paged_plan", "msa_paged_plan_held", "msa_paged_append", "msa_paged_block_scores",
            "msa_paged_block_topk", "msa_paged_attn", "msa_last_error", "msa_check_device_status", "msa_version", "msa_launch_count")
 
 
@@ -149,7 +149,7 @@ class PagedShape:
                               + [(n, (N, H), f32, kind) for n in ("k_scale", "v_scale")])
         k_idx, sel, scores = (N, PAGE, self.d_idx), (T, H, self.topk), (T, H, self.max_blocks)
         specs = {
-            OP_PAGED_PLAN: [("new_lens", (R,), i32, need), ("lens", (R,), i32, need), ("ended", (R,), i32, maybe), table,
+            OP_PAGED_PLAN: [("new_lens", (R,), i32, need), ("lens", (R,), i32, need), ("ended", (R,), i32, maybe), ("held", (R,), i32, maybe), table,
                             ("free_pages", (N,), i32, need), ("free_state", (2,), i32, need), ("lens", (R,), i32, out),
                             ("free_state", (2,), i32, out), ("q_starts", (R + 1,), i32, out), ("row_req", (T,), i32, out),
                             ("row_pos", (T,), i32, out), ("slots", (T,), i32, out), ("segs", (self.n_segs + 1,), i32, out)],
@@ -215,14 +215,14 @@ def lib() -> ctypes.CDLL:
             GS = ctypes.POINTER(_CPagedShape)
             L.msa_paged_workspace_size.argtypes = [GS, ctypes.c_int]
             L.msa_paged_workspace_size.restype = sz
-            for fn, ptrs in (("msa_paged_plan", 14), ("msa_paged_append", 11), ("msa_paged_block_scores", 8),
+            for fn, ptrs in (("msa_paged_plan", 14), ("msa_paged_plan_held", 15), ("msa_paged_append", 11), ("msa_paged_block_scores", 8),
                              ("msa_paged_block_topk", 4), ("msa_paged_attn", 12)):
                 getattr(L, fn).argtypes = [GS] + [P] * ptrs + [sz, P]
             L.msa_selftest_wait_timeout.argtypes = [P, ctypes.c_uint, P]
             for fn in ("msa_index_select", "msa_sparse_attn_fwd", "msa_kl_fwd", "msa_fused_bwd", "msa_fused_bwd_kl",
                        "msa_train_step", "msa_train_step_staged", "msa_check_device_status", "msa_block_mask",
                        "msa_warmup_kl", "msa_index_proj_fwd", "msa_index_proj_bwd", "msa_selftest_wait_timeout",
-                       "msa_kv_append", "msa_paged_plan", "msa_paged_append", "msa_paged_block_scores",
+                       "msa_kv_append", "msa_paged_plan", "msa_paged_plan_held", "msa_paged_append", "msa_paged_block_scores",
                        "msa_paged_block_topk", "msa_paged_attn"):
                 getattr(L, fn).restype = ctypes.c_int
             L.msa_last_error.restype = ctypes.c_char_p
@@ -495,14 +495,16 @@ def _paged(shape: PagedShape, op: int, workspace, stream, *tensors):
     return r
 
 
-def paged_plan(shape: PagedShape, new_lens, lens, block_table, free_pages, free_state, *, ended=None, out=None,
+def paged_plan(shape: PagedShape, new_lens, lens, block_table, free_pages, free_state, *, ended=None, held=None, out=None,
                workspace=None, stream=None) -> PagedPlan:
     """msa_paged_plan: the step's pages, block tables and slot maps from the
     requests' lengths.  new_lens, lens, ended [R], free_state [2] int32; block_table
-    [R, max_blocks] and free_pages [n_pages] int32 are updated in place.  Returns a
+    [R, max_blocks] and free_pages [n_pages] int32 are updated in place.  held [R]
+    int32, the pages in each slot's row of the table, is updated in place too: with
+    it (msa_paged_plan_held) lengths may be lowered between steps.  Returns a
     PagedPlan (pass `out` to reuse its tensors; its lens and free_state may be
     the tensors passed in)."""
-    return PagedPlan(*_paged(shape, OP_PAGED_PLAN, workspace, stream, new_lens, lens, ended, block_table, free_pages, free_state,
+    return PagedPlan(*_paged(shape, OP_PAGED_PLAN, workspace, stream, new_lens, lens, ended, held, block_table, free_pages, free_state,
                              *(out or (None,) * 7)))
 
 

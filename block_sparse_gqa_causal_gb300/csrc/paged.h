@@ -99,7 +99,7 @@ cudaError_t allow_smem(K *kernel, int bytes, std::atomic<unsigned long long> &do
 
 struct PlanArgs {
     const int32_t *new_lens, *lens_in, *ended, *free_in;
-    int32_t *block_table, *free_pages, *lens_out, *free_out, *q_starts, *row_req, *row_pos, *slots, *segs;
+    int32_t *held, *block_table, *free_pages, *lens_out, *free_out, *q_starts, *row_req, *row_pos, *slots, *segs;
 };
 size_t paged_plan_scratch_ints(const PagedProblem &p);
 cudaError_t launch_paged_plan(const PagedProblem &p, const PlanArgs &a, int32_t *scratch, DeviceStatus *st, cudaStream_t s);

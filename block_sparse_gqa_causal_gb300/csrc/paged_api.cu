@@ -134,6 +134,16 @@ msa_status msa_paged_plan(const msa_paged_shape *shape, const int32_t *new_lens,
                           int32_t *lens_out, int32_t *free_out, int32_t *q_starts, int32_t *row_req, int32_t *row_pos,
                           int32_t *slots, int32_t *segs, void *workspace, size_t workspace_bytes, void *stream)
 {
+    return msa_paged_plan_held(shape, new_lens, lens_in, ended, nullptr, block_table, free_pages, free_in, lens_out, free_out,
+                               q_starts, row_req, row_pos, slots, segs, workspace, workspace_bytes, stream);
+}
+
+msa_status msa_paged_plan_held(const msa_paged_shape *shape, const int32_t *new_lens, const int32_t *lens_in,
+                               const int32_t *ended, int32_t *held, int32_t *block_table, int32_t *free_pages,
+                               const int32_t *free_in, int32_t *lens_out, int32_t *free_out, int32_t *q_starts,
+                               int32_t *row_req, int32_t *row_pos, int32_t *slots, int32_t *segs, void *workspace,
+                               size_t workspace_bytes, void *stream)
+{
     PagedProblem p;
     msa_status st = begin(shape, MSA_OP_PAGED_PLAN, workspace, workspace_bytes, p);
     if (st != MSA_OK) return st;
@@ -143,7 +153,8 @@ msa_status msa_paged_plan(const msa_paged_shape *shape, const int32_t *new_lens,
                 {slots, "slots", 4}, {segs, "segs", 4}});
     if (st != MSA_OK) return st;
     if ((uintptr_t)ended % 4) return refuse(MSA_ERR_INVALID_ARGUMENT, "ended is not 4-byte aligned");
-    const PlanArgs a{new_lens, lens_in, ended, free_in, block_table, free_pages, lens_out, free_out, q_starts, row_req,
+    if ((uintptr_t)held % 4) return refuse(MSA_ERR_INVALID_ARGUMENT, "held is not 4-byte aligned");
+    const PlanArgs a{new_lens, lens_in, ended, free_in, held, block_table, free_pages, lens_out, free_out, q_starts, row_req,
                      row_pos, slots, segs};
     int32_t *scratch = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + kHeadBytes);
     return done(launch_paged_plan(p, a, scratch, status(workspace), static_cast<cudaStream_t>(stream)),

@@ -96,8 +96,8 @@ int launch(const Call &c, void *const *p, void *ws, size_t n, void *stream)
     auto f32 = [&](int i) { return static_cast<float *>(p[i]); };
     switch (c.op) {
     case MSA_OP_PAGED_PLAN:
-        return msa_paged_plan(&c.shape, i32(0), i32(1), i32(2), i32(3), i32(4), i32(5), i32(6), i32(7), i32(8), i32(9), i32(10),
-                              i32(11), i32(12), ws, n, stream);
+        return msa_paged_plan_held(&c.shape, i32(0), i32(1), i32(2), i32(3), i32(4), i32(5), i32(6), i32(7), i32(8), i32(9),
+                                   i32(10), i32(11), i32(12), i32(13), ws, n, stream);
     case MSA_OP_PAGED_APPEND:
         return msa_paged_append(&c.shape, p[0], p[1], p[2], i32(3), i32(4), p[5], p[6], f32(7), f32(8), p[9], ws, n, stream);
     case MSA_OP_PAGED_BLOCK_SCORES:

@@ -3,7 +3,9 @@
 //
 // Request r holds ceil(l/128) pages for its l tokens and brings n new ones; it
 // takes ceil((l+n)/128) - ceil(l/128) pages from the front of a ring of free
-// pages, requests in order.  A request that ended gives its pages back behind
+// pages, requests in order.  Where lengths may be lowered between steps, the
+// pages held are told apart from them: those past the length are filled again
+// before any is taken.  A request that ended gives its pages back behind
 // the ring's free ones, so a step's releases never meet its takes and the two
 // need no order.  Everything else is exclusive sums over the requests: first
 // row, first page taken, first segment.
@@ -89,7 +91,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedProblem p, PlanArgs a, 
     __shared__ int bad, n_ended;
     __shared__ int3 ended[1024];
     chain_next();
-    chain_wait(a.new_lens, a.lens_in, a.ended, a.free_in, a.block_table, a.free_pages, scratch);
+    chain_wait(a.new_lens, a.lens_in, a.ended, a.free_in, a.held, a.block_table, a.free_pages, scratch);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, nwarp = nthr >> 5;
     const int head = a.free_in[0], count = a.free_in[1];
     const int most = p.max_blocks * kPage;
@@ -106,14 +108,24 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedProblem p, PlanArgs a, 
             q.had = a.lens_in[r];
             q.n = a.new_lens[r];
             const bool ended = a.ended && a.ended[r] != 0;
+            int pages = pages_of(q.had);                         // in the slot's row of the table
             if (q.had < 0 || q.had > most || q.n < 0 || q.n > most - (ended ? 0 : q.had)) {
                 bad = 1;
                 return q;
             }
+            if (a.held) {
+                const int h = a.held[r];
+                if (h < pages || h > p.max_blocks) {
+                    bad = 1;
+                    return q;
+                }
+                pages = h;
+            }
             q.old = ended ? 0 : q.had;
-            q.held = pages_of(q.old);
-            q.after = pages_of(q.old + q.n);
-            q.s = {q.n, q.after - q.held, ended ? pages_of(q.had) : 0, q.n > 0 ? q.after - q.old / kPage : 0};
+            q.held = ended ? 0 : pages;
+            const int last = pages_of(q.old + q.n);
+            q.after = max(q.held, last);
+            q.s = {q.n, q.after - q.held, ended ? pages : 0, q.n > 0 ? last - q.old / kPage : 0};
         }
         return q;
     };
@@ -189,6 +201,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedProblem p, PlanArgs a, 
         if (r < p.R) {
             a.q_starts[r] = why ? 0 : (int)at.rows;
             a.lens_out[r] = why ? a.lens_in[r] : q.old + q.n;
+            if (a.held && !why) a.held[r] = q.after;
             if (!why) reinterpret_cast<int4 *>(scratch)[1 + r] = make_int4((int)at.take, (int)at.segs, q.old, q.held);
         }
         // pages of ended requests go behind the free ones, a warp to a request

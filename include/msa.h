@@ -397,11 +397,26 @@ size_t msa_paged_workspace_size(const msa_paged_shape *shape, int op);
  * more rows than T, too few free pages, a ring state out of range) is not
  * made: lengths, ring and block_table stay as they were, the plan has no rows
  * (q_starts 0, every row -1), and the status word is set.
+ *
+ * lens_in is what the step before wrote.  A caller that drops the last tokens
+ * of a request (speculative rows that were rejected) lowers its length; over a
+ * page border that takes msa_paged_plan_held, since a page past the length is
+ * otherwise no longer the request's and lost to the pool.
+ *   held [R] (may be NULL: ceil(l/128), as msa_paged_plan)  number of pages in
+ *           the slot's row of block_table, at least ceil(l/128) and at most
+ *           max_blocks (else the step is not made).  Those past the length are
+ *           filled again before any is taken, and go back when the request has
+ *           ended.  Updated in place; zeros for an empty table.
  */
 msa_status msa_paged_plan(const msa_paged_shape *shape, const int32_t *new_lens, const int32_t *lens_in,
                           const int32_t *ended, int32_t *block_table, int32_t *free_pages, const int32_t *free_in,
                           int32_t *lens_out, int32_t *free_out, int32_t *q_starts, int32_t *row_req, int32_t *row_pos,
                           int32_t *slots, int32_t *segs, void *workspace, size_t workspace_bytes, void *stream);
+msa_status msa_paged_plan_held(const msa_paged_shape *shape, const int32_t *new_lens, const int32_t *lens_in,
+                               const int32_t *ended, int32_t *held, int32_t *block_table, int32_t *free_pages,
+                               const int32_t *free_in, int32_t *lens_out, int32_t *free_out, int32_t *q_starts,
+                               int32_t *row_req, int32_t *row_pos, int32_t *slots, int32_t *segs, void *workspace,
+                               size_t workspace_bytes, void *stream);
 
 /*
  * New tokens into the paged cache: k_new, v_new [T, Hkv, d] and k_idx_new

@@ -182,3 +182,20 @@ def test_plan_reference_conserves_pages():
         assert sorted(held + left) == list(range(n_pages))
         n = starts[-1]
         assert len(set(slots[:n])) == n and np.all(slots[n:] == -1)
+
+
+def test_the_plan_with_held_pages_is_refused_like_the_plan(api):
+    sh, g = api.PagedShape(**GOOD), P(1 << 21)
+    fn = lambda ptrs, ws=P(1 << 20), n=1 << 40: (api.lib().msa_paged_plan_held(ctypes.byref(sh.c()), *ptrs, ws, n, None),
+                                                 api.lib().msa_last_error().decode())
+    for i in range(14):                                    # 2: ended, 3: held, both may be NULL
+        if i not in (2, 3):
+            rc, msg = fn([g] * i + [None] + [g] * (13 - i))
+            assert rc == 1 and "is NULL" in msg, i
+        rc, msg = fn([g] * i + [P((1 << 21) + 2)] + [g] * (13 - i))
+        assert rc == 1 and "aligned" in msg, i
+    assert fn([g] * 14, ws=None) == (1, "workspace is NULL") and fn([g] * 14, n=4096)[0] == 3
+    import torch
+    i32 = lambda *n: torch.zeros(n, dtype=torch.int32)
+    with pytest.raises(ValueError, match="held"):
+        api.paged_plan(sh, i32(4), i32(4), i32(4, 16), i32(64), i32(2), held=i32(3))
