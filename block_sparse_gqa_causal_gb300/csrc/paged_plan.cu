@@ -56,7 +56,7 @@ __device__ __forceinline__ void fill_entry(const PagedProblem &p, const PlanArgs
     if (blk >= rq.w) {
         const int at = head + rq.x + (blk - rq.w);   // under twice the ring: its takes are at most its pages
         page = a.free_pages[at < p.n_pages ? at : at - p.n_pages];
-        if (off == 0) *entry = page;            // every page taken is opened by one row of the step
+        if (off == 0) *entry = (unsigned)page < (unsigned)p.n_pages ? page : -1;   // every page taken is opened by one row of the step
     } else {
         page = *entry;                          // the partly filled last page
     }
@@ -88,14 +88,14 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedProblem p, PlanArgs a, 
                                                     DeviceStatus *st)
 {
     __shared__ Sums warp_sum[32];
-    __shared__ int bad, n_ended;
+    __shared__ int bad, n_ended, lost;
     __shared__ int3 ended[1024];
     chain_next();
     chain_wait(a.new_lens, a.lens_in, a.ended, a.free_in, a.held, a.block_table, a.free_pages, scratch);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, nwarp = nthr >> 5;
     const int head = a.free_in[0], count = a.free_in[1];
     const int most = p.max_blocks * kPage;
-    if (tid == 0) bad = 0;
+    if (tid == 0) bad = lost = 0;
     __syncthreads();
 
     struct Req {
@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedProblem p, PlanArgs a, 
                 const int32_t *row = a.block_table + (long long)e.x * p.max_blocks;
                 const int first = (int)(((long long)head + count + e.z) % p.n_pages);
                 auto place = [&](int j) { return first + j < p.n_pages ? first + j : first + j - p.n_pages; };
+                unsigned top = 0;
                 constexpr int U = 16;                            // loads in flight before the stores they may not pass
                 for (int j0 = lane; j0 < e.y; j0 += 32 * U) {
                     int32_t page[U];
@@ -223,15 +224,32 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedProblem p, PlanArgs a, 
 #pragma unroll
                     for (int u = 0; u < U; ++u)
                         if (j0 + 32 * u < e.y) a.free_pages[place(j0 + 32 * u)] = page[u];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) top = max(top, (unsigned)page[u]);
+                }
+                if (top >= (unsigned)p.n_pages) {
+                    report(st, kDevCheck, 103, (int)top);
+                    lost = 1;
                 }
             }
             __syncthreads();
         }
     }
+    long long back = total.gone;
+    if (total.gone > 0 && warp == 0 && lost) {                 // entries that are no pages do not enter the ring: the others move up
+        back = 0;
+        for (long long j0 = 0; j0 < total.gone; j0 += 32) {
+            const int page = j0 + lane < total.gone ? a.free_pages[((long long)head + count + j0 + lane) % p.n_pages] : -1;
+            const unsigned fine = __ballot_sync(0xffffffffu, (unsigned)page < (unsigned)p.n_pages);
+            if (fine >> lane & 1) a.free_pages[((long long)head + count + back + __popc(fine & ((1u << lane) - 1))) % p.n_pages] = page;
+            back += __popc(fine);
+            __syncwarp();
+        }
+    }
     if (tid == 0) {
         a.q_starts[p.R] = (int)total.rows;
         a.free_out[0] = why ? head : (int)((head + total.take) % p.n_pages);
-        a.free_out[1] = why ? count : (int)(count - total.take + total.gone);
+        a.free_out[1] = why ? count : (int)(count - total.take + back);
     }
     if (!fused) return;
     __syncthreads();

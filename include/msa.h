@@ -397,6 +397,9 @@ size_t msa_paged_workspace_size(const msa_paged_shape *shape, int op);
  * more rows than T, too few free pages, a ring state out of range) is not
  * made: lengths, ring and block_table stay as they were, the plan has no rows
  * (q_starts 0, every row -1), and the status word is set.
+ * An ended request's table entry that is no page does not enter the ring; a
+ * ring entry that is none is written to block_table as -1, and the rows on it
+ * have no slot.  Both are recorded in the status word.
  *
  * lens_in is what the step before wrote.  A caller that drops the last tokens
  * of a request (speculative rows that were rejected) lowers its length; over a

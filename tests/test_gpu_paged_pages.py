@@ -127,3 +127,62 @@ def test_speculative_rows_are_dropped_and_written_again(api):
         sv.lens = sv.lens - i32(drop)
     free = int(sv.free[1])
     assert free + int(held.sum()) == 13 and (held >= (sv.lens + 127) // PAGE).all()
+
+
+@pytest.mark.parametrize("R,T,nb", [(3, 8, 70), (40, 2000, 20), (1100, 1200, 3)])
+@pytest.mark.parametrize("held", [False, True])
+def test_entries_that_are_no_pages_do_not_enter_the_ring(api, R, T, nb, held):
+    """Ended requests whose table has entries out of range: recorded, the other pages free in their order."""
+    rng = np.random.default_rng(R + held)
+    lens = rng.integers(1, nb * PAGE + 1, R)
+    lens[0] = nb * PAGE
+    m = (lens + 127) // PAGE
+    n_pages = int(m.sum()) + R + 4
+    ids = rng.permutation(n_pages).astype(np.int32)
+    table, at = np.full((R, nb), -1, np.int32), 0
+    for r in range(R):
+        table[r, :m[r]] = ids[at:at + m[r]]
+        at += m[r]
+    ended = (rng.random(R) < 0.6).astype(int)
+    ended[0] = 1
+    hurt = (rng.random((R, nb)) < 0.3) & (np.arange(nb) < m[:, None]) & (ended == 1)[:, None]
+    hurt[0, 0] = True
+    table[hurt] = rng.choice([-1, n_pages, -2 ** 31, 2 ** 31 - 1], hurt.sum())
+    new = np.where(rng.random(R) < 0.5, 1, 0)
+    have = np.where(ended, 0, lens)
+    new = np.where(have + new > nb * PAGE, 0, new)
+    head, count = n_pages - 2, n_pages - at                     # the ring's end is passed
+    ring = np.full(n_pages, -9, np.int32)
+    ring[(head + np.arange(count)) % n_pages] = ids[at:]
+    sh = api.PagedShape(R=R, T=T, max_blocks=nb, n_pages=n_pages, Hq=2, Hkv=2, d=64, d_idx=64, topk=2)
+    ws, dt, dr, h = api.new_paged_workspace(sh, api.OP_PAGED_PLAN), i32(table), i32(ring), i32(m) if held else None
+    p = api.paged_plan(sh, i32(new), i32(lens), dt, dr, i32([head, count]), ended=i32(ended), held=h, workspace=ws)
+    with pytest.raises(api.MsaError, match="site 103"):
+        api.check_device_status(ws)
+    taken = (have + new + 127) // PAGE - (have + 127) // PAGE
+    back = [table[r, j] for r in range(R) if ended[r] for j in range(m[r]) if not hurt[r, j]]
+    left = list(ids[at:])[taken.sum():] + back
+    got, (head2, count2) = dr.cpu().numpy(), p.free_state.tolist()
+    assert head2 == (head + taken.sum()) % n_pages and count2 == len(left)
+    assert [got[(head2 + i) % n_pages] for i in range(count2)] == left
+    assert p.lens.tolist() == (have + new).tolist() and (p.slots[:int(new.sum())] >= 0).all()
+
+
+def test_a_ring_entry_that_is_no_page_stays_out_of_the_table(api):
+    """Its rows have no slot and its column is -1, in the step that takes it and in the next; when the request has ended
+    it does not come back."""
+    import torch
+    for T in (4, 1500):
+        sh = api.PagedShape(R=2, T=T, max_blocks=2, n_pages=4, Hq=2, Hkv=1, d=64, d_idx=64, topk=2)
+        table, ring, ws = torch.full((2, 2), 7, dtype=torch.int32, device="cuda"), i32([9, 3, 0, 1]), api.new_paged_workspace(sh, api.OP_PAGED_PLAN)
+        lens, free = i32([0, 0]), i32([0, 4])
+        for new, slots in (([2, 2], [-1, -1, 3 * PAGE, 3 * PAGE + 1]), ([1, 1], [-1, 3 * PAGE + 2])):
+            p = api.paged_plan(sh, i32(new), lens, table, ring, free, workspace=ws)
+            lens, free = p.lens, p.free_state
+            with pytest.raises(api.MsaError, match="site 102"):
+                api.check_device_status(ws)
+            assert p.slots[:len(slots)].tolist() == slots and table.tolist() == [[-1, 7], [3, 7]]
+        p = api.paged_plan(sh, i32([0, 0]), lens, table, ring, free, ended=i32([1, 1]), workspace=ws)
+        with pytest.raises(api.MsaError, match="site 103"):
+            api.check_device_status(ws)
+        assert p.free_state.tolist() == [2, 3] and [int(ring[(2 + i) % 4]) for i in range(3)] == [0, 1, 3]
