@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PagedProblem p, PlanArgs a, 
     if (bad) why = 1;                                            // a length out of range
     else if (!ring_ok || total.gone + count > p.n_pages) why = 2;  // the ring's state
     else if (total.rows > p.T) why = 3;                          // more rows than T
-    else if (total.take > count) why = 4;                        // too few free pages
+    else if (total.take > count) why = 4;                        // too few free pages; those that come back do not count
     if (why) {
         if (tid == 0) report(st, kDevCheck, 101, why);
         total = Sums{};

@@ -383,8 +383,9 @@ size_t msa_paged_workspace_size(const msa_paged_shape *shape, int op);
  * The plan of a step: block tables, slot maps and page allocation from the
  * requests' lengths.  Request r has lens_in[r] tokens cached and brings
  * new_lens[r] (0 or more).  ended (may be NULL) marks slots whose request is
- * over: its pages go back first, and the slot's new tokens, if any, are the
- * first of another request.
+ * over: its pages go back, and the slot's new tokens, if any, are the first of
+ * another request.  Pages that go back are free from the next step on; this
+ * step takes from those that were free before it.
  *   free_pages [n_pages]  ring of free pages; free_in = {head, count}: the
  *                         free ones are free_pages[(head + i) % n_pages], i < count
  * Takes ceil((l + n)/128) - ceil(l/128) pages for each request, requests in
@@ -394,7 +395,7 @@ size_t msa_paged_workspace_size(const msa_paged_shape *shape, int op);
  * (= l + n), free_out, q_starts, row_req, row_pos, slots and segs.  lens_out
  * may be lens_in and free_out may be free_in; no other arrays may overlap.
  * A step that does not fit (a negative length, one past 128 * max_blocks,
- * more rows than T, too few free pages, a ring state out of range) is not
+ * more rows than T, more pages taken than were free, a ring state out of range) is not
  * made: lengths, ring and block_table stay as they were, the plan has no rows
  * (q_starts 0, every row -1), and the status word is set.
  * An ended request's table entry that is no page does not enter the ring; a

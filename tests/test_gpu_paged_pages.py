@@ -186,3 +186,21 @@ def test_a_ring_entry_that_is_no_page_stays_out_of_the_table(api):
         with pytest.raises(api.MsaError, match="site 103"):
             api.check_device_status(ws)
         assert p.free_state.tolist() == [2, 3] and [int(ring[(2 + i) % 4]) for i in range(3)] == [0, 1, 3]
+
+
+def test_pages_that_go_back_are_free_from_the_next_step_on(api):
+    """A full pool in which one request ends and another starts in its slot: refused in that step, made after one that only
+    gives the pages back."""
+    pool = Pool(api, 2, 700, 3, 6, seed=1)
+    new = [300, 384]
+    pool.check(pool.step(new), new)
+    assert pool.free.tolist()[1] == 0
+    before = [t.clone() for t in (pool.table, pool.ring, pool.free, pool.lens, pool.held)]
+    p = api.paged_plan(pool.sh, i32([200, 0]), pool.lens, pool.table, pool.ring, pool.free, held=pool.held, ended=i32([1, 0]), workspace=pool.ws)
+    with pytest.raises(api.MsaError, match="site 101, info 4"):
+        api.check_device_status(pool.ws)
+    for a, b in zip(before, (pool.table, pool.ring, p.free_state, p.lens, pool.held)):
+        assert a.tolist() == b.tolist()
+    for new, ended in (([0, 0], [1, 0]), ([200, 0], None)):
+        pool.check(pool.step(new, ended), new)
+    assert pool.lens.tolist() == [200, 384] and pool.free.tolist()[1] == 1
