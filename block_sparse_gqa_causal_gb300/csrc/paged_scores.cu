@@ -18,6 +18,8 @@
 // caches of 131,072 to 1,048,576 tokens (605 MB) 93 us, 96% of the copy rate,
 // against 100 for a grid of (tile, share) CTAs.  With more rows than
 // kPrefixRows, whole tiles are dealt out.
+#include <limits.h>
+
 #include <algorithm>
 #include <type_traits>
 
@@ -88,10 +90,12 @@ scores_kernel(PagedProblem p, const bf16 *__restrict__ q_idx, const __grid_const
         const int first = q_starts[req], end = min(q_starts[req + 1], p.T);
         return t < first || t >= end || (t - first) % rows_per_tile != 0 ? 0 : min(rows_per_tile, end - t);
     };
-    // pages that some row of the tile sees
+    // pages that some row of the tile sees (positions in any order)
     auto tile_pages = [&](int t) {
+        int last = row_pos[t];
         const int n = tile_rows(t);
-        const int last = n ? row_pos[t + n - 1] : -1;
+        if (n == 0) last = -1;
+        for (int u = 1; u < n; ++u) last = max(last, row_pos[t + u]);
         if (last >= 0 && last / kPage >= p.max_blocks) report(st, kDevCheck, 122, last);
         return last < 0 ? 0 : min(last / kPage + 1, p.max_blocks);
     };
@@ -195,7 +199,7 @@ scores_kernel(PagedProblem p, const bf16 *__restrict__ q_idx, const __grid_const
             t = me.t;
             h0 = me.h0;
             const int rows = tile_rows(t), req = row_req[t];
-            first_pos = row_pos[t];
+            first_pos = INT_MAX;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -210,7 +214,9 @@ scores_kernel(PagedProblem p, const bf16 *__restrict__ q_idx, const __grid_const
                         a[mt][ks][e] = ok ? __ldg(src + ks * 8 + q4) : 0u;
                         a[mt][ks][2 + e] = ok ? __ldg(src + ks * 8 + q4 + 4) : 0u;
                     }
+                    if (pos[mt][e] >= 0) first_pos = min(first_pos, pos[mt][e]);
                 }
+            first_pos = __reduce_min_sync(0xffffffffu, first_pos);
         }
         const int c = me.c;
         float mx[MT][2];

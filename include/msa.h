@@ -350,7 +350,8 @@ msa_status msa_kv_append(const msa_shape *shape, const void *k_new, const void *
  *   k_scale, v_scale [n_pages, Hkv]     fp32, powers of two: a row's values
  *                                       are code * scale
  *   k_idx       [n_pages, 128, d_idx]   bf16
- * A row at position p sees its request's tokens 0 .. p.  All shape fields have
+ * A row at position p sees its request's tokens 0 .. p; positions of a request
+ * may be in any order and equal.  All shape fields have
  * to be valid in every call.  Supported: d, d_idx in {64, 128}; Hq/Hkv in
  * {1, 2, 4, 8}; topk <= 32; max_blocks, n_pages <= 2^23; R <= 2^24; Hkv <=
  * 32768; n_pages * Hkv < 2^31; T * Hq < 2^24.  16-byte alignment of the bf16

@@ -744,3 +744,36 @@ def test_outputs_on_a_given_stream_are_not_reused_early(api):
         side.synchronize()
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
         del o, lse, junk
+
+
+@pytest.mark.parametrize("Hkv,di,lens,q", [(8, 128, [500, 700, 40, 2000], [3, 17, 40, 16]), (1, 64, [4000, 130], [100, 130]), (40, 128, [300, 1260], [2, 5]),
+                                           (2, 64, [900, 700], [300, 300]), (8, 128, [5000], [4])])
+@pytest.mark.parametrize("order", ["down", "shuffled", "equal"])
+def test_positions_of_a_request_in_any_order(api, Hkv, di, lens, q, order):
+    """Rows whose positions do not ascend (branches of a draft, say): each row's scores and attention are its own."""
+    import torch
+    rng = np.random.default_rng(sum(lens) + Hkv)
+    table, n_pages = lay_out(lens, rng, max_blocks=max((n + 127) // 128 for n in lens) + 2)
+    starts, req, pos = rows_of(lens, q, 2)
+    for r in range(len(q)):
+        at = slice(starts[r], starts[r + 1])
+        pos[at] = {"down": pos[at][::-1], "shuffled": rng.integers(0, lens[r], q[r]), "equal": np.where(rng.random(q[r]) < 0.5, lens[r] // 2, lens[r] - 1)}[order]
+    T, nb, n = len(req), table.shape[1], starts[-1]
+    qt, qv = bf(rng.standard_normal((T, Hkv, di)))
+    kt, kv = bf(rng.standard_normal((n_pages, PAGE, di)))
+    sh = api.PagedShape(R=len(lens), T=T, max_blocks=nb, n_pages=n_pages, Hq=Hkv, Hkv=Hkv, d=64, d_idx=di, topk=3)
+    ws = api.new_paged_workspace(sh, api.OP_PAGED_BLOCK_SCORES)
+    got = api.paged_block_scores(sh, qt, kt, i32(table), i32(starts), i32(req), i32(pos), workspace=ws)
+    status_ok(api, ws)
+    sel = api.paged_block_topk(sh, got, i32(pos)).cpu().numpy()
+    got = got.cpu().numpy()
+    want, mag = ref.block_scores(qv, kv, table, req, pos, di ** -0.5)
+    fine = np.isfinite(want[:n])
+    assert np.array_equal(fine, np.isfinite(got[:n])) and np.all(got[:n][~fine] == -np.inf)
+    assert np.all(np.abs(got[:n][fine] - want[:n][fine]) <= di * 2.0 ** -23 * mag[:n][fine] + 2.0 ** -23 * np.abs(want[:n][fine]))
+    assert np.array_equal(sel[:n], ref.topk(got, pos, 3)[:n])
+    k8, ks = filled_cache(rng, n_pages, Hkv, 64, table, lens)
+    v8, vs = filled_cache(rng, n_pages, Hkv, 64, table, lens)
+    q8, qv = bf(rng.standard_normal((T, Hkv, 64)))
+    args = (q8, f8(k8), f8(v8), dev(ks), dev(vs), i32(table), i32(req), i32(pos))
+    check_attn(api, sh, args, sel, (qv, k8, v8, ks, vs, table, req, pos, sel, 0.125), n)
