@@ -232,7 +232,6 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
     __shared__ long long before[kPrefixRows + 1];   // blocks, and count, of the rows before each row, one group
     __shared__ int abort_flag;
 
-    chain_next();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = p.G;
     const bool even = arrived != nullptr;         // stretches of equal length; else whole rows are dealt out
 
@@ -275,6 +274,10 @@ attn_kernel(PagedProblem p, const bf16 *__restrict__ q, const __grid_constant__ 
         tmem_alloc(&tmem_slot, kColumns);
         tmem_relinquish();
     }
+    // Not before: a successor that holds TMEM waits for this grid's end, and a CTA of another stream's kernel that wants
+    // all of it for the successor's; this grid's must not be behind that one in the queue.
+    __syncthreads();
+    chain_next();
     chain_wait(q, k_scale, v_scale, block_table, row_req, row_pos, sel, part_o, part_ml, arrived);
     if (even)
         for (int t = tid; t < p.T; t += kThreads) {

@@ -777,3 +777,25 @@ def test_positions_of_a_request_in_any_order(api, Hkv, di, lens, q, order):
     q8, qv = bf(rng.standard_normal((T, Hkv, 64)))
     args = (q8, f8(k8), f8(v8), dev(ks), dev(vs), i32(table), i32(req), i32(pos))
     check_attn(api, sh, args, sel, (qv, k8, v8, ks, vs, table, req, pos, sel, 0.125), n)
+
+
+def test_attention_beside_kernels_that_take_all_of_tensor_memory(api):
+    """Chained attention calls on one stream, the contiguous selection (512 columns a CTA) on another, at sizes that share
+    an SM: both come out as alone."""
+    import torch
+    sh, args, sel, _ = attn_case(api, lens=[3000 + 50 * i for i in range(20)], q=[1] * 20, Hq=16, Hkv=2, d=64, k=16, sparse=True)
+    sel, ws = i32(sel), api.new_paged_workspace(sh, api.OP_PAGED_ATTN)
+    full = api.Shape(B=1, Nq=2048, Nk=2048, Hq=8, Hkv=2, d=64, d_idx=64, topk=4)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    qi, ki = (torch.randn(1, 2048, *m, 64, device="cuda", generator=g).bfloat16() for m in ((2,), ()))
+    want, want2 = api.paged_attn(sh, *args, sel_idx=sel, workspace=ws), api.index_select(full, qi, ki)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [api.paged_attn(sh, *args, sel_idx=sel, workspace=ws, stream=streams[0]) for _ in range(6)]
+        with torch.cuda.stream(streams[1]):
+            got2 = [api.index_select(full, qi, ki) for _ in range(6)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a[0], want[0]) and torch.equal(a[1], want[1]) for a in got)
+        assert all(torch.equal(a, want2) for a in got2)
+    status_ok(api, ws)
