@@ -470,8 +470,10 @@ def paged_workspace_size(shape: PagedShape, op: int) -> int:
 
 def new_paged_workspace(shape: PagedShape, op: int, device=None) -> torch.Tensor:
     """A workspace of a paged call, its first 4,096 bytes (status word, arrival counts) zeroed."""
-    ws = torch.empty(paged_workspace_size(shape, op), dtype=torch.uint8, device=device or "cuda")
-    ws[:4096].zero_()
+    dev = torch.device("cuda" if device is None else device)
+    with torch.cuda.device(dev) if dev.type == "cuda" else contextlib.nullcontext():     # its size goes by the device's SMs
+        ws = torch.empty(paged_workspace_size(shape, op), dtype=torch.uint8, device=dev)
+        ws[:4096].zero_()
     return ws
 
 
@@ -487,8 +489,7 @@ def _paged(shape: PagedShape, op: int, workspace, stream, *tensors):
             return _paged(shape, op, workspace, None, *tensors)
     if workspace is None:
         dev = next(t.device for t in tensors if t is not None)
-        with torch.cuda.device(dev) if dev.type == "cuda" else contextlib.nullcontext():
-            workspace = new_paged_workspace(shape, op, dev)
+        workspace = new_paged_workspace(shape, op, dev)
     r = (_binding or binding()).call(shape._calls[op], workspace, *tensors)
     if type(r) is int:
         _check(r)

@@ -199,3 +199,28 @@ def test_the_plan_with_held_pages_is_refused_like_the_plan(api):
     i32 = lambda *n: torch.zeros(n, dtype=torch.int32)
     with pytest.raises(ValueError, match="held"):
         api.paged_plan(sh, i32(4), i32(4), i32(4, 16), i32(64), i32(2), held=i32(3))
+
+
+def test_a_workspace_is_sized_by_its_own_device(api, monkeypatch):
+    """The attention's scratch goes by the SMs of the device that the workspace is for, not of the current one (devices are faked)."""
+    import torch
+    current = [0]
+
+    class On:
+        def __init__(self, dev):
+            self.to = current[0] if torch.device(dev).index is None else torch.device(dev).index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.to
+
+        def __exit__(self, *_):
+            current[0] = self.before
+
+    real = torch.empty
+    monkeypatch.setattr(torch.cuda, "device", On)
+    monkeypatch.setattr(torch, "empty", lambda n, dtype, device: real(n, dtype=dtype))
+    monkeypatch.setattr(api, "paged_workspace_size", lambda shape, op: 8192 + 256 * current[0])
+    sh = api.PagedShape(**GOOD)
+    for dev, n in (("cuda:3", 3), (torch.device("cuda", 2), 2), (1, 1), ("cuda", 0), (None, 0)):
+        ws = api.new_paged_workspace(sh, api.OP_PAGED_ATTN, dev)
+        assert ws.numel() == 8192 + 256 * n and not ws[:4096].any() and current == [0]
