@@ -3,7 +3,8 @@ _paged_binding.so (the paged calls' Python binding) with the host compiler.
 
 Each .cu under csrc/ compiles to an object in parallel; the objects link
 into block_sparse_gqa_causal_gb300/libmsa.so, without torch.  The binding is
-compiled against the torch that is installed and linked with libmsa.so.
+compiled against the torch that is installed and linked with libmsa.so; where
+there is no torch it is left out, and where it fails libmsa.so is there already.
 """
 from __future__ import annotations
 
@@ -44,8 +45,12 @@ def _stale(out: str, deps: list[str]) -> bool:
 
 
 def _binding_commands(out: str):
-    """The object of the binding (named by the versions it is compiled for) and the commands that make and link it."""
-    import torch
+    """The binding's source, its object (named by the versions it is compiled for) and the commands that make and link it;
+    None without torch."""
+    try:
+        import torch
+    except ImportError:
+        return None
     at = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     inc = [os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include"),
@@ -76,11 +81,6 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) 
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
 
-    bsrc, bobj, bcompile, blink = _binding_commands(BINDING + ".tmp")
-    bstale = force or _stale(bobj, [bsrc, headers[-1]])
-    if bstale:
-        jobs.append(bcompile)
-
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0 or verbose or ptxas_info:
@@ -88,15 +88,20 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) 
         if r.returncode != 0:
             raise RuntimeError(f"{os.path.basename(cmd[0])} failed for {cmd[-3]}")
 
-    if jobs:
-        with ThreadPoolExecutor(min(len(jobs), os.cpu_count() or 4)) as ex:
-            list(ex.map(run, jobs))
-    if force or jobs or _stale(LIB, objs):
-        tmp = LIB + ".tmp"
-        run([nvcc(), *ARCH, "-shared", "-Xlinker", "-soname", "-Xlinker", os.path.basename(LIB), "-o", tmp, *objs])
-        os.replace(tmp, LIB)
-    if bstale or _stale(BINDING, [bobj, LIB]):
-        run(blink)
+    binding = _binding_commands(BINDING + ".tmp")
+    with ThreadPoolExecutor(max(1, min(len(jobs) + 1, os.cpu_count() or 4))) as ex:
+        bjob = None
+        if binding and (force or _stale(binding[1], [binding[0], headers[-1]])):
+            bjob = ex.submit(run, binding[2])
+        list(ex.map(run, jobs))
+        if force or jobs or _stale(LIB, objs):
+            tmp = LIB + ".tmp"
+            run([nvcc(), *ARCH, "-shared", "-Xlinker", "-soname", "-Xlinker", os.path.basename(LIB), "-o", tmp, *objs])
+            os.replace(tmp, LIB)
+        if bjob:
+            bjob.result()
+    if binding and (bjob or _stale(BINDING, [binding[1], LIB])):
+        run(binding[3])
         os.replace(BINDING + ".tmp", BINDING)
     return LIB
 
