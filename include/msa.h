@@ -364,6 +364,9 @@ msa_status msa_kv_append(const msa_shape *shape, const void *k_new, const void *
  * What device memory says (lengths, pages, selections) is checked on the
  * device: an entry out of range is left out and recorded in the status word.
  * Outputs do not overlap inputs or one another, but where a call says so.
+ * Scores and attention take any rows, and are made for few of them a request:
+ * each row reads its pages for itself (of scores, each 32 (row, group) pairs),
+ * so a prompt's chunk costs its rows' times the bytes.
  */
 typedef struct {
     int R, T, max_blocks, n_pages, Hq, Hkv, d, d_idx, topk;
