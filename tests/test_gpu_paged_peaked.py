@@ -44,14 +44,14 @@ def expected(q, K, V, sv, scale):
     return o, lse, do, dz + steps + 2.0 ** -21 * (1 + np.abs(lse) + np.abs(m))
 
 
-def peaked(n, d, G, rest, value, seed=0):
+def peaked(n, d, G, rest, value, seed=0, least=9, most=16):
     """One request of n tokens, token 0 above the rest by 9 to 16 nats (another gap for each head).
     rest: the other tokens' logits all equal, or N(0, 1).  value: of the cache, every value one ("ones"), the sink's zero
     and the others' 0.5 + N(0, 1) / 2 ("sink"), the same with the scale of the sink's page and of one in the tail 2^12
     times the others', their other values at feature 0 alone ("scales"), or N(0, 1) ("normal")."""
     rng = np.random.default_rng(n + d + G + seed)
     table, n_pages = lay_out([n], rng)
-    gaps = 9 + 7 * np.arange(G) / max(1, G - 1)
+    gaps = least + (most - least) * np.arange(G) / max(1, G - 1)
     half = d // 2
     q = np.zeros((G, d))
     q[:, :half] = (gaps * np.sqrt(d) / half)[:, None]
@@ -89,7 +89,7 @@ def run(api, q, cache, table, n_pages, n, G, d, R=1, sel=None, k=16):
     qt, qv = bf(np.broadcast_to(q, (R, G, d)))
     ws = api.new_paged_workspace(sh, api.OP_PAGED_ATTN)
     s = None if sel is None else i32(np.broadcast_to(sel, (R, 1, k)))
-    o, lse = api.paged_attn(sh, qt, f8(k8), f8(v8), dev(ks), dev(vs), i32(np.broadcast_to(table, (R, table.shape[1]))), i32(np.arange(R)),
+    o, lse = api.paged_attn(sh, qt, f8(k8), f8(v8), dev(ks), dev(vs), i32(np.repeat(table, R, 0)), i32(np.arange(R)),
                             i32([n - 1] * R), sel_idx=s, workspace=ws)
     api.check_device_status(ws)
     blocks = np.arange((n + PAGE - 1) // PAGE) if sel is None else sel[sel >= 0]
@@ -145,3 +145,13 @@ def test_a_weight_that_grows_page_by_page(api):
         k8[table[0, c], 0, 17, :d // 2] = ref.e4m3_encode(np.full(d // 2, c * 0.03 / ks[table[0, c], 0]))
     run(api, q, cache, table, n_pages, n, G, d)
     run(api, q, cache, table, n_pages, n, G, d, R=400)
+
+
+@pytest.mark.parametrize("n,d", [(200, 64), (9000, 128)])
+@pytest.mark.parametrize("rest", ["equal", "normal"])
+@pytest.mark.parametrize("value", ["sink", "scales"])
+def test_tails_down_to_the_last_level(api, n, d, rest, value):
+    """Sixteen to thirty-six nats below a sink without value: 8 bits down to 2^-42 (29 nats; 21 where the sink's page has 2^12
+    times the scale), less behind that, nothing from 2^-50 on."""
+    q, cache, table, n_pages = peaked(n, d, 8, rest, value, least=16, most=36)
+    run(api, q, cache, table, n_pages, n, 8, d)
