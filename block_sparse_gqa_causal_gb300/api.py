@@ -27,6 +27,7 @@ LIB_PATH = os.path.join(_HERE, "libmsa.so")
 OP_INDEX_SELECT, OP_SPARSE_ATTN_FWD, OP_KL_FWD, OP_FUSED_BWD, OP_FUSED_BWD_KL, OP_TRAIN_STEP = 0, 1, 2, 3, 4, 5
 OP_WARMUP_KL = 6
 OP_PAGED_PLAN, OP_PAGED_APPEND, OP_PAGED_BLOCK_SCORES, OP_PAGED_BLOCK_TOPK, OP_PAGED_ATTN = 16, 17, 18, 19, 20
+OP_PAGED_FORK, OP_PAGED_COMPACT, OP_PAGED_COPY, OP_PAGED_CHUNK_SCORES, OP_PAGED_CHUNK_ATTN = 32, 33, 34, 35, 36
 PAGE = 128      # tokens of a cache page
 STATUS = {0: "MSA_OK", 1: "MSA_ERR_INVALID_ARGUMENT", 2: "MSA_ERR_UNSUPPORTED", 3: "MSA_ERR_WORKSPACE",
           4: "MSA_ERR_CUDA", 5: "MSA_ERR_TIMEOUT", 6: "MSA_ERR_DEVICE"}
@@ -34,7 +35,9 @@ EXPORTS = ("msa_workspace_size", "msa_index_select", "msa_sparse_attn_fwd", "msa
            "msa_fused_bwd_kl", "msa_train_step", "msa_train_step_staged", "msa_block_mask", "msa_warmup_kl",
            "msa_index_proj_workspace_size", "msa_index_proj_fwd", "msa_index_proj_bwd", "msa_kv_append",
            "msa_paged_workspace_size", "msa_paged_plan", "msa_paged_plan_held", "msa_paged_append", "msa_paged_block_scores",
-           "msa_paged_block_topk", "msa_paged_attn", "msa_last_error", "msa_check_device_status", "msa_version", "msa_launch_count")
+           "msa_paged_block_topk", "msa_paged_attn", "msa_paged_fork", "msa_paged_compact", "msa_paged_copy",
+           "msa_paged_chunk_scores", "msa_paged_chunk_attn", "msa_rotary_fwd", "msa_rotary_bwd", "msa_last_error", "msa_check_device_status",
+           "msa_version", "msa_launch_count")
 
 
 class MsaError(RuntimeError):
@@ -104,6 +107,19 @@ class _CPagedShape(ctypes.Structure):
         ("scale", ctypes.c_float), ("scale_idx", ctypes.c_float)]
 
 
+class _MoreCalls(dict):
+    """A shape's handles by op; those of OP_PAGED_COPY by (op, number of moves), made when they are first asked for."""
+
+    def __init__(self, fields, specs):
+        self.fields, self.copied = fields, specs.pop(OP_PAGED_COPY)
+        super().__init__({op: binding().prepare(op[0] if isinstance(op, tuple) else op, fields, args) for op, args in specs.items()})
+
+    def __missing__(self, op):
+        call, moves = op
+        self[op] = binding().prepare(call, self.fields, [("moves", (moves, 3), 0, 0), *self.copied])
+        return self[op]
+
+
 @dataclass(frozen=True)
 class PagedShape:
     """msa_paged_shape: R requests, T rows (query tokens) of a step, block tables
@@ -161,8 +177,38 @@ class PagedShape:
             OP_PAGED_ATTN: [("q", (T, self.Hq, D), bf, need), *cache(need), table, *row("row_req", "row_pos"),
                             ("sel_idx", sel, i32, maybe), ("o", (T, self.Hq, D), bf, out), ("lse", (T, self.Hq), f32, out)],
         }
-        fields = (R, T, self.max_blocks, N, self.Hq, H, D, self.d_idx, self.topk, self.scale, self.scale_idx)
-        return {op: binding().prepare(op, fields, args) for op, args in specs.items()}
+        return {op: binding().prepare(op, self._fields, args) for op, args in specs.items()}
+
+    @property
+    def _fields(self) -> tuple:
+        return (self.R, self.T, self.max_blocks, self.n_pages, self.Hq, self.Hkv, self.d, self.d_idx, self.topk, self.scale, self.scale_idx)
+
+    @cached_property
+    def _more_calls(self) -> "_MoreCalls":
+        """As _calls, of the calls for shared pages and chunks."""
+        i32, f32, bf, f8 = 0, 1, 2, 3
+        need, maybe, out = 0, 1, 2
+        R, T, H, N, D = self.R, self.T, self.Hkv, self.n_pages, self.d
+        table = ("block_table", (R, self.max_blocks), i32, need)
+        starts_pos = [table, ("q_starts", (R + 1,), i32, need), ("row_pos", (T,), i32, need)]
+        cache = lambda kind: ([(n, (N, H, PAGE, D), f8, kind) for n in ("k8", "v8")]  # noqa: E731
+                              + [(n, (N, H), f32, kind) for n in ("k_scale", "v_scale")])
+        k_idx = (N, PAGE, self.d_idx)
+        specs = {
+            OP_PAGED_FORK: [("src", (R,), i32, need), ("fork_lens", (R,), i32, maybe), ("lens", (R,), i32, need), ("held", (R,), i32, maybe),
+                            table, ("free_pages", (N,), i32, need), ("free_state", (2,), i32, need), ("shares", (N,), i32, need),
+                            ("moves", (R, 3), i32, out)],
+            OP_PAGED_COPY: [*cache(maybe), ("k_idx", k_idx, bf, maybe)],      # behind the moves, of any number
+            OP_PAGED_CHUNK_SCORES: [("q_idx", (T, H, self.d_idx), bf, need), ("k_idx", k_idx, bf, need), *starts_pos,
+                                    ("block_scores", (T, H, self.max_blocks), f32, out)],
+            OP_PAGED_CHUNK_ATTN: [("q", (T, self.Hq, D), bf, need), *cache(need), *starts_pos, ("sel_idx", (T, H, self.topk), i32, maybe),
+                                  ("o", (T, self.Hq, D), bf, out), ("lse", (T, self.Hq), f32, out)],
+        }
+        for op, given, made in ((OP_PAGED_COMPACT, need, out), ((OP_PAGED_COMPACT, None), maybe, maybe)):     # without shares none are written
+            specs[op] = [("lens", (R,), i32, need), ("held", (R,), i32, maybe), table, ("shares", (N,), i32, given),
+                         ("block_table", (R, self.max_blocks), i32, out), ("free_pages", (N,), i32, out), ("free_state", (2,), i32, out),
+                         ("shares", (N,), i32, made), ("moves", (max(1, N // 2), 3), i32, out)]
+        return _MoreCalls(self._fields, specs)
 
 
 class PagedPlan(NamedTuple):
@@ -176,6 +222,51 @@ class PagedPlan(NamedTuple):
     row_pos: torch.Tensor
     slots: torch.Tensor
     segs: torch.Tensor
+
+
+class PagedCompact(NamedTuple):
+    """What msa_paged_compact writes (int32 tensors): block_table [R, max_blocks],
+    free_pages [n_pages], free_state [2], shares [n_pages] (None without any) and
+    moves [max(1, n_pages // 2), 3]."""
+    block_table: torch.Tensor
+    free_pages: torch.Tensor
+    free_state: torch.Tensor
+    shares: torch.Tensor | None
+    moves: torch.Tensor
+
+
+class _CRotaryShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("T", "Hq", "Hkv", "d", "d_rot", "interleaved", "period", "offset")] + [
+        ("scale", ctypes.c_float)] + [(n, ctypes.c_longlong) for n in ("q_stride", "k_stride", "q_out_stride", "k_out_stride")]
+
+
+@dataclass(frozen=True)
+class RotaryShape:
+    """msa_rotary_shape: T tokens of Hq query and Hkv key heads of d features, the
+    first d_rot (0: all) of which turn, paired with those d_rot/2 further on or,
+    interleaved, with their neighbours.  Without positions token t is at offset
+    + t % period (0: T).  scale (0: 1) multiplies the turned features.  The
+    strides go by the tensors."""
+    T: int
+    Hq: int
+    Hkv: int
+    d: int
+    d_rot: int = 0
+    interleaved: bool = False
+    period: int = 0
+    offset: int = 0
+    scale: float = 0.0
+
+    def c(self) -> _CRotaryShape:
+        return _CRotaryShape(self.T, self.Hq, self.Hkv, self.d, self.d_rot or self.d, self.interleaved, self.period, self.offset, self.scale)
+
+    def __getstate__(self):
+        return {n: getattr(self, n) for n in self.__dataclass_fields__}     # as PagedShape's
+
+    @cached_property
+    def _call(self):
+        return binding().prepare_rotary(self.T, self.Hq, self.Hkv, self.d, self.d_rot or self.d, self.interleaved, self.period, self.offset,
+                                        self.scale)
 
 
 _lock = threading.Lock()
@@ -216,14 +307,20 @@ def lib() -> ctypes.CDLL:
             L.msa_paged_workspace_size.argtypes = [GS, ctypes.c_int]
             L.msa_paged_workspace_size.restype = sz
             for fn, ptrs in (("msa_paged_plan", 14), ("msa_paged_plan_held", 15), ("msa_paged_append", 11), ("msa_paged_block_scores", 8),
-                             ("msa_paged_block_topk", 4), ("msa_paged_attn", 12)):
+                             ("msa_paged_block_topk", 4), ("msa_paged_attn", 12), ("msa_paged_fork", 10), ("msa_paged_compact", 10),
+                             ("msa_paged_chunk_scores", 7), ("msa_paged_chunk_attn", 12)):
                 getattr(L, fn).argtypes = [GS] + [P] * ptrs + [sz, P]
+            L.msa_paged_copy.argtypes = [GS, P, ctypes.c_int, P, P, P, P, P, P, sz, P]
+            RS = ctypes.POINTER(_CRotaryShape)
+            for fn in ("msa_rotary_fwd", "msa_rotary_bwd"):
+                getattr(L, fn).argtypes = [RS] + [P] * 7
             L.msa_selftest_wait_timeout.argtypes = [P, ctypes.c_uint, P]
             for fn in ("msa_index_select", "msa_sparse_attn_fwd", "msa_kl_fwd", "msa_fused_bwd", "msa_fused_bwd_kl",
                        "msa_train_step", "msa_train_step_staged", "msa_check_device_status", "msa_block_mask",
                        "msa_warmup_kl", "msa_index_proj_fwd", "msa_index_proj_bwd", "msa_selftest_wait_timeout",
                        "msa_kv_append", "msa_paged_plan", "msa_paged_plan_held", "msa_paged_append", "msa_paged_block_scores",
-                       "msa_paged_block_topk", "msa_paged_attn"):
+                       "msa_paged_block_topk", "msa_paged_attn", "msa_paged_fork", "msa_paged_compact", "msa_paged_copy",
+                       "msa_paged_chunk_scores", "msa_paged_chunk_attn", "msa_rotary_fwd", "msa_rotary_bwd"):
                 getattr(L, fn).restype = ctypes.c_int
             L.msa_last_error.restype = ctypes.c_char_p
             L.msa_version.restype = ctypes.c_char_p
@@ -489,8 +586,9 @@ def _paged(shape: PagedShape, op: int, workspace, stream, *tensors):
             return _paged(shape, op, workspace, None, *tensors)
     if workspace is None:
         dev = next(t.device for t in tensors if t is not None)
-        workspace = new_paged_workspace(shape, op, dev)
-    r = (_binding or binding()).call(shape._calls[op], workspace, *tensors)
+        workspace = new_paged_workspace(shape, op[0] if type(op) is tuple else op, dev)
+    calls = shape._calls if op in shape._calls else shape._more_calls
+    r = (_binding or binding()).call(calls[op], workspace, *tensors)
     if type(r) is int:
         _check(r)
     return r
@@ -536,6 +634,93 @@ def paged_attn(shape: PagedShape, q, k8, v8, k_scale, v_scale, block_table, row_
     """msa_paged_attn: (o [T, Hq, d] bf16, lse [T, Hq] fp32) of q [T, Hq, d] bf16 over
     the 8-bit cache: the blocks of sel_idx [T, Hkv, topk], or all of them when it is None."""
     return _paged(shape, OP_PAGED_ATTN, workspace, stream, q, k8, v8, k_scale, v_scale, block_table, row_req, row_pos, sel_idx, o, lse)
+
+
+def paged_fork(shape: PagedShape, src, lens, block_table, free_pages, free_state, shares, *, fork_lens=None, held=None, moves=None,
+               workspace=None, stream=None):
+    """msa_paged_fork: slot r goes on from slot src[r]'s cache (r: as it is, -1: it
+    ends), from its first fork_lens[r] tokens (all of them).  src, fork_lens,
+    lens, held [R], block_table [R, max_blocks], free_pages, shares [n_pages] and
+    free_state [2] int32; all but src and fork_lens are updated in place.
+    Returns moves [R, 3], the copies that paged_copy has to make in each layer's
+    caches before anything is appended."""
+    return _paged(shape, OP_PAGED_FORK, workspace, stream, src, fork_lens, lens, held, block_table, free_pages, free_state, shares, moves)[0]
+
+
+def paged_compact(shape: PagedShape, lens, block_table, shares=None, *, held=None, out=None, workspace=None, stream=None) -> PagedCompact:
+    """msa_paged_compact: the pages in use moved to the front of the pool, for
+    paged_copy in each layer's caches.  lens, held [R], block_table [R, max_blocks],
+    shares [n_pages] int32.  Pass `out` to reuse its tensors; its block_table
+    and shares may be the tensors passed in."""
+    o = list(out or (None,) * 5)
+    if shares is None:
+        t, f, s, m = _paged(shape, (OP_PAGED_COMPACT, None), workspace, stream, lens, held, block_table, None, o[0], o[1], o[2], None, o[4])
+        return PagedCompact(t, f, s, None, m)
+    return PagedCompact(*_paged(shape, OP_PAGED_COMPACT, workspace, stream, lens, held, block_table, shares, *o))
+
+
+def paged_copy(shape: PagedShape, moves, k8, v8, k_scale, v_scale, k_idx, *, workspace=None, stream=None) -> None:
+    """msa_paged_copy: the moves [n, 3] int32 of paged_fork or paged_compact, made in a
+    layer's caches (as paged_append's).  The K and V group, or k_idx, may be None."""
+    _paged(shape, (OP_PAGED_COPY, moves.shape[0]), workspace, stream, moves, k8, v8, k_scale, v_scale, k_idx)
+
+
+def paged_chunk_scores(shape: PagedShape, q_idx, k_idx, block_table, q_starts, row_pos, *, block_scores=None, workspace=None, stream=None):
+    """msa_paged_chunk_scores: paged_block_scores for chunks of new tokens."""
+    return _paged(shape, OP_PAGED_CHUNK_SCORES, workspace, stream, q_idx, k_idx, block_table, q_starts, row_pos, block_scores)[0]
+
+
+def paged_chunk_attn(shape: PagedShape, q, k8, v8, k_scale, v_scale, block_table, q_starts, row_pos, *, sel_idx=None, o=None, lse=None,
+                     workspace=None, stream=None):
+    """msa_paged_chunk_attn: paged_attn for chunks of new tokens, (o [T, Hq, d] bf16, lse [T, Hq] fp32)."""
+    return _paged(shape, OP_PAGED_CHUNK_ATTN, workspace, stream, q, k8, v8, k_scale, v_scale, block_table, q_starts, row_pos, sel_idx, o, lse)
+
+
+def rotary_freqs(d_rot: int, base: float = 10000.0, *, factor: float = 1.0, original_len: int = 0, low: float = 1.0, high: float = 4.0,
+                 device=None) -> torch.Tensor:
+    """The frequencies of msa_rotary_fwd, d_rot/2 64-bit fractions of a turn, of f_i =
+    base^(-2i / d_rot) radians a position.  For contexts `factor` times longer: all
+    divided by it (original_len 0), or only those that turn `low` times or less over
+    the original_len tokens that the model was trained on; those that turn `high`
+    times or more stay, and between the two the share that is divided falls evenly."""
+    if d_rot < 2 or d_rot % 2 or not base > 1 or not factor >= 1 or original_len < 0 or not 0 <= low < high:
+        raise ValueError("rotary_freqs: need an even d_rot >= 2, base > 1, factor >= 1, original_len >= 0, 0 <= low < high")
+    turns = []
+    for i in range(d_rot // 2):
+        f = float(base) ** (-2 * i / d_rot) / (2 * math.pi)
+        kept = min(1.0, max(0.0, (original_len * f - low) / (high - low))) if original_len else 0.0
+        turns.append(round((f * kept + f / factor * (1 - kept)) * 2.0 ** 64))
+    return torch.tensor(turns, dtype=torch.int64, device=device or "cuda")
+
+
+def rotary_scale(factor: float) -> float:
+    """The usual scale of the turned features in contexts `factor` times longer: 1 + 0.1 ln factor."""
+    return 1.0 + 0.1 * math.log(factor) if factor > 1 else 1.0
+
+
+def _rotary(shape: RotaryShape, back: bool, q, k, freqs, positions, q_out, k_out, stream):
+    if stream is not None:
+        dev = freqs.device
+        if stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        with torch.cuda.stream(stream):
+            return _rotary(shape, back, q, k, freqs, positions, q_out, k_out, None)
+    r = (_binding or binding()).rotary(shape._call, back, q, k, positions, freqs, q_out, k_out)
+    if type(r) is int:
+        _check(r)
+    return r
+
+
+def rotary_fwd(shape: RotaryShape, q, k, freqs, *, positions=None, q_out=None, k_out=None, stream=None):
+    """msa_rotary_fwd: (q_out, k_out) of q [.., Hq, d] and k [.., Hkv, d] bf16, T tokens
+    each, evenly spaced (slices of one projection's output, say); one may be
+    None.  freqs: rotary_freqs'.  positions [T] int32.  q_out may be q, k_out k."""
+    return _rotary(shape, False, q, k, freqs, positions, q_out, k_out, stream)
+
+
+def rotary_bwd(shape: RotaryShape, dq_out, dk_out, freqs, *, positions=None, dq=None, dk=None, stream=None):
+    """msa_rotary_bwd: (dq, dk), the gradients of rotary_fwd's inputs from those of its outputs."""
+    return _rotary(shape, True, dq_out, dk_out, freqs, positions, dq, dk, stream)
 
 
 def check_device_status(workspace, stream=None) -> None:

@@ -123,4 +123,40 @@ cudaError_t launch_paged_attn(const PagedProblem &p, const bf16 *q, const uint8_
                               const int32_t *row_req, const int32_t *row_pos, const int32_t *sel, bf16 *o, float *lse,
                               float *scratch, DeviceStatus *st, cudaStream_t s);
 
+struct ForkArgs {
+    const int32_t *src, *fork_lens;
+    int32_t *lens, *held, *block_table, *free_pages, *free_state, *shares, *moves;
+};
+size_t paged_fork_scratch_bytes(const PagedProblem &p);
+cudaError_t launch_paged_fork(const PagedProblem &p, const ForkArgs &a, void *scratch, DeviceStatus *st, cudaStream_t s);
+
+struct CompactArgs {
+    const int32_t *lens, *held, *block_table, *shares;
+    int32_t *block_table_out, *free_pages, *free_state, *shares_out, *moves;
+};
+size_t paged_compact_scratch_bytes(const PagedProblem &p);
+cudaError_t launch_paged_compact(const PagedProblem &p, const CompactArgs &a, void *scratch, DeviceStatus *st, cudaStream_t s);
+
+cudaError_t launch_paged_copy(const PagedProblem &p, const int32_t *moves, int n_moves, uint8_t *k8, uint8_t *v8, float *k_scale,
+                              float *v_scale, bf16 *k_idx, DeviceStatus *st, cudaStream_t s);
+
+// Chunks of new tokens (paged_chunk.cu): scratch bytes of the tiles' plan, and for attention of the cut tiles' states.
+size_t paged_chunk_scratch_bytes(const PagedProblem &p, bool attention);
+cudaError_t launch_paged_chunk_scores(const PagedProblem &p, const bf16 *q_idx, const bf16 *k_idx, const int32_t *block_table,
+                                      const int32_t *q_starts, const int32_t *row_pos, float *scores, void *scratch, DeviceStatus *st,
+                                      cudaStream_t s);
+cudaError_t launch_paged_chunk_attn(const PagedProblem &p, const bf16 *q, const uint8_t *k8, const uint8_t *v8, const float *k_scale,
+                                    const float *v_scale, const int32_t *block_table, const int32_t *q_starts, const int32_t *row_pos,
+                                    const int32_t *sel, bf16 *o, float *lse, void *scratch, DeviceStatus *st, cudaStream_t s);
+
+// Rotary positions (rotary.cu).
+struct RotaryProblem {
+    int T, Hq, Hkv, d, d_rot, period, offset, num_sms;
+    bool interleaved, backward;
+    float scale;
+    long long q_stride, k_stride, q_out_stride, k_out_stride;
+};
+cudaError_t launch_rotary(const RotaryProblem &p, const bf16 *q, const bf16 *k, const int32_t *positions,
+                          const unsigned long long *freqs, bf16 *q_out, bf16 *k_out, cudaStream_t s);
+
 }  // namespace msa

@@ -1,5 +1,5 @@
-// paged_binding.cpp -- argument marshalling of the paged-cache calls for
-// Python: checks dtypes, shapes, layouts and devices, allocates the outputs
+// paged_binding.cpp -- argument marshalling of the paged-cache calls and the
+// rotary ones for Python: checks dtypes, shapes, layouts and devices, allocates the outputs
 // that were not given and passes raw pointers and the current CUDA stream to
 // the C-ABI.  The calls' kernels take a few microseconds for a decoding step;
 // the same checks written in Python took three times as long.
@@ -104,6 +104,16 @@ int launch(const Call &c, void *const *p, void *ws, size_t n, void *stream)
         return msa_paged_block_scores(&c.shape, p[0], p[1], i32(2), i32(3), i32(4), i32(5), f32(6), ws, n, stream);
     case MSA_OP_PAGED_BLOCK_TOPK:
         return msa_paged_block_topk(&c.shape, f32(0), i32(1), i32(2), ws, n, stream);
+    case MSA_OP_PAGED_FORK:
+        return msa_paged_fork(&c.shape, i32(0), i32(1), i32(2), i32(3), i32(4), i32(5), i32(6), i32(7), i32(8), ws, n, stream);
+    case MSA_OP_PAGED_COMPACT:
+        return msa_paged_compact(&c.shape, i32(0), i32(1), i32(2), i32(3), i32(4), i32(5), i32(6), i32(7), i32(8), ws, n, stream);
+    case MSA_OP_PAGED_COPY:
+        return msa_paged_copy(&c.shape, i32(0), (int)c.args[0].shape[0], p[1], p[2], f32(3), f32(4), p[5], ws, n, stream);
+    case MSA_OP_PAGED_CHUNK_SCORES:
+        return msa_paged_chunk_scores(&c.shape, p[0], p[1], i32(2), i32(3), i32(4), f32(5), ws, n, stream);
+    case MSA_OP_PAGED_CHUNK_ATTN:
+        return msa_paged_chunk_attn(&c.shape, p[0], p[1], p[2], f32(3), f32(4), i32(5), i32(6), i32(7), i32(8), p[9], f32(10), ws, n, stream);
     default:
         return msa_paged_attn(&c.shape, p[0], p[1], p[2], f32(3), f32(4), i32(5), i32(6), i32(7), i32(8), p[9], f32(10), ws, n,
                               stream);
@@ -212,7 +222,121 @@ PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t nargs)
     END_HANDLE_TH_ERRORS
 }
 
+constexpr const char *kRotaryCapsule = "msa_rotary_call";
+
+void destroy_rotary(PyObject *capsule) { delete static_cast<msa_rotary_shape *>(PyCapsule_GetPointer(capsule, kRotaryCapsule)); }
+
+// prepare_rotary(T, Hq, Hkv, d, d_rot, interleaved, period, offset, scale) -> handle of the calls
+PyObject *prepare_rotary(PyObject *, PyObject *args)
+{
+    auto s = std::make_unique<msa_rotary_shape>();
+    *s = msa_rotary_shape{};
+    if (!PyArg_ParseTuple(args, "iiiiipiif", &s->T, &s->Hq, &s->Hkv, &s->d, &s->d_rot, &s->interleaved, &s->period, &s->offset, &s->scale))
+        return nullptr;
+    PyObject *capsule = PyCapsule_New(s.get(), kRotaryCapsule, destroy_rotary);
+    if (capsule) s.release();
+    return capsule;
+}
+
+// The distance between the T tokens of a bf16 tensor [.., heads, d], a token's heads one after another; -1 where there is none.
+int64_t token_stride(const at::Tensor &t, int64_t T, int64_t heads, int64_t d)
+{
+    const int64_t n = t.dim();
+    if (n < 2 || t.scalar_type() != at::kBFloat16 || t.size(n - 1) != d || t.size(n - 2) != heads || t.numel() != T * heads * d) return -1;
+    if (t.stride(n - 1) != 1 || (heads > 1 && t.stride(n - 2) != d)) return -1;
+    int64_t stride = 0, next = 0;
+    for (int64_t i = n - 3; i >= 0; --i) {
+        if (t.size(i) == 1) continue;
+        if (!stride) stride = t.stride(i);
+        else if (t.stride(i) != next) return -1;
+        next = t.stride(i) * t.size(i);
+    }
+    return stride ? stride : heads * d;      // one token
+}
+
+// rotary(handle, backward, q, k, positions, freqs, q_out, k_out) -> (q_out, k_out), or the C call's status where that is not MSA_OK
+PyObject *rotary(PyObject *, PyObject *const *args, Py_ssize_t nargs)
+{
+    HANDLE_TH_ERRORS
+    if (nargs != 8) {
+        PyErr_SetString(PyExc_TypeError, "rotary(handle, backward, q, k, positions, freqs, q_out, k_out)");
+        return nullptr;
+    }
+    const auto *given = static_cast<const msa_rotary_shape *>(PyCapsule_GetPointer(args[0], kRotaryCapsule));
+    if (!given) return nullptr;
+    msa_rotary_shape s = *given;
+    auto complain = [](const std::string &what) {
+        PyErr_SetString(PyExc_ValueError, what.c_str());
+        return static_cast<PyObject *>(nullptr);
+    };
+    static const char *const names[] = {"q", "k", "positions", "freqs", "q_out", "k_out"};
+    const at::Tensor *t[6];
+    c10::optional<at::Device> dev;
+    for (int i = 0; i < 6; ++i) {
+        t[i] = nullptr;
+        if (args[2 + i] == Py_None) continue;
+        if (!THPVariable_Check(args[2 + i])) return complain(std::string(names[i]) + ": need a tensor");
+        t[i] = &THPVariable_Unpack(args[2 + i]);
+        if (!dev) dev = t[i]->device();
+        if (t[i]->device() != *dev) return complain(std::string(names[i]) + ": need a tensor on " + dev->str() + ", got " + described(*t[i]));
+    }
+    if (!dev || !dev->is_cuda()) return complain("need CUDA tensors" + (dev ? ", got " + dev->str() : std::string()));
+    if (!t[0] && !t[1]) return complain("q and k are None");
+    if (!t[3] || t[3]->scalar_type() != at::kLong || t[3]->sizes() != at::IntArrayRef({s.d_rot / 2}) || !t[3]->is_contiguous())
+        return complain("freqs: need a contiguous Long tensor of " + std::to_string(s.d_rot / 2) + " numbers" + (t[3] ? ", got " + described(*t[3]) : std::string()));
+    if (t[2] && (t[2]->scalar_type() != at::kInt || t[2]->numel() != s.T || !t[2]->is_contiguous()))
+        return complain("positions: need a contiguous Int tensor of " + std::to_string(s.T) + " numbers, got " + described(*t[2]));
+    const at::DeviceGuard guard(*dev);
+    long long *strides[4] = {&s.q_stride, &s.k_stride, &s.q_out_stride, &s.k_out_stride};
+    at::Tensor fresh[2];
+    void *ptr[4] = {};
+    for (int i = 0; i < 4; ++i) {
+        const int io = i & 1, heads = io ? s.Hkv : s.Hq, at = i < 2 ? i : 2 + i;
+        if (i >= 2 && !t[io]) {
+            if (t[at]) return complain(std::string(names[at]) + " without its input");
+            continue;
+        }
+        if (!t[at] && i >= 2) {
+            fresh[io] = at::empty(t[io]->sizes(), at::TensorOptions().dtype(at::kBFloat16).device(*dev));
+            ptr[i] = fresh[io].data_ptr();
+            continue;
+        }
+        if (!t[at]) continue;
+        const int64_t stride = token_stride(*t[at], s.T, heads, s.d);
+        if (stride < 0)
+            return complain(std::string(names[at]) + ": need BFloat16 [.., " + std::to_string(heads) + ", " + std::to_string(s.d) + "] of " +
+                            std::to_string(s.T) + " evenly spaced tokens, each contiguous, got " + described(*t[at]));
+        *strides[i] = stride;
+        ptr[i] = t[at]->data_ptr();
+    }
+    const int back = PyObject_IsTrue(args[1]);
+    if (back < 0) return nullptr;
+    const int status = (back ? msa_rotary_bwd : msa_rotary_fwd)(
+        &s, ptr[0], ptr[1], t[2] ? static_cast<int32_t *>(t[2]->data_ptr()) : nullptr, static_cast<unsigned long long *>(t[3]->data_ptr()), ptr[2], ptr[3],
+        c10::cuda::getCurrentCUDAStream(dev->index()).stream());
+    if (status != MSA_OK) return PyLong_FromLong(status);
+    PyObject *out = PyTuple_New(2);
+    if (!out) return nullptr;
+    for (int io = 0; io < 2; ++io) {
+        PyObject *obj = args[6 + io];
+        if (fresh[io].defined()) {
+            obj = THPVariable_Wrap(std::move(fresh[io]));
+            if (!obj) {
+                Py_DECREF(out);
+                return nullptr;
+            }
+        } else {
+            Py_INCREF(obj);
+        }
+        PyTuple_SET_ITEM(out, io, obj);
+    }
+    return out;
+    END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef methods[] = {
+    {"prepare_rotary", prepare_rotary, METH_VARARGS, nullptr},
+    {"rotary", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rotary)), METH_FASTCALL, nullptr},
     {"prepare", prepare, METH_VARARGS, nullptr},
     {"call", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};

@@ -1,0 +1,53 @@
+// paged_chunk.h -- the tiles that chunks of new tokens are cut into, shared by
+// the chunk calls' kernels (paged_chunk.cu, paged_chunk_attn.cu).
+#pragma once
+
+#include "paged.h"
+
+namespace msa {
+
+// Up to `tokens` consecutive rows of one request.
+struct ChunkTile {
+    int row, rows, req, pages;      // first row, rows, request; pages that its furthest row sees
+};
+
+// The plan: the number of tiles, the tiles in the order of rows, and the pages of those before each (one more than tiles).
+struct ChunkPlan {
+    int *n_tiles;
+    ChunkTile *tiles;
+    long long *before;
+    __host__ __device__ ChunkPlan(void *at, long long most)
+    {
+        n_tiles = static_cast<int *>(at);
+        tiles = reinterpret_cast<ChunkTile *>(n_tiles + 4);
+        before = reinterpret_cast<long long *>(tiles + most);
+    }
+    static size_t bytes(long long most) { return (size_t)(16 + most * sizeof(ChunkTile) + (most + 1) * 8 + 255) / 256 * 256; }
+};
+
+// Tiles of `tokens` rows that T rows of R requests make at most.
+inline long long chunk_tiles(const PagedProblem &p, int tokens)
+{
+    const long long whole = p.T / tokens, any = p.T;
+    return whole + p.R < any ? whole + p.R : any;
+}
+
+cudaError_t launch_chunk_plan(const PagedProblem &p, const int32_t *q_starts, const int32_t *row_pos, int tokens, void *plan,
+                              DeviceStatus *st, cudaStream_t s);
+
+// The last i < n with before[i] * scale <= w, by a whole warp (before[0] = 0 <= w).
+MSA_DEV int chunk_find(const long long *before, int n, long long scale, long long w, int lane)
+{
+    int lo = 0;
+    while (n - lo > 1) {
+        const int step = (n - lo + 31) / 32;
+        const int i = lo + lane * step;
+        const unsigned in = __ballot_sync(0xffffffffu, i < n && before[i] * scale <= w);
+        const int last = 31 - __clz(in);                 // lane 0's is always in
+        lo += last * step;
+        n = min(n, lo + step);
+    }
+    return lo;
+}
+
+}  // namespace msa

@@ -359,8 +359,8 @@ msa_status msa_kv_append(const msa_shape *shape, const void *k_new, const void *
  * msa_paged_workspace_size bytes with the status word of the other calls; its
  * first 4,096 bytes (all of a smaller one) have to be zero before the first
  * call on it, and again after msa_check_device_status() reported a timeout or
- * after a call that is not of these five (which may leave anything behind byte
- * 256); these five may share one, ordered on one stream.
+ * after a call that is not one of these (which may leave anything behind byte
+ * 256); the paged calls may share one, ordered on one stream.
  * What device memory says (lengths, pages, selections) is checked on the
  * device: an entry out of range is left out and recorded in the status word.
  * Outputs do not overlap inputs or one another, but where a call says so.
@@ -379,7 +379,12 @@ enum {
     MSA_OP_PAGED_APPEND = 17,
     MSA_OP_PAGED_BLOCK_SCORES = 18,
     MSA_OP_PAGED_BLOCK_TOPK = 19,
-    MSA_OP_PAGED_ATTN = 20
+    MSA_OP_PAGED_ATTN = 20,
+    MSA_OP_PAGED_FORK = 32,
+    MSA_OP_PAGED_COMPACT = 33,
+    MSA_OP_PAGED_COPY = 34,
+    MSA_OP_PAGED_CHUNK_SCORES = 35,
+    MSA_OP_PAGED_CHUNK_ATTN = 36
 };
 size_t msa_paged_workspace_size(const msa_paged_shape *shape, int op);
 
@@ -489,6 +494,123 @@ msa_status msa_paged_attn(const msa_paged_shape *shape, const void *q, const voi
                           const float *v_scale, const int32_t *block_table, const int32_t *row_req, const int32_t *row_pos,
                           const int32_t *sel_idx, void *o, float *lse, void *workspace, size_t workspace_bytes,
                           void *stream);
+
+/*
+ * Requests that go on from another request's cache (beams that change places,
+ * requests that start from a shared prompt), and pages that several tables
+ * hold.  Whole pages are shared: they are never written again, since new
+ * tokens go behind a request's length.  Each page has a count of the table
+ * entries that hold it besides the first:
+ *   shares [n_pages] int32   0 for a page in one table, and for a free one
+ * Where pages are shared, requests end through msa_paged_fork (src = -1), not
+ * through msa_paged_plan's `ended`, which gives pages back whoever else holds
+ * them; and a length is not lowered below what was forked.
+ *
+ * msa_paged_fork, for slot r with src[r] =
+ *   r         nothing happens
+ *   -1        the request ends: length 0, its pages let go
+ *   another s the request ends, and the slot goes on from the first n tokens of
+ *             what slot s held before the call (n = fork_lens[r], all lens[s]
+ *             where fork_lens is NULL): its first n / 128 pages are shared, and
+ *             if n ends inside a page the slot takes one from the ring's head
+ *             (slots in order) and moves[r] = {page of s, page taken, n % 128}
+ * moves of the other slots are {-1, -1, 0}; msa_paged_copy makes them, for
+ * each layer's caches.  Pages that no table holds any longer go behind the
+ * free ones, in the order of the ended requests' slots and blocks, and are
+ * free from the next call on.  lens, held (may be NULL, as in msa_paged_plan_held), block_table,
+ * free_pages, free_state ({head, count}) and shares are updated in place; table
+ * columns past a slot's pages are left as they were.
+ * A call that does not fit (a source, length, count of pages or ring state out
+ * of range, n > lens[s], more pages taken than were free) is not made: moves are
+ * {-1, -1, 0}, the rest stays, and the status word is set.  A table entry
+ * that is no page is passed over and recorded, a ring entry that is none is
+ * written to block_table as -1, its move left out, and recorded.
+ */
+msa_status msa_paged_fork(const msa_paged_shape *shape, const int32_t *src, const int32_t *fork_lens, int32_t *lens,
+                          int32_t *held, int32_t *block_table, int32_t *free_pages, int32_t *free_state, int32_t *shares,
+                          int32_t *moves, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The pages in use moved to the front of the pool, so that the rest of it can
+ * be given away.  With u pages in use (those in the first ceil(lens/128), or
+ * held, columns of any row), the i-th of those with a number >= u goes to the
+ * i-th free number below u:
+ *   moves [max(1, n_pages / 2), 3] int32   {from, to, 128}, then {-1, -1, 0}
+ * for msa_paged_copy, and the tables follow: block_table_out (columns past a
+ * row's pages as they were), shares_out (with shares; both may be NULL),
+ * free_pages {u, u + 1, .., n_pages - 1, then -1} and free_state {0, n_pages - u}.
+ * Pages that were in no table and not in the ring are free again.  block_table_out may be block_table and
+ * shares_out may be shares.  A length or count of pages out of range is taken
+ * as the nearest one that is in it, an entry that is no page is left as it
+ * is; both are recorded in the status word.
+ */
+msa_status msa_paged_compact(const msa_paged_shape *shape, const int32_t *lens, const int32_t *held, const int32_t *block_table,
+                             const int32_t *shares, int32_t *block_table_out, int32_t *free_pages, int32_t *free_state,
+                             int32_t *shares_out, int32_t *moves, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Copies between pages of the caches: for each of the n_moves {from, to, rows}
+ * the scales and the first `rows` tokens (at most 128); the other tokens of `to` are
+ * left as they were.  A move with from < 0 is none.  No page is in two moves, but as `from`.  The four K and V
+ * arrays may all be NULL, and so may k_idx.  Another move that names no
+ * page, or rows out of 0..128, is left out and recorded in the status word.
+ */
+msa_status msa_paged_copy(const msa_paged_shape *shape, const int32_t *moves, int n_moves, void *k8, void *v8, float *k_scale,
+                          float *v_scale, void *k_idx, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * msa_paged_block_scores and msa_paged_attn for chunks of new tokens: the same
+ * values from the same arrays, in tiles of 256 (row, head) pairs of a request
+ * that read a page once for all of them.  A request's rows are those from
+ * q_starts[r] to q_starts[r + 1], 0 <= q_starts[0], ascending, at most T; a row with a
+ * negative position, or behind the last request, is left as it was.
+ * A row_pos past 128 * max_blocks - 1, and starts that do not ascend, are left
+ * out and recorded in the status word.  Scores are made for any Hkv.
+ *
+ * Attention: queries enter the products as they are, probabilities with 8
+ * significant bits, however small; sums are fp32.  With a selection, a tile
+ * reads the blocks that any of its rows selected.  Entries that msa_paged_attn
+ * leaves out and records are left out and recorded here too.  Deterministic.
+ * A NaN in a cached row reaches those rows only that see it.
+ */
+msa_status msa_paged_chunk_scores(const msa_paged_shape *shape, const void *q_idx, const void *k_idx, const int32_t *block_table,
+                                  const int32_t *q_starts, const int32_t *row_pos, float *block_scores, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+msa_status msa_paged_chunk_attn(const msa_paged_shape *shape, const void *q, const void *k8, const void *v8, const float *k_scale,
+                                const float *v_scale, const int32_t *block_table, const int32_t *q_starts, const int32_t *row_pos,
+                                const int32_t *sel_idx, void *o, float *lse, void *workspace, size_t workspace_bytes,
+                                void *stream);
+
+/*
+ * Rotary positions for queries and keys, in training and before a cache is
+ * written.  The method's description leaves positions to the model.  Token t at
+ * position p has the pairs (x_i, x_j) of the first d_rot features of each head
+ * turned by p * f_i and scaled:
+ *   y_i = scale (x_i cos(p f_i) - x_j sin(p f_i))
+ *   y_j = scale (x_i sin(p f_i) + x_j cos(p f_i)),
+ * j = i + d_rot/2 for i < d_rot/2, or, interleaved, pairs (2i, 2i + 1); the
+ * features from d_rot on are copied.  msa_rotary_bwd takes the gradients of y to those of x: the
+ * transposed map.
+ *   q, q_out [T, Hq, d], k, k_out [T, Hkv, d] bf16, the heads of a token one
+ *           after another, tokens q_stride, .. elements apart (0: Hq * d, Hkv * d);
+ *           a pair may be NULL; an output may be its input (same stride), nothing else overlaps
+ *   positions [T] int32; a token with a negative one is left as it was.  NULL:
+ *           offset + t % period (0: T)
+ *   freqs   [d_rot / 2] 64-bit: f_i / 2 pi turns, as a fraction of 2^64, so that
+ *           p * freqs[i] mod 2^64 is the angle's turn, exact at any position
+ * Supported: d a multiple of 16 up to 256, d_rot a multiple of 16 up to d,
+ * strides multiples of 8.  16-byte alignment of q, k and their outputs.  Cosines and
+ * sines are fp32, results rounded once.
+ */
+typedef struct {
+    int T, Hq, Hkv, d, d_rot, interleaved, period, offset;
+    float scale;         /* 0 -> 1 */
+    long long q_stride, k_stride, q_out_stride, k_out_stride;
+} msa_rotary_shape;
+msa_status msa_rotary_fwd(const msa_rotary_shape *shape, const void *q, const void *k, const int32_t *positions,
+                          const unsigned long long *freqs, void *q_out, void *k_out, void *stream);
+msa_status msa_rotary_bwd(const msa_rotary_shape *shape, const void *dq_out, const void *dk_out, const int32_t *positions,
+                          const unsigned long long *freqs, void *dq, void *dk, void *stream);
 
 /* Message of the last failed call on this host thread ("" if none). */
 const char *msa_last_error(void);
