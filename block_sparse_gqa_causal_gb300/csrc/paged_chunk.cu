@@ -54,7 +54,7 @@ __device__ long long plan_scan(long long x, long long *buf, long long &total)
 
 // One CTA: a request to a thread, then a tile to a thread, then a tile to a warp for the furthest position of its rows.
 __global__ void __launch_bounds__(kPlanThreads)
-chunk_plan_kernel(PagedProblem p, const int32_t *q_starts, const int32_t *row_pos, int tokens, int most, void *at, DeviceStatus *st)
+chunk_plan_kernel(PagedProblem p, const int32_t *q_starts, const int32_t *row_pos, int tokens, int pairs, int most, void *at, DeviceStatus *st)
 {
     __shared__ int first[kPlanThreads], start[kPlanThreads], rows[kPlanThreads];
     __shared__ long long buf[32];
@@ -108,7 +108,7 @@ chunk_plan_kernel(PagedProblem p, const int32_t *q_starts, const int32_t *row_po
     for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
         const int i = i0 + tid;
         long long all;
-        const long long mine = plan_scan(i < n ? plan.tiles[i].pages : 0, buf, all);
+        const long long mine = plan_scan(i < n ? plan.tiles[i].pages * tile_halves(plan.tiles[i].rows * pairs) : 0, buf, all);
         if (i < n) plan.before[i] = sum + mine;
         sum += all;
     }
@@ -119,8 +119,8 @@ chunk_plan_kernel(PagedProblem p, const int32_t *q_starts, const int32_t *row_po
 }
 
 // ---------------------------------------------------------------- scores
-constexpr int kTileRows = 256;
 constexpr int kStages = 3;
+constexpr int kLeast = 2;                      // units of work to a stretch at least
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr int kSub = 128 * 128;               // [128 rows][64 bf16], swizzled
@@ -134,27 +134,31 @@ struct ScoresSmem {
     static constexpr int BYTES = (OFF_BAR + 256 > 120 * 1024 ? OFF_BAR + 256 : 120 * 1024) + 1024;
 };
 
-// One stretch's walk over its tiles; every warp has its own.
+// One stretch's walk over its tiles; every warp has its own.  A page belongs to the stretch that its first unit is in.
 struct Walk {
     ChunkPlan plan;
-    int parts;                      // head parts of a tile
+    int parts, pairs;               // head parts of a tile, pairs of a token
     long long at, end;
-    int i, part, c0, c1;            // tile, head part, pages [c0, c1)
+    int i, part, c0, c1, mt;        // tile, head part, pages [c0, c1), halves
     ChunkTile t;
-    __device__ Walk(const ChunkPlan &pl, int parts_, long long from, long long to, int tile)
-        : plan(pl), parts(parts_), at(from), end(to), i(tile)
+    __device__ Walk(const ChunkPlan &pl, int parts_, int pairs_, long long from, long long to, int tile)
+        : plan(pl), parts(parts_), pairs(pairs_), at(from), end(to), i(tile)
     {
     }
     __device__ bool next()
     {
-        if (at >= end) return false;
-        while (at >= plan.before[i + 1] * parts) ++i;    // tiles without pages are passed over
-        t = plan.tiles[i];
-        const long long in = at - plan.before[i] * parts;
-        part = (int)(in / t.pages);
-        c0 = (int)(in - (long long)part * t.pages);
-        c1 = (int)min((long long)t.pages, c0 + (end - at));
-        at += c1 - c0;
+        do {
+            if (at >= end) return false;
+            while (at >= plan.before[i + 1] * parts) ++i;    // tiles without pages are passed over
+            t = plan.tiles[i];
+            mt = tile_halves(t.rows * pairs);
+            const long long in = at - plan.before[i] * parts, whole = (long long)t.pages * mt;
+            part = (int)(in / whole);
+            const long long off = in - part * whole, stop = min(whole, off + (end - at));
+            c0 = (int)((off + mt - 1) / mt);
+            c1 = (int)((stop + mt - 1) / mt);
+            at += stop - off;
+        } while (c0 >= c1);
         return true;
     }
 };
@@ -203,14 +207,14 @@ chunk_scores_kernel(PagedProblem p, const __grid_constant__ CUtensorMap tmap_q, 
 
     const ChunkPlan plan(plan_at, most);
     const int n_tiles = *plan.n_tiles;
-    const long long total = plan.before[n_tiles] * parts, share = (total + gridDim.x - 1) / gridDim.x;
-    const long long from = min(total, share * blockIdx.x), to = min(total, from + share);
+    const ChunkShare mine(plan.before[n_tiles] * parts, gridDim.x, kLeast, blockIdx.x);
+    const long long from = mine.from, to = mine.to;
     if (warp == 0) {
         const int i = from < to ? chunk_find(plan.before, n_tiles, parts, from, lane) : 0;
         if (lane == 0) sh_tile = i;
     }
     __syncthreads();
-    Walk walk(plan, parts, from, to, sh_tile);
+    Walk walk(plan, parts, p.Hkv, from, to, sh_tile);
 
     if (warp == 0) {
         int n = 0, qn = 0, q_issued = 0, issued = 0;
@@ -219,8 +223,7 @@ chunk_scores_kernel(PagedProblem p, const __grid_constant__ CUtensorMap tmap_q, 
             const int a = qn & 1;
             if (!(ok = mbar_wait_warp(&q_empty[a], ((uint32_t)(qn >> 1) & 1u) ^ 1u, st, 172, abort_flag))) break;
             const long long first = (long long)walk.t.row * p.Hkv + walk.part * kTileRows;
-            const int here = parts > 1 ? min(kTileRows, p.Hkv - walk.part * kTileRows) : walk.t.rows * p.Hkv;
-            const int mt = here > 128 ? 2 : 1;
+            const int mt = walk.mt;
             if (elect_one()) {
                 mbar_arrive_expect_tx(&q_full[a], mt * S::KB * kSub);
                 for (int m = 0; m < mt; ++m)
@@ -261,8 +264,7 @@ chunk_scores_kernel(PagedProblem p, const __grid_constant__ CUtensorMap tmap_q, 
         bool ok = true;
         while (ok && walk.next()) {
             const int aq = qn & 1;
-            const int here = parts > 1 ? min(kTileRows, p.Hkv - walk.part * kTileRows) : walk.t.rows * p.Hkv;
-            const int mt = here > 128 ? 2 : 1;
+            const int mt = walk.mt;
             if (!(ok = mbar_wait_warp(&q_full[aq], (uint32_t)(qn >> 1) & 1u, st, 175, abort_flag))) break;
             const uint64_t dq = sdesc_k128(smem_u32(smem + aq * S::Q));
             for (int c = walk.c0; c < walk.c1; ++c, ++n) {
@@ -297,7 +299,7 @@ chunk_scores_kernel(PagedProblem p, const __grid_constant__ CUtensorMap tmap_q, 
         bool ok = true;
         while (ok && walk.next()) {
             const int here = parts > 1 ? min(kTileRows, p.Hkv - walk.part * kTileRows) : walk.t.rows * p.Hkv;
-            const int mt = here > 128 ? 2 : 1;
+            const int mt = walk.mt;
             const long long rho = (long long)walk.t.row * p.Hkv + walk.part * kTileRows + row;
             const bool mine = row < here;
             int pos = mine ? row_pos[rho / p.Hkv] : -1;
@@ -389,11 +391,11 @@ chunk_scores_kernel(PagedProblem p, const __grid_constant__ CUtensorMap tmap_q, 
 
 }  // namespace
 
-cudaError_t launch_chunk_plan(const PagedProblem &p, const int32_t *q_starts, const int32_t *row_pos, int tokens, void *plan,
+cudaError_t launch_chunk_plan(const PagedProblem &p, const int32_t *q_starts, const int32_t *row_pos, int tokens, int pairs, void *plan,
                               DeviceStatus *st, cudaStream_t s)
 {
     return launch_chained("paged_chunk_plan_kernel", chunk_plan_kernel, dim3(1), kPlanThreads, 0, s, p, q_starts, row_pos, tokens,
-                          (int)chunk_tiles(p, tokens), plan, st);
+                          pairs, (int)chunk_tiles(p, tokens), plan, st);
 }
 
 // Rows of a tile: as many as make 256 (row, group) pairs; a row with more groups than that is cut into parts.
@@ -406,7 +408,7 @@ cudaError_t launch_paged_chunk_scores(const PagedProblem &p, const bf16 *q_idx, 
                                       cudaStream_t s)
 {
     const int tokens = score_tokens(p), parts = p.Hkv > kTileRows ? (p.Hkv + kTileRows - 1) / kTileRows : 1;
-    cudaError_t e = launch_chunk_plan(p, q_starts, row_pos, tokens, scratch, st, s);
+    cudaError_t e = launch_chunk_plan(p, q_starts, row_pos, tokens, p.Hkv, scratch, st, s);
     if (e != cudaSuccess) return e;
     CUtensorMap tq, tk;
     const unsigned long long pairs = (unsigned long long)p.T * p.Hkv;

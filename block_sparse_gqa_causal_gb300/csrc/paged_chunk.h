@@ -11,7 +11,13 @@ struct ChunkTile {
     int row, rows, req, pages;      // first row, rows, request; pages that its furthest row sees
 };
 
-// The plan: the number of tiles, the tiles in the order of rows, and the pages of those before each (one more than tiles).
+constexpr int kTileRows = 256;      // (row, head) pairs of a tile: two products of 128 rows
+
+// Products that a page costs a tile of `pairs` pairs.
+__host__ __device__ __forceinline__ int tile_halves(int pairs) { return pairs > kTileRows / 2 ? 2 : 1; }
+
+// The plan: the number of tiles, the tiles in the order of rows, and the work of those before each (one more than
+// tiles), in products: pages x halves.
 struct ChunkPlan {
     int *n_tiles;
     ChunkTile *tiles;
@@ -32,8 +38,21 @@ inline long long chunk_tiles(const PagedProblem &p, int tokens)
     return whole + p.R < any ? whole + p.R : any;
 }
 
-cudaError_t launch_chunk_plan(const PagedProblem &p, const int32_t *q_starts, const int32_t *row_pos, int tokens, void *plan,
+// pairs: those of a token.
+cudaError_t launch_chunk_plan(const PagedProblem &p, const int32_t *q_starts, const int32_t *row_pos, int tokens, int pairs, void *plan,
                               DeviceStatus *st, cudaStream_t s);
+
+// The stretch of CTA `cta`: work units [from, to) of `total`.
+struct ChunkShare {
+    long long share, from, to;
+    __host__ __device__ ChunkShare(long long total, int ctas, int least, int cta)
+    {
+        share = (total + ctas - 1) / ctas;
+        if (share < least) share = least;
+        from = share * cta < total ? share * cta : total;
+        to = from + share < total ? from + share : total;
+    }
+};
 
 // The last i < n with before[i] * scale <= w, by a whole warp (before[0] = 0 <= w).
 MSA_DEV int chunk_find(const long long *before, int n, long long scale, long long w, int lane)
