@@ -13,15 +13,13 @@
 // halves, A and B, whose products alternate on the tensor cores while the other
 // half's scores become probabilities.
 //
-// Codes to bf16.  e4m3 products would need queries and probabilities as pairs
-// of e4m3 terms, and small probabilities as several levels of those; as bf16
-// everything is exact but the probabilities' own 8 bits, at any size.  An
-// e4m3 value is a bf16 with its exponent moved: the code's bits shifted into
-// place, times 2^120, exact for subnormal codes too.  Four warps do that once a
-// page for both halves (one value converted to a probability computed); they
-// keep the order 0, 2, 1, 3 of each four features, in which two pairs of bytes
-// come out of a word without being sorted.  The queries are laid down in that
-// order, and O's columns are put right when they are written.
+// Codes to 16 bits.  e4m3 products would need queries and probabilities as pairs
+// of e4m3 terms, and small probabilities as several levels of those.  So four
+// warps turn the codes into 16-bit tiles, once a page for both halves (one value
+// converted to a probability computed): K to fp16, which is one instruction for
+// two codes, against queries brought to fp16 by a power of two for each row and
+// head; V to bf16, so that probabilities keep their 8 bits at any size, which
+// takes five.
 //
 // Softmax.  With t_j = l_j log2 e + log2 vs, the weight of token j's codes is
 // 2^t_j and that of the sum 2^t_j / vs, so one reference m per row bounds both
@@ -43,8 +41,8 @@
 // A: its pages go to the two halves in turn, both with the same queries, and A joins them.
 //   warps 0..3, 4..7   softmax of half A, B, a pair to a thread
 //   warps 8..11        codes of K and V to bf16 tiles in shared memory, loaded a tile ahead
-//   warp 12            tcgen05.mma issuer
-//   warp 13            planner: pages, scales and masks, through a ring
+//   warps 12, 13       tcgen05.mma issuers of half A, B
+//   warp 14            planner: pages, scales and masks, through a ring
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -61,7 +59,7 @@ namespace {
 using namespace tc;
 
 constexpr int kSoftWarps = 8, kCodeWarps = 4;
-constexpr int kCode0 = kSoftWarps, kMma = kCode0 + kCodeWarps, kPlanner = kMma + 1;
+constexpr int kCode0 = kSoftWarps, kMma = kCode0 + kCodeWarps, kPlanner = kMma + 2;
 constexpr int kThreads = 32 * (kPlanner + 1);
 constexpr int kStages = 2;                    // K and V tiles
 constexpr int kRing = 8;                      // pages the planner is ahead
@@ -71,6 +69,28 @@ constexpr float kLag = 8.f;                   // log2 of what a probability may 
 constexpr int kMaskWords = kTileRows / 32;    // a bit to each row of a tile (at most 256, with G = 1)
 constexpr int kWindow = 1 << 15;              // blocks whose union is taken in one go
 constexpr int kListWarps = 4;
+
+// mbar_wait_warp of tc.cuh with its failure out of line: it is in two dozen places, and the kernel's code has to stay in the
+// instruction cache (at 180 KB every wait cost 400 cycles, and a page 12,000 instead of 3,000).
+__device__ __forceinline__ void gave_up(DeviceStatus *st, int site, int parity, volatile int *abort_flag)
+{
+    report(st, kDevTimeout, site, parity);
+    *abort_flag = 1;
+}
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, DeviceStatus *st, int site, volatile int *abort_flag)
+{
+    bool ok = mbar_try_wait(bar, parity);
+    for (uint32_t it = 0; !ok; ++it) {
+        ok = mbar_try_wait(bar, parity);
+        if ((it & 1023u) != 1023u || ok) continue;
+        if (*abort_flag) break;
+        if (it >= (1u << 21)) {                // seconds
+            gave_up(st, site, (int)parity, abort_flag);
+            break;
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
 
 enum Kind { kPageEntry = 0, kEndEntry = 1, kExit = 2 };
 
@@ -139,6 +159,7 @@ struct Args {
     bf16 *o;
     float *lse;
     int tokens, words, ctas;   // rows of a tile, mask words of an entry
+    int shift;                 // log2 G
     DeviceStatus *st;
 };
 
@@ -274,96 +295,159 @@ __global__ void __launch_bounds__(1024) chunk_sum_kernel(Args a, AttnPlan plan)
 struct Pieces {
     const AttnPlan &plan;
     const Args &a;
-    long long n_items, total;
+    int n_items;                // at most rows x groups
+    long long total;
     __device__ Pieces(const AttnPlan &pl, const Args &ar) : plan(pl), a(ar)
     {
         const int n = *pl.tiles.n_tiles;
-        n_items = (long long)n * ar.p.Hkv;
+        n_items = n * ar.p.Hkv;
         total = ar.sel ? pl.before[n_items] : pl.tiles.before[n] * ar.p.Hkv;
     }
     // the item that unit w is in, by a whole warp
-    __device__ long long find(long long w, int lane) const
+    __device__ int find(long long w, int lane) const
     {
-        if (a.sel) return chunk_find(plan.before, (int)n_items, 1, w, lane);
+        if (a.sel) return chunk_find(plan.before, n_items, 1, w, lane);
         const int i = chunk_find(plan.tiles.before, *plan.tiles.n_tiles, a.p.Hkv, w, lane);
         const long long in = w - plan.tiles.before[i] * a.p.Hkv, one = plan.tiles.before[i + 1] - plan.tiles.before[i];
-        return (long long)i * a.p.Hkv + in / one;
+        return i * a.p.Hkv + (int)(in / one);
     }
-    __device__ long long start(long long item) const
+    __device__ long long start(int item) const
     {
         if (a.sel) return plan.before[item];
-        const long long i = item / a.p.Hkv, one = plan.tiles.before[i + 1] - plan.tiles.before[i];
+        const int i = item / a.p.Hkv;
+        const long long one = plan.tiles.before[i + 1] - plan.tiles.before[i];
         return plan.tiles.before[i] * a.p.Hkv + one * (item % a.p.Hkv);
     }
-    __device__ int pages(long long item) const { return a.sel ? plan.pages[item] : plan.tiles.tiles[item / a.p.Hkv].pages; }
+    __device__ int pages(int item) const { return a.sel ? plan.pages[item] : plan.tiles.tiles[item / a.p.Hkv].pages; }
 };
 
 // Pages [c0, c1) of an item of `pages` pages from unit `start` on that are [from, to)'s, a page where its first unit is.
 __device__ __forceinline__ void cut(long long start, int pages, int mt, long long from, long long to, int &c0, int &c1)
 {
-    const long long off = max(0ll, from - start), stop = min((long long)pages * mt, to - start);
-    c0 = (int)((off + mt - 1) / mt);
-    c1 = stop > 0 ? (int)((stop + mt - 1) / mt) : 0;
+    const long long off = max(0ll, from - start), stop = max(0ll, min((long long)pages * mt, to - start));
+    c0 = (int)((off + mt - 1) >> (mt - 1));            // mt is 1 or 2
+    c1 = (int)((stop + mt - 1) >> (mt - 1));
 }
 
 // ---------------------------------------------------------------- the kernel
-// Four e4m3 codes to bf16: features 0 and 2, then 1 and 3.
-__device__ __forceinline__ uint2 widen(uint32_t w)
+// Two e4m3 codes to fp16, exactly (a NaN to a NaN).
+__device__ __forceinline__ uint32_t widen(uint16_t codes)
 {
-    const __nv_bfloat162 up = __halves2bfloat162(__ushort_as_bfloat16(0x7B80), __ushort_as_bfloat16(0x7B80));   // 2^120
-    uint32_t even = ((w << 4) & 0x07F007F0u) | ((w << 8) & 0x80008000u), odd = ((w >> 4) & 0x07F007F0u) | (w & 0x80008000u);
-    const __nv_bfloat162 e = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&even), up), o = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&odd), up);
-    return make_uint2(*reinterpret_cast<const uint32_t *>(&e), *reinterpret_cast<const uint32_t *>(&o));
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(r) : "h"(codes));
+    return r;
+}
+__device__ __forceinline__ uint32_t to_bf16(uint32_t h)
+{
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    return pack_bf16(f.x, f.y);
 }
 // The codes among four that are NaN (0x7F, 0xFF), bit 7 of each byte.
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
-// Writes the tile of 128 tokens that this thread's words `u` are part of.  NaNs stay (K) or become 0 and are told (V).
+// A tile's codes as the four warps take them: 16 at a time, eight tokens by 64 features to a warp's load, so that eight
+// lanes store to eight different places of the swizzle.
+template <int D>
+struct Place {
+    int token, feature;        // of word 0; word j's is kStep tokens on
+    static constexpr int kWords = D / 16, kStep = D == 128 ? 16 : 32;
+    __device__ explicit Place(int tid)
+    {
+        const int w = tid >> 5, lane = tid & 31;
+        token = (D == 128 ? w >> 1 : w) * 8 + (lane & 7);
+        feature = (D == 128 ? (w & 1) * 64 : 0) + (lane >> 3) * 16;
+    }
+};
+// Writes this thread's words of a tile of 128 tokens, K as fp16, V as bf16; of V, true where a code is NaN (to be mended).
 template <int D, bool V>
-__device__ __forceinline__ bool lay_down(uint8_t *tile, const uint4 (&u)[D / 16], int tid)
+__device__ __forceinline__ bool lay_down(uint8_t *tile, const uint4 (&u)[D / 16], const Place<D> &at)
 {
-    constexpr int CPR = D / 16;           // 16-code words of a token
-    bool nan = false;
+    const int c = (at.feature & 63) >> 3, r = at.token & 7;
+    uint8_t *row = tile + (at.feature >> 6) * kSub + at.token * 128;
+    uint8_t *place[2] = {row + ((c ^ r) << 4), row + (((c + 1) ^ r) << 4)};
+    __half2 sum = __float2half2_rn(0.f);           // at most 64 codes of at most 448
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) {
-        const int i = tid + 128 * j, r = i / CPR, c = i % CPR;
-        uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
-        uint32_t x[8];
-        const uint32_t bad = nan_codes(w[0]) | nan_codes(w[1]) | nan_codes(w[2]) | nan_codes(w[3]);
-        if (V && bad) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t b = nan_codes(w[k]);
-                w[k] &= ~(b | (b - (b >> 7)));
-            }
-            nan = true;
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint2 v = widen(w[k]);
-            x[2 * k] = v.x;
-            x[2 * k + 1] = v.y;
-            if (!V && bad) {
-                const uint32_t b = nan_codes(w[k]);
-                if (b & 0x80u) x[2 * k] |= 0x00007FC0u;
-                if (b & 0x800000u) x[2 * k] |= 0x7FC00000u;
-                if (b & 0x8000u) x[2 * k + 1] |= 0x00007FC0u;
-                if (b & 0x80000000u) x[2 * k + 1] |= 0x7FC00000u;
-            }
-        }
-        // the 32 bytes' two halves in an order that keeps eight lanes on different banks
-        uint8_t *row = tile + (c >> 2) * kSub + r * 128;
-        const int at = 2 * (c & 3), turn = (c >> 2) & 1;
+        const uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int k = h ^ turn;
-            const uint4 y = k ? make_uint4(x[4], x[5], x[6], x[7]) : make_uint4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<uint4 *>(row + (((at + k) ^ (r & 7)) << 4)) = y;
+            uint32_t x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t y = w[2 * h + (k >> 1)];
+                x[k] = widen((uint16_t)(k & 1 ? y >> 16 : y));
+                if constexpr (V) {
+                    sum = __hadd2(sum, *reinterpret_cast<const __half2 *>(&x[k]));
+                    x[k] = to_bf16(x[k]);
+                }
+            }
+            *reinterpret_cast<uint4 *>(place[h] + j * Place<D>::kStep * 128) = make_uint4(x[0], x[1], x[2], x[3]);
         }
     }
-    return nan;
+    return V && (__hisnan(__low2half(sum)) || __hisnan(__high2half(sum)));
+}
+// Its NaNs of V to 0.
+template <int D>
+__device__ __forceinline__ void mend(uint8_t *tile, const uint8_t *codes, const Place<D> &p)
+{
+#pragma unroll 1
+    for (int j = 0; j < D / 16; ++j) {
+#pragma unroll 1
+        for (int k = 0; k < 16; ++k) {
+            const int r = p.token + j * Place<D>::kStep, f = p.feature + k;
+            if ((codes[r * D + f] & 0x7F) != 0x7F) continue;
+            *reinterpret_cast<uint16_t *>(tile + (f >> 6) * kSub + r * 128 + ((((f & 63) >> 3) ^ (r & 7)) << 4) + (f & 7) * 2) = 0;
+        }
+    }
 }
 
+// The NaN features of the visible tokens' V codes into a row that has been written.
+template <int D>
+__device__ __forceinline__ void spoil(const Args &a, const AttnPlan &plan, const Item &it, int pos, int token, float *part, bf16 *o)
+{
+#pragma unroll 1
+    for (int c = it.c0; c < it.c1; ++c) {
+        const int block = a.sel ? plan.blocks[it.at + c] : c, page = a.block_table[(long long)it.req * a.p.max_blocks + block];
+        if ((unsigned)page >= (unsigned)a.p.n_pages) continue;
+        if (a.sel && !(plan.masks[(it.at + c) * a.words + (token >> 5)] >> (token & 31) & 1)) continue;
+        const uint4 *row = reinterpret_cast<const uint4 *>(a.v8 + ((long long)page * a.p.Hkv + it.group) * kPage * D);
+#pragma unroll 1
+        for (int j = 0; j < kPage && block * kPage + j <= pos; ++j)
+#pragma unroll 1
+            for (int w = 0; w < D / 16; ++w) {
+                const uint4 u = row[j * (D / 16) + w];
+                if (!(nan_codes(u.x) | nan_codes(u.y) | nan_codes(u.z) | nan_codes(u.w))) continue;
+                const uint8_t *codes = reinterpret_cast<const uint8_t *>(row + j * (D / 16) + w);
+#pragma unroll 1
+                for (int k = 0; k < 16; ++k) {
+                    if ((codes[k] & 0x7F) != 0x7F) continue;
+                    const int f = w * 16 + k;
+                    if (part) part[f] = __uint_as_float(0x7FC00000u);
+                    else o[f] = __ushort_as_bfloat16(0x7FC0);
+                }
+            }
+    }
+}
+
+__device__ __forceinline__ uint64_t pair(float x, float y)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void split(uint64_t v, float &x, float &y) { asm("mov.b64 {%0, %1}, %2;\n" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 chunk_attn_kernel(Args a, AttnPlan plan)
@@ -389,14 +473,14 @@ chunk_attn_kernel(Args a, AttnPlan plan)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&ring_full[i], 1);
-            mbar_init(&ring_empty[i], kSoftWarps + kCodeWarps + 1);
+            mbar_init(&ring_empty[i], kSoftWarps + kCodeWarps + 2);
             nan_item[i] = -1;
         }
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&k_full[i], kCodeWarps);
-            mbar_init(&k_empty[i], 1);
+            mbar_init(&k_empty[i], 2);
             mbar_init(&v_full[i], kCodeWarps);
-            mbar_init(&v_empty[i], 1);
+            mbar_init(&v_empty[i], 2);
         }
         for (int h = 0; h < 2; ++h) {
             mbar_init(&q_full[h], 4);
@@ -404,7 +488,7 @@ chunk_attn_kernel(Args a, AttnPlan plan)
             mbar_init(&p_full[h], 4);
             mbar_init(&o_full[h], 1);
         }
-        mbar_init(drained, 1);
+        mbar_init(drained, 2);
         mbar_init(b_ready, 4);
         mbar_init(b_read, 4);
         *abort_flag = 0;
@@ -422,7 +506,7 @@ chunk_attn_kernel(Args a, AttnPlan plan)
     chain_wait(a.q, a.k8, a.v8, a.k_scale, a.v_scale, a.block_table, a.row_pos, a.sel, a.o, a.lse);
 
     // the ring's next entry, for a consumer
-    auto wait_entry = [&](int e) { return mbar_wait_warp(&ring_full[e % kRing], (uint32_t)(e / kRing) & 1u, st, 181, abort_flag); };
+    auto wait_entry = [&](int e) { return wait(&ring_full[e % kRing], (uint32_t)(e / kRing) & 1u, st, 181, abort_flag); };
     auto done_entry = [&](int e) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&ring_empty[e % kRing]);
@@ -433,7 +517,7 @@ chunk_attn_kernel(Args a, AttnPlan plan)
         const ChunkShare mine(pieces.total, gridDim.x, kLeast, blockIdx.x);
         int e = 0, seq = 0;
         bool ok = true;
-        auto open = [&]() { return mbar_wait_warp(&ring_empty[e % kRing], ((uint32_t)(e / kRing) & 1u) ^ 1u, st, 182, abort_flag); };
+        auto open = [&]() { return wait(&ring_empty[e % kRing], ((uint32_t)(e / kRing) & 1u) ^ 1u, st, 182, abort_flag); };
         auto push = [&](int kind) {        // an entry that is no page
             if (!(ok = open())) return;
             if (lane == 0) {
@@ -444,12 +528,12 @@ chunk_attn_kernel(Args a, AttnPlan plan)
             __syncwarp();
             ++e;
         };
-        long long item = mine.from < mine.to ? pieces.find(mine.from, lane) : 0;
+        int item = mine.from < mine.to ? pieces.find(mine.from, lane) : 0;
         const float qk = p.scale * kLog2e;
         for (; ok && mine.from < mine.to && item < pieces.n_items; ++item) {
             const long long start = pieces.start(item);
             if (start >= mine.to) break;
-            const int pages = pieces.pages(item), g = (int)(item % p.Hkv);
+            const int pages = pieces.pages(item), g = item % p.Hkv;
             const ChunkTile t = plan.tiles.tiles[item / p.Hkv];
             const int mt = tile_halves(t.rows * p.G);
             int c0, c1;
@@ -521,10 +605,10 @@ chunk_attn_kernel(Args a, AttnPlan plan)
                         x.halves = h;
                         x.first = h & ~begun;
                         x.a = qk * ks;
-                        const int ex = max((int)(__float_as_uint(vs) >> 23 & 255) - 127, -100);
+                        const int ex = min(max((int)(__float_as_uint(vs) >> 23 & 255) - 127, -100), 126);
                         x.lv = (float)ex;
-                        x.il = ldexpf(1.f, -ex);
-                        x.pv = ldexpf(vs, -ex);
+                        x.il = __uint_as_float((uint32_t)(127 - ex) << 23);
+                        x.pv = vs * x.il;
                         for (int w = 0; w < kMaskWords; ++w) x.mask[w] = mask[w];
                         mbar_arrive(&ring_full[e % kRing]);
                     }
@@ -539,7 +623,7 @@ chunk_attn_kernel(Args a, AttnPlan plan)
         if (ok) push(kExit);
     } else if (warp >= kCode0 && warp < kMma) {
         // ------------------------------------------------ codes to bf16
-        const int tid = threadIdx.x - 32 * kCode0;
+        const Place<D> place(threadIdx.x - 32 * kCode0);
         uint4 k[D / 16], v[D / 16];
         int e = 0, n = 0;
         // the next page's codes' place and item; false at the end
@@ -559,7 +643,8 @@ chunk_attn_kernel(Args a, AttnPlan plan)
         };
         auto load = [&](uint4 (&u)[D / 16], const uint8_t *codes) {
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j) u[j] = __ldg(reinterpret_cast<const uint4 *>(codes) + tid + 128 * j);
+            for (int j = 0; j < D / 16; ++j)
+                u[j] = __ldg(reinterpret_cast<const uint4 *>(codes + (place.token + j * Place<D>::kStep) * D + place.feature));
         };
         long long tile = 0, tile2 = 0;
         int item = 0, item2 = 0;
@@ -569,15 +654,18 @@ chunk_attn_kernel(Args a, AttnPlan plan)
             const int s = n % kStages;
             const uint32_t free = ((uint32_t)(n / kStages) & 1u) ^ 1u;
             load(v, a.v8 + tile);
-            if (!mbar_wait_warp(&k_empty[s], free, st, 183, abort_flag)) break;
-            lay_down<D, false>(sm + S::OFF_K + s * S::TILE, k, tid);
+            if (!wait(&k_empty[s], free, st, 183, abort_flag)) break;
+            lay_down<D, false>(sm + S::OFF_K + s * S::TILE, k, place);
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&k_full[s]);
             const bool more = next(tile2, item2);
             if (more) load(k, a.k8 + tile2);
-            if (!mbar_wait_warp(&v_empty[s], free, st, 184, abort_flag)) break;
-            if (lay_down<D, true>(sm + S::OFF_V + s * S::TILE, v, tid)) nan_item[item % kRing] = item;
+            if (!wait(&v_empty[s], free, st, 184, abort_flag)) break;
+            if (lay_down<D, true>(sm + S::OFF_V + s * S::TILE, v, place)) {
+                mend<D>(sm + S::OFF_V + s * S::TILE, a.v8 + tile, place);
+                nan_item[item % kRing] = item;
+            }
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&v_full[s]);
@@ -585,82 +673,72 @@ chunk_attn_kernel(Args a, AttnPlan plan)
             tile = tile2;
             item = item2;
         }
-    } else if (warp == kMma) {
-        // ------------------------------------------------ MMA issuer: a half's scores, then the half before's P V
-        constexpr uint32_t I_S = idesc_bf16(128, kPage), I_O = idesc_bf16(128, D) | kBMajorMN;
-        const uint64_t dQ = sdesc_k128(smem_u32(sm)), dK = sdesc_k128(smem_u32(sm + S::OFF_K));
+    } else if (warp == kMma || warp == kMma + 1) {
+        // ------------------------------------------------ MMA issuers, one for each half: S, then P V
+        constexpr uint32_t I_S = idesc_f16(128, kPage), I_O = idesc_bf16(128, D) | kBMajorMN;
+        const int h = warp - kMma;
+        const uint32_t tS = tmem + h * 128, tO = tmem + 256 + h * D;
+        const uint64_t dQ = sdesc_k128(smem_u32(sm) + h * S::TILE), dK = sdesc_k128(smem_u32(sm + S::OFF_K));
         const uint64_t dV = sdesc_sw128(smem_u32(sm + S::OFF_V), kSub, 1024);
-        int n = 0, e = 0;
-        uint32_t done[2] = {0, 0};             // products with P of each half
-        struct {
-            int half, page;
-            bool first, last;                  // of the half's pages; half of the page
-        } due{-1, 0, false, false};
-        bool ok = true;
-        auto issue_o = [&]() {
-            const int h = due.half, s = due.page % kStages;
-            due.half = -1;
-            ok = mbar_wait_warp(&p_full[h], done[h]++ & 1u, st, 185, abort_flag) &&
-                 mbar_wait_warp(&v_full[s], (uint32_t)(due.page / kStages) & 1u, st, 186, abort_flag);
-            if (!ok) return;
-            fence_after_sync();
-            if (elect_one()) {
-#pragma unroll
-                for (int ks = 0; ks < kPage / 16; ++ks)
-                    mma_bf16_ts(tmem + 256 + h * D, tmem + h * 128 + ks * 8, desc_adv(dV, s * S::TILE + ks * 2048), I_O, !due.first || ks > 0);
-                if (due.last) mma_commit(&v_empty[s]);
-            }
-            __syncwarp();
-        };
-        while (ok) {
-            if (!(ok = wait_entry(e))) break;
+        uint32_t n = 0, ops = 0;
+        int begun = -1;                        // the item whose queries are there
+        for (int e = 0;; ++e) {
+            if (!wait_entry(e)) break;
             const Entry &x = ring[e % kRing];
-            const int kind = x.kind, item = x.item, halves = x.halves, first = x.first;
+            const int kind = x.kind, item = x.item;
+            const bool mine = x.halves >> h & 1, first = x.first >> h & 1;
             done_entry(e);
-            ++e;
             if (kind == kExit) break;
             if (kind == kEndEntry) {
-                if (due.half >= 0) issue_o();
-                if (!ok) break;
-                if (elect_one()) {
-                    mma_commit(&o_full[0]);
-                    mma_commit(&o_full[1]);
-                }
+                // an item without a page for this half ends after it has begun there too: never two ends ahead
+                if (begun != item && !wait(&q_full[h], (uint32_t)item & 1u, st, 188, abort_flag)) break;
+                if (elect_one()) mma_commit(&o_full[h]);
                 __syncwarp();
                 continue;
             }
-            const int s = n % kStages;
-            if (!(ok = mbar_wait_warp(&k_full[s], (uint32_t)(n / kStages) & 1u, st, 187, abort_flag))) break;
-            for (int h = 0; ok && h < 2; ++h) {
-                if (!(halves >> h & 1)) continue;
-                if (first >> h & 1 && !(ok = mbar_wait_warp(&q_full[h], (uint32_t)item & 1u, st, 188, abort_flag))) break;
-                if (due.half == h) issue_o();          // its P is where the scores go
-                if (!ok) break;
-                fence_after_sync();
-                if (elect_one()) {
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t off = (ks >> 2) * kSub + (ks & 3) * 32;
-                        mma_bf16(tmem + h * 128, desc_adv(dQ, h * S::TILE + off), desc_adv(dK, s * S::TILE + off), I_S, ks > 0);
-                    }
-                    mma_commit(&s_full[h]);
-                    if (halves >> (h + 1) == 0) mma_commit(&k_empty[s]);
-                }
-                __syncwarp();
-                if (due.half >= 0) issue_o();
-                due = {h, n, (first >> h & 1) != 0, halves >> (h + 1) == 0};
-            }
+            const uint32_t s = n % kStages, phase = n / kStages & 1u;
             ++n;
+            if (!wait(&k_full[s], phase, st, 187, abort_flag)) break;
+            if (!mine) {                       // the other half's alone
+                if (lane == 0) mbar_arrive(&k_empty[s]);
+                if (!wait(&v_full[s], phase, st, 186, abort_flag)) break;
+                if (lane == 0) mbar_arrive(&v_empty[s]);
+                continue;
+            }
+            if (begun != item && !wait(&q_full[h], (uint32_t)item & 1u, st, 188, abort_flag)) break;
+            begun = item;
+            fence_after_sync();
+            if (elect_one()) {
+                const uint64_t k = desc_adv(dK, s * S::TILE);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t off = (ks >> 2) * kSub + (ks & 3) * 32;
+                    mma_bf16(tS, desc_adv(dQ, off), desc_adv(k, off), I_S, ks > 0);
+                }
+                mma_commit(&s_full[h]);
+                mma_commit(&k_empty[s]);
+            }
+            __syncwarp();
+            if (!wait(&v_full[s], phase, st, 186, abort_flag) || !wait(&p_full[h], ops++ & 1u, st, 185, abort_flag)) break;
+            fence_after_sync();
+            if (elect_one()) {
+                const uint64_t v = desc_adv(dV, s * S::TILE);
+#pragma unroll
+                for (int ks = 0; ks < kPage / 16; ++ks) mma_bf16_ts(tO, tS + ks * 8, desc_adv(v, ks * 2048), I_O, !first || ks > 0);
+                mma_commit(&v_empty[s]);
+            }
+            __syncwarp();
         }
         if (elect_one()) mma_commit(drained);
         __syncwarp();
-        mbar_wait(drained, 0, nullptr, 0, nullptr);    // every product has ended
+        mbar_wait(drained, 0, nullptr, 0, nullptr);    // every product of both has ended
     } else if (warp < kSoftWarps) {
         // ------------------------------------------------ softmax: a (row, head) pair to a thread
         const int half = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lanes + half * 128, tO = tmem + lanes + 256 + half * D;
         float m = -INFINITY, z = 0.f;          // reference (log2), sum
+        float q_down = 1.f;                    // what the queries were not multiplied by
         int cur = -1, pos = -1, token = 0, ops = 0, splits = 0;
         bool used = false;
         Item it{};
@@ -669,29 +747,51 @@ chunk_attn_kernel(Args a, AttnPlan plan)
             cur = item;
             it = items[item % kRing];
             const int rho = it.split ? r : half * 128 + r, pairs = it.rows * p.G;
-            token = rho / p.G;
+            token = rho >> a.shift;
             pos = rho < pairs ? a.row_pos[it.row + token] : -1;
             if ((long long)pos >= (long long)p.max_blocks * kPage) pos = -1;
             m = -INFINITY;
             z = 0.f;
             used = false;
-            // this warp's 32 pairs of queries, features in the order of the codes'
+            // this warp's 32 pairs of queries, as fp16: each times the power of two that brings its largest feature to 2^14 or above
             constexpr int CPR = D / 8, RPI = 32 / CPR, N = 32 / RPI;
-            uint4 u[N];
+            constexpr int ROUND = N < 8 ? N : 8;
             const int c = lane % CPR;
+#pragma unroll 1
+            for (int j0 = 0; j0 < N; j0 += ROUND) {
+                uint4 u[ROUND];
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const int rr = (warp & 3) * 32 + j * RPI + lane / CPR, rh = it.split ? rr : half * 128 + rr;
-                u[j] = make_uint4(0, 0, 0, 0);
-                if (rh < pairs)
-                    u[j] = __ldg(reinterpret_cast<const uint4 *>(a.q + ((long long)(it.row + rh / p.G) * p.Hq + it.group * p.G + rh % p.G) * D) + c);
-            }
+                for (int j = 0; j < ROUND; ++j) {
+                    const int rr = (warp & 3) * 32 + (j0 + j) * RPI + lane / CPR, rh = it.split ? rr : half * 128 + rr;
+                    u[j] = make_uint4(0, 0, 0, 0);
+                    if (rh < pairs)
+                        u[j] = __ldg(reinterpret_cast<const uint4 *>(a.q + ((long long)(it.row + (rh >> a.shift)) * p.Hq + it.group * p.G + (rh & (p.G - 1))) * D) + c);
+                }
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const int rr = (warp & 3) * 32 + j * RPI + lane / CPR;
-                const uint4 y = make_uint4(__byte_perm(u[j].x, u[j].y, 0x5410), __byte_perm(u[j].x, u[j].y, 0x7632),
-                                           __byte_perm(u[j].z, u[j].w, 0x5410), __byte_perm(u[j].z, u[j].w, 0x7632));
-                *reinterpret_cast<uint4 *>(sm + half * S::TILE + (c >> 3) * kSub + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = y;
+                for (int j = 0; j < ROUND; ++j) {
+                    const int rr = (warp & 3) * 32 + (j0 + j) * RPI + lane / CPR;
+                    uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
+                    float2 f[4];
+                    float top = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        f[k] = unpack_bf16(w[k]);
+                        top = fmaxf(top, fmaxf(fabsf(f[k].x), fabsf(f[k].y)));
+                    }
+#pragma unroll
+                    for (int o = 1; o < CPR; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const int ex = top > 0.f ? min(14 - ((int)(__float_as_uint(top) >> 23) - 127), 126) : 0;   // 126 falls short below 2^-112
+                    const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const __half2 h = __floats2half2_rn(f[k].x * up, f[k].y * up);
+                        w[k] = *reinterpret_cast<const uint32_t *>(&h);
+                    }
+                    *reinterpret_cast<uint4 *>(sm + half * S::TILE + (c >> 3) * kSub + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+                    const float of_row = __shfl_sync(0xffffffffu, down, (lane % RPI) * CPR);
+                    if (lane / RPI == j0 + j) q_down = of_row;
+                }
             }
             fence_proxy_async();
             __syncwarp();
@@ -700,111 +800,105 @@ chunk_attn_kernel(Args a, AttnPlan plan)
 
         // Scores to probabilities, in their place.
         auto page = [&](int lim, bool first, float fa, float lv, float il, float pv) {
-            if (!mbar_wait_warp(&s_full[half], (uint32_t)ops++ & 1u, st, 189, abort_flag)) return false;
+            if (!wait(&s_full[half], (uint32_t)ops++ & 1u, st, 189, abort_flag)) return false;
             fence_after_sync();
-            const bool all = __all_sync(0xffffffffu, lim >= kPage - 1);
+            used = true;
             if (!__any_sync(0xffffffffu, lim >= 0)) {
                 const uint32_t none[16] = {};
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_st16(tS + c * 16, none);
+#pragma unroll 1
+                for (int c = 0; c < 64; c += 16) tmem_st16(tS + c, none);
             } else {
-                float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                // two passes over the scores, 32 at a time, the next ones on their way from TMEM meanwhile; rolled up, so that
+                // the code stays small
+                const bool all = __all_sync(0xffffffffu, lim >= kPage - 1);
+                uint32_t x[32], y[32];
+                float mq[2] = {-INFINITY, -INFINITY};
+                auto top = [&](uint32_t (&v)[32], int c) {
+                    if (!all) {                    // masked scores: minus infinity from here on
 #pragma unroll
-                for (int c64 = 0; c64 < 2; ++c64) {
-                    uint32_t s0[32], s1[32];
-                    tmem_ld32_nowait(tS + c64 * 64, s0);
-                    tmem_ld32_nowait(tS + c64 * 64 + 32, s1);
-                    tmem_wait32(s0);
-                    tmem_wait32(s1);
-                    if (all) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) mq[j & 3] = fmaxf(mq[j & 3], fmaxf(__uint_as_float(s0[j]), __uint_as_float(s1[j])));
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            if (c64 * 64 + j <= lim) mq[j & 3] = fmaxf(mq[j & 3], __uint_as_float(s0[j]));
-                            if (c64 * 64 + 32 + j <= lim) mq[j & 3] = fmaxf(mq[j & 3], __uint_as_float(s1[j]));
-                        }
+                        for (int j = 0; j < 32; ++j) v[j] = c + j <= lim ? v[j] : 0xFF800000u;
+                        tmem_st16(tS + c, v);
+                        tmem_st16(tS + c + 16, v + 16);
                     }
-                }
-                const float t = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * fa + lv;
-                const bool up = t > m + kLag;
-                const float keep = up ? ex2(m - t) : 1.f;
-                if (!first && __any_sync(0xffffffffu, up && m != -INFINITY)) {
 #pragma unroll
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32_nowait(tO + c, o);
-                        tmem_wait32(o);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
-                        tmem_st16(tO + c, o);
-                        tmem_st16(tO + c + 16, o + 16);
-                    }
-                }
-                z *= keep;
-                m = up ? t : m;
-                const float c0 = m == -INFINITY ? lv : lv - m;
-                float zp[4] = {0.f, 0.f, 0.f, 0.f};
-                auto powers = [&](auto plain_tag) {
-                    constexpr bool kPlain = decltype(plain_tag)::value;    // no token is masked, no factor
-#pragma unroll
-                    for (int c64 = 0; c64 < 2; ++c64) {
-                        uint32_t sr[2][32];
-                        tmem_ld32_nowait(tS + c64 * 64, sr[0]);
-                        tmem_ld32_nowait(tS + c64 * 64 + 32, sr[1]);
-                        tmem_wait32(sr[0]);
-                        tmem_wait32(sr[1]);
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            uint32_t pk[16];
-#pragma unroll
-                            for (int j = 0; j < 32; j += 2) {
-                                const int at = c64 * 64 + x * 32 + j;
-                                float e0 = ex2(fmaf(__uint_as_float(sr[x][j]), fa, c0)), e1 = ex2(fmaf(__uint_as_float(sr[x][j + 1]), fa, c0));
-                                if constexpr (!kPlain) {
-                                    e0 = at <= lim ? e0 : 0.f;
-                                    e1 = at + 1 <= lim ? e1 : 0.f;
-                                }
-                                zp[(j >> 1) & 3] += e0 + e1;
-                                pk[j / 2] = kPlain ? pack_bf16(e0, e1) : pack_bf16(at <= lim ? e0 * pv : 0.f, at + 1 <= lim ? e1 * pv : 0.f);
-                            }
-                            tmem_st16(tS + c64 * 32 + x * 16, pk);
-                        }
-                    }
+                    for (int j = 0; j < 32; j += 2) mq[j >> 1 & 1] = fmaxf(mq[j >> 1 & 1], fmaxf(__uint_as_float(v[j]), __uint_as_float(v[j + 1])));
                 };
-                if (all && pv == 1.f) powers(std::true_type{});
-                else powers(std::false_type{});
-                z += ((zp[0] + zp[1]) + (zp[2] + zp[3])) * il;
+                tmem_ld32_nowait(tS, x);
+#pragma unroll 1
+                for (int c = 0; c < kPage; c += 64) {
+                    tmem_wait32(x);
+                    tmem_ld32_nowait(tS + c + 32, y);
+                    top(x, c);
+                    tmem_wait32(y);
+                    if (c + 64 < kPage) tmem_ld32_nowait(tS + c + 64, x);
+                    top(y, c + 32);
+                }
+                if (!all) tmem_wait_st();
+                tmem_ld32_nowait(tS, x);
+                const float t = fmaxf(mq[0], mq[1]) * fa + lv;
+                const bool up = t > m + kLag;
+                if (__any_sync(0xffffffffu, up)) {
+                    const float keep = up ? ex2(m - t) : 1.f;
+                    if (!first) {
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16_nowait(tO + c, o);
+                            tmem_wait16(o);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
+                            tmem_st16(tO + c, o);
+                        }
+                    }
+                    z *= keep;
+                    m = up ? t : m;
+                }
+                const float c0 = m == -INFINITY ? lv : lv - m;
+                const uint64_t fa2 = pair(fa, fa), c02 = pair(c0, c0);
+                uint64_t zp[2] = {0, 0};
+                auto powers = [&](const uint32_t (&v)[32], int c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        float e0, e1;
+                        split(fma2(pair(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), fa2, c02), e0, e1);
+                        e0 = ex2(e0);
+                        e1 = ex2(e1);
+                        zp[j >> 1 & 1] = add2(zp[j >> 1 & 1], pair(e0, e1));
+                        pk[j / 2] = pack_bf16(e0, e1);
+                    }
+                    if (pv != 1.f) {               // exact: a power of two
+                        const __nv_bfloat162 pv2 = __float2bfloat162_rn(pv);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const __nv_bfloat162 q = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&pk[j]), pv2);
+                            pk[j] = *reinterpret_cast<const uint32_t *>(&q);
+                        }
+                    }
+                    tmem_st16(tS + c / 2, pk);
+                };
+#pragma unroll 1
+                for (int c = 0; c < kPage; c += 64) {
+                    tmem_wait32(x);
+                    tmem_ld32_nowait(tS + c + 32, y);
+                    powers(x, c);                  // P takes the columns from half of the scores' on: behind what was read
+                    tmem_wait32(y);
+                    if (c + 64 < kPage) tmem_ld32_nowait(tS + c + 64, x);
+                    powers(y, c + 32);
+                }
+                float z0, z1;
+                split(add2(zp[0], zp[1]), z0, z1);
+                z += (z0 + z1) * il;
             }
             tmem_wait_st();
             fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[half]);
-            used = true;
             return true;
         };
 
-        // The features of a visible token's V codes that are NaN.
-        auto spoiled = [&](uint32_t (&bad)[D / 32]) {
-            for (int w = 0; w < D / 32; ++w) bad[w] = 0;
-            for (int c = it.c0; c < it.c1; ++c) {
-                const int block = a.sel ? plan.blocks[it.at + c] : c, page = a.block_table[(long long)it.req * p.max_blocks + block];
-                if ((unsigned)page >= (unsigned)p.n_pages) continue;
-                if (a.sel && !(plan.masks[(it.at + c) * a.words + (token >> 5)] >> (token & 31) & 1)) continue;
-                const uint4 *row = reinterpret_cast<const uint4 *>(a.v8 + ((long long)page * p.Hkv + it.group) * kPage * D);
-                for (int j = 0; j < kPage && block * kPage + j <= pos; ++j)
-                    for (int w = 0; w < D / 16; ++w) {
-                        const uint4 u = row[j * (D / 16) + w];
-                        const uint32_t x[4] = {nan_codes(u.x), nan_codes(u.y), nan_codes(u.z), nan_codes(u.w)};
-                        for (int k = 0; k < 4; ++k)
-                            bad[w / 2] |= ((x[k] >> 7 & 1) | (x[k] >> 14 & 2) | (x[k] >> 21 & 4) | (x[k] >> 28 & 8)) << ((w & 1) * 16 + k * 4);
-                    }
-            }
-        };
-
         auto finish = [&](int item) {
-            if (!mbar_wait_warp(&o_full[half], (uint32_t)item & 1u, st, 190, abort_flag)) return false;
+            if (!wait(&o_full[half], (uint32_t)item & 1u, st, 190, abort_flag)) return false;
             fence_after_sync();
             const int rho = it.split ? r : half * 128 + r;
             const bool mine = rho < it.rows * p.G && pos >= 0;
@@ -815,9 +909,9 @@ chunk_attn_kernel(Args a, AttnPlan plan)
                     state[r] = make_float2(used ? m : -INFINITY, used ? z : 0.f);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(b_ready);
-                    return mbar_wait_warp(b_read, turn, st, 191, abort_flag);   // A has read this half's sums
+                    return wait(b_read, turn, st, 191, abort_flag);   // A has read this half's sums
                 }
-                if (!mbar_wait_warp(b_ready, turn, st, 192, abort_flag)) return false;
+                if (!wait(b_ready, turn, st, 192, abort_flag)) return false;
                 const float2 b = state[r];
                 const bool none = b.y == 0.f;                 // nothing visible on B's pages
                 const float top = none ? m : fmaxf(m, b.x);
@@ -828,53 +922,44 @@ chunk_attn_kernel(Args a, AttnPlan plan)
             }
             const bool any_a = __any_sync(0xffffffffu, wa != 0.f), any_b = __any_sync(0xffffffffu, wb != 0.f);
             const float inv = it.part >= 0 ? 1.f : z == 0.f ? 0.f : 1.f / z;
-            uint32_t bad[D / 32];
-            const bool look = nan_item[item % kRing] == item;
-            if (look && mine) spoiled(bad);
-            __syncwarp();
-            const long long row = (long long)(it.row + token) * p.Hq + it.group * p.G + rho % p.G;
-            float *part = plan.part + ((long long)it.part * kTileRows + rho) * D;
+            const long long row = (long long)(it.row + token) * p.Hq + it.group * p.G + (rho & (p.G - 1));
+            float *part = it.part >= 0 ? plan.part + ((long long)it.part * kTileRows + rho) * D : nullptr;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+                float x[16];
 #pragma unroll
-            for (int c = 0; c < D; c += 32) {
-                float x[32];
-#pragma unroll
-                for (int j = 0; j < 32; ++j) x[j] = 0.f;
-                uint32_t o[32];
+                for (int j = 0; j < 16; ++j) x[j] = 0.f;
+                uint32_t o[16];
                 if (any_a) {
-                    tmem_ld32_nowait(tO + c, o);
-                    tmem_wait32(o);
+                    tmem_ld16_nowait(tO + c, o);
+                    tmem_wait16(o);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) x[j] = wa == 0.f ? 0.f : __uint_as_float(o[j]) * wa;
+                    for (int j = 0; j < 16; ++j) x[j] = wa == 0.f ? 0.f : __uint_as_float(o[j]) * wa;
                 }
                 if (any_b) {
-                    tmem_ld32_nowait(tO + D + c, o);
-                    tmem_wait32(o);
+                    tmem_ld16_nowait(tO + D + c, o);
+                    tmem_wait16(o);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) x[j] += wb == 0.f ? 0.f : __uint_as_float(o[j]) * wb;
+                    for (int j = 0; j < 16; ++j) x[j] += wb == 0.f ? 0.f : __uint_as_float(o[j]) * wb;
                 }
-                if (look && mine) {
+                if (mine && part) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const int f = (j & ~3) | (j & 3) >> 1 | (j & 1) << 1;       // column j is feature f
-                        if (bad[c / 32] >> f & 1) x[j] = __uint_as_float(0x7FC00000u);
-                    }
-                }
-                if (mine && it.part >= 0) {
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4 *>(part + c + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+                    for (int j = 0; j < 16; j += 4) *reinterpret_cast<float4 *>(part + c + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
                 } else if (mine) {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8)
+                    for (int j = 0; j < 16; j += 8)
                         *reinterpret_cast<uint4 *>(a.o + row * D + c + j) =
-                            make_uint4(pack_bf16(x[j] * inv, x[j + 2] * inv), pack_bf16(x[j + 1] * inv, x[j + 3] * inv),
-                                       pack_bf16(x[j + 4] * inv, x[j + 6] * inv), pack_bf16(x[j + 5] * inv, x[j + 7] * inv));
+                            make_uint4(pack_bf16(x[j] * inv, x[j + 1] * inv), pack_bf16(x[j + 2] * inv, x[j + 3] * inv),
+                                       pack_bf16(x[j + 4] * inv, x[j + 5] * inv), pack_bf16(x[j + 6] * inv, x[j + 7] * inv));
                 }
                 __syncwarp();
             }
             if (mine) {
-                if (it.part >= 0) plan.stats(a.ctas, D)[(long long)it.part * kTileRows + rho] = make_float2(z == 0.f ? -INFINITY : m, z);
+                if (part) plan.stats(a.ctas, D)[(long long)it.part * kTileRows + rho] = make_float2(z == 0.f ? -INFINITY : m, z);
                 else a.lse[row] = z == 0.f ? -INFINITY : (m + log2f(z)) * kLn2;
+                if (nan_item[item % kRing] == item) spoil<D>(a, plan, it, pos, token, part, a.o + row * D);
             }
+            __syncwarp();
             if (it.split) {
                 fence_before_sync();
                 __syncwarp();
@@ -893,7 +978,7 @@ chunk_attn_kernel(Args a, AttnPlan plan)
                 const bool seen = x.mask[token >> 5] >> (token & 31) & 1;
                 const int lim = seen ? min(pos - x.block * kPage, kPage - 1) : -1;
                 const bool first = x.first >> half & 1;
-                const float fa = x.a, lv = x.lv, il = x.il, pv = x.pv;
+                const float fa = x.a * q_down, lv = x.lv, il = x.il, pv = x.pv;
                 done_entry(e);
                 if (!page(lim, first, fa, lv, il, pv)) break;
             } else {
@@ -922,10 +1007,11 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(Args a, AttnPlan plan)
     const Pieces pieces(plan, a);
     const ChunkShare mine(pieces.total, a.ctas, kLeast, cta);
     if (mine.from >= mine.to) return;
-    const long long item = pieces.find(mine.from, lane), start = pieces.start(item);
+    const int item = pieces.find(mine.from, lane);
+    const long long start = pieces.start(item);
     if (start >= mine.from) return;
     const ChunkTile t = plan.tiles.tiles[item / p.Hkv];
-    const int pages = pieces.pages(item), mt = tile_halves(t.rows * p.G), g = (int)(item % p.Hkv);
+    const int pages = pieces.pages(item), mt = tile_halves(t.rows * p.G), g = item % p.Hkv;
     int c0, c1;
     cut(start, pages, mt, mine.from, mine.to, c0, c1);
     if (c0 == 0 || c0 >= c1 || c1 != pages) return;
@@ -959,7 +1045,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(Args a, AttnPlan plan)
     const long long row = (long long)(t.row + rho / p.G) * p.Hq + g * p.G + rho % p.G;
     const float inv = z == 0.f ? 0.f : 1.f / z;
     if (lane * 4 < D)
-        *reinterpret_cast<uint2 *>(a.o + row * D + lane * 4) = make_uint2(pack_bf16(x[0] * inv, x[2] * inv), pack_bf16(x[1] * inv, x[3] * inv));
+        *reinterpret_cast<uint2 *>(a.o + row * D + lane * 4) = make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
     if (lane == 0) a.lse[row] = z == 0.f ? -INFINITY : (m + log2f(z)) * kLn2;
 }
 
@@ -985,7 +1071,7 @@ cudaError_t launch_paged_chunk_attn(const PagedProblem &p, const bf16 *q, const 
     cudaError_t e = launch_chunk_plan(p, q_starts, row_pos, tokens, p.G, scratch, st, s);
     if (e != cudaSuccess) return e;
     const AttnPlan plan = attn_plan(p, scratch, sel != nullptr);
-    const Args a{p, q, k8, v8, k_scale, v_scale, block_table, row_pos, sel, o, lse, tokens, mask_words(p), p.num_sms, st};
+    const Args a{p, q, k8, v8, k_scale, v_scale, block_table, row_pos, sel, o, lse, tokens, mask_words(p), p.num_sms, p.G == 8 ? 3 : p.G / 2, st};
     if (sel) {
         const long long items = chunk_tiles(p, tokens) * p.Hkv, ctas = std::min((items + kListWarps - 1) / kListWarps, 8LL * p.num_sms);
         if ((e = launch_chained("paged_chunk_list_kernel", chunk_list_kernel, dim3((unsigned)ctas), 32 * kListWarps, 0, s, a, plan)) != cudaSuccess) return e;

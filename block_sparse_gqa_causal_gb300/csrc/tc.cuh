@@ -155,6 +155,9 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N)
            | ((uint32_t)(M >> 4) << 24);   // M / 16
 }
 
+// The same with fp16 A/B.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) { return idesc_bf16(M, N) & ~((1u << 7) | (1u << 10)); }
+
 // D[tmem] (+)= A[smem] * B[smem]^T, issued by one thread.
 MSA_DEV void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, bool accumulate)
 {

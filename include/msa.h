@@ -567,8 +567,9 @@ msa_status msa_paged_copy(const msa_paged_shape *shape, const int32_t *moves, in
  * A row_pos past 128 * max_blocks - 1, and starts that do not ascend, are left
  * out and recorded in the status word.  Scores are made for any Hkv.
  *
- * Attention: queries enter the products as they are, probabilities with 8
- * significant bits, however small; sums are fp32.  With a selection, a tile
+ * Attention: queries enter the products with 8 significant bits, features
+ * below 2^-31 of their row's and head's largest off by 2^-39 of it at most;
+ * probabilities with 8 significant bits, however small; sums are fp32.  With a selection, a tile
  * reads the blocks that any of its rows selected.  Entries that msa_paged_attn
  * leaves out and records are left out and recorded here too.  Deterministic.
  * A NaN in a cached row reaches those rows only that see it.
