@@ -462,8 +462,8 @@ chunk_attn_kernel(Args a, AttnPlan plan)
     uint64_t *ring_full = bars, *ring_empty = bars + kRing, *k_full = bars + 2 * kRing, *k_empty = k_full + kStages;
     uint64_t *v_full = k_empty + kStages, *v_empty = v_full + kStages, *q_full = v_empty + kStages;
     uint64_t *s_full = q_full + 2, *p_full = s_full + 2, *o_full = p_full + 2, *drained = o_full + 2;
-    uint64_t *b_ready = drained + 1, *b_read = drained + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 3);
+    uint64_t *b_ready = drained + 1, *b_read = drained + 2, *turn = drained + 3;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drained + 5);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *nan_item = reinterpret_cast<volatile int *>(tmem_slot + 2);     // by item: its number if a V code of it is NaN
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -487,6 +487,7 @@ chunk_attn_kernel(Args a, AttnPlan plan)
             mbar_init(&s_full[h], 1);
             mbar_init(&p_full[h], 4);
             mbar_init(&o_full[h], 1);
+            mbar_init(&turn[h], 1);
         }
         mbar_init(drained, 2);
         mbar_init(b_ready, 4);
@@ -674,7 +675,7 @@ chunk_attn_kernel(Args a, AttnPlan plan)
             item = item2;
         }
     } else if (warp == kMma || warp == kMma + 1) {
-        // ------------------------------------------------ MMA issuers, one for each half: S, then P V
+        // ------------------------------------------------ MMA issuers, one for each half: a page's P V, then the next one's S
         constexpr uint32_t I_S = idesc_f16(128, kPage), I_O = idesc_bf16(128, D) | kBMajorMN;
         const int h = warp - kMma;
         const uint32_t tS = tmem + h * 128, tO = tmem + 256 + h * D;
@@ -682,52 +683,75 @@ chunk_attn_kernel(Args a, AttnPlan plan)
         const uint64_t dV = sdesc_sw128(smem_u32(sm + S::OFF_V), kSub, 1024);
         uint32_t n = 0, ops = 0;
         int begun = -1;                        // the item whose queries are there
-        for (int e = 0;; ++e) {
+        int due = -1, left = -1;               // the page whose P V is due; the one whose V this half does not read
+        bool due_first = false;
+        bool ok = true;
+        // the product due, once its P is there
+        auto p_there = [&]() {
+            return wait(&v_full[due % kStages], (uint32_t)(due / kStages) & 1u, st, 186, abort_flag) &&
+                   wait(&p_full[h], ops++ & 1u, st, 185, abort_flag);
+        };
+        auto issue_o = [&]() {
+            const uint64_t v = desc_adv(dV, due % kStages * S::TILE);
+#pragma unroll
+            for (int ks = 0; ks < kPage / 16; ++ks) mma_bf16_ts(tO, tS + ks * 8, desc_adv(v, ks * 2048), I_O, !due_first || ks > 0);
+            mma_commit(&v_empty[due % kStages]);
+        };
+        for (int e = 0; ok; ++e) {
             if (!wait_entry(e)) break;
             const Entry &x = ring[e % kRing];
             const int kind = x.kind, item = x.item;
-            const bool mine = x.halves >> h & 1, first = x.first >> h & 1;
+            const bool mine = kind == kPageEntry && (x.halves >> h & 1), first = x.first >> h & 1;
             done_entry(e);
             if (kind == kExit) break;
-            if (kind == kEndEntry) {
-                // an item without a page for this half ends after it has begun there too: never two ends ahead
-                if (begun != item && !wait(&q_full[h], (uint32_t)item & 1u, st, 188, abort_flag)) break;
-                if (elect_one()) mma_commit(&o_full[h]);
-                __syncwarp();
-                continue;
+            const uint32_t s = n % kStages;
+            // what this entry's products wait for
+            if (kind == kPageEntry) {
+                ok = wait(&k_full[s], n / kStages & 1u, st, 187, abort_flag);
+                // (V of the page before was laid down before this K)
+                if (left >= 0 && lane == 0) mbar_arrive(&v_empty[left % kStages]);
+            } else if (left >= 0) {
+                ok = wait(&v_full[left % kStages], (uint32_t)(left / kStages) & 1u, st, 186, abort_flag);
+                if (ok && lane == 0) mbar_arrive(&v_empty[left % kStages]);
             }
-            const uint32_t s = n % kStages, phase = n / kStages & 1u;
-            ++n;
-            if (!wait(&k_full[s], phase, st, 187, abort_flag)) break;
-            if (!mine) {                       // the other half's alone
-                if (lane == 0) mbar_arrive(&k_empty[s]);
-                if (!wait(&v_full[s], phase, st, 186, abort_flag)) break;
-                if (lane == 0) mbar_arrive(&v_empty[s]);
-                continue;
+            left = -1;
+            if (!ok) break;
+            if ((mine || kind == kEndEntry) && begun != item) {        // an item ends only after it has begun: never two ends ahead
+                if (!(ok = wait(&q_full[h], (uint32_t)item & 1u, st, 188, abort_flag))) break;
+                begun = item;
             }
-            if (begun != item && !wait(&q_full[h], (uint32_t)item & 1u, st, 188, abort_flag)) break;
-            begun = item;
+            const bool o = due >= 0;           // whosever this page is: V's place is waited for
+            if (o && !(ok = p_there())) break;
+            // the halves take turns
+            if (!(ok = wait(&turn[h], ((uint32_t)e & 1u) ^ (h == 0), st, 193, abort_flag))) break;
             fence_after_sync();
             if (elect_one()) {
-                const uint64_t k = desc_adv(dK, s * S::TILE);
+                if (o) issue_o();
+                if (mine) {
+                    const uint64_t k = desc_adv(dK, s * S::TILE);
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t off = (ks >> 2) * kSub + (ks & 3) * 32;
-                    mma_bf16(tS, desc_adv(dQ, off), desc_adv(k, off), I_S, ks > 0);
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t off = (ks >> 2) * kSub + (ks & 3) * 32;
+                        mma_bf16(tS, desc_adv(dQ, off), desc_adv(k, off), I_S, ks > 0);
+                    }
+                    mma_commit(&s_full[h]);
+                    mma_commit(&k_empty[s]);
+                } else if (kind == kPageEntry) {
+                    mbar_arrive(&k_empty[s]);
+                } else {
+                    mma_commit(&o_full[h]);
                 }
-                mma_commit(&s_full[h]);
-                mma_commit(&k_empty[s]);
+                mbar_arrive(&turn[h ^ 1]);
             }
             __syncwarp();
-            if (!wait(&v_full[s], phase, st, 186, abort_flag) || !wait(&p_full[h], ops++ & 1u, st, 185, abort_flag)) break;
-            fence_after_sync();
-            if (elect_one()) {
-                const uint64_t v = desc_adv(dV, s * S::TILE);
-#pragma unroll
-                for (int ks = 0; ks < kPage / 16; ++ks) mma_bf16_ts(tO, tS + ks * 8, desc_adv(v, ks * 2048), I_O, !first || ks > 0);
-                mma_commit(&v_empty[s]);
+            if (o) due = -1;
+            if (mine) {
+                due = (int)n;
+                due_first = first;
+            } else if (kind == kPageEntry) {
+                left = (int)n;
             }
-            __syncwarp();
+            n += kind == kPageEntry;
         }
         if (elect_one()) mma_commit(drained);
         __syncwarp();

@@ -387,3 +387,25 @@ def test_prompts_shared_and_served_in_chunks(api, graph):
     tb, ln = table.cpu().numpy(), lens.cpu().numpy()
     held = {int(tb[r, b]) for r in range(R) for b in range(-(-ln[r] // PAGE))}
     assert len(held) == used                         # no page is lost
+
+
+@pytest.mark.parametrize("G,Hkv", [(8, 2), (4, 1), (1, 3)])
+@pytest.mark.parametrize("stretch", [1, 3, 9])
+def test_chunk_blocks_that_one_half_of_a_tile_selects(api, G, Hkv, stretch):
+    """Runs of blocks that only the first, or only the last, rows of a tile have."""
+    rng = np.random.default_rng(G + stretch)
+    tokens = 256 // G
+    lens, q = [7000, 300], [2 * tokens + tokens // 2 + 3, 5]
+    sh, args, _, r = attn_case(api, lens=lens, q=q, Hq=G * Hkv, Hkv=Hkv, d=64, k=24, sparse=True)
+    pos, sel = r[7], np.full((sh.T, Hkv, 24), -1, np.int32)
+    for t, p in enumerate(pos):
+        late = (t % tokens) >= tokens // 2
+        for g in range(Hkv):
+            c = [b for b in range(p // PAGE) if (b // stretch % 2 == 1) == late]
+            c = sorted(rng.choice(c, min(len(c), 20 if t % 5 else 3), replace=False)) if c else []
+            c += [p // PAGE] if t % 3 else []
+            sel[t, g, :len(c)] = c[:24]
+    # a row's list holds no more entries than it has blocks
+    for t, p in enumerate(pos):
+        sel[t, :, min(24, p // PAGE + 1):] = -1
+    check_chunk(api, sh, args, starts_of(q), sel, r[:8] + (sel,) + r[9:], sh.T)
