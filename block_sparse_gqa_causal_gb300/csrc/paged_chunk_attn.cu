@@ -23,9 +23,12 @@
 //
 // Softmax.  With t_j = l_j log2 e + log2 vs, the weight of token j's codes is
 // 2^t_j and that of the sum 2^t_j / vs, so one reference m per row bounds both
-// and P V adds up in TMEM across pages of different scales.  m is the largest t
-// so far, or up to kLag less: only then are the sums rescaled.  P (bf16) takes
-// the place of its scores in TMEM and is read from there as the A operand.
+// and P V adds up in TMEM across pages of different scales.  bf16 and fp32 keep
+// their bits at any size, so m need not be the largest t, only within 2^90 of it:
+// it is that of the row's first page, and the pages after it are searched for a
+// larger one only if the codes' largest value, 448, times the row's sum of |q|
+// could pass 2^90 times the reference.  Otherwise the scores are read once.  P
+// (bf16) takes their place in TMEM and is read from there as the A operand.
 //
 // A NaN code must not reach rows that do not see its token, and 0 x NaN does:
 // NaNs of V enter the products as 0, and rows that see one (looked for only
@@ -65,7 +68,9 @@ constexpr int kStages = 2;                    // K and V tiles
 constexpr int kRing = 8;                      // pages the planner is ahead
 constexpr int kSub = 128 * 128;               // [128 rows][64 bf16], swizzled
 constexpr int kLeast = 4;                     // products to a stretch at least
-constexpr float kLag = 8.f;                   // log2 of what a probability may outgrow its reference by
+// log2 of what a probability may outgrow its reference by where it has been looked at, and where it cannot by more: sums of
+// 2^20 probabilities of at most 2^kFar times codes of at most 2^9 stay finite.
+constexpr float kLag = 8.f, kFar = 90.f;
 constexpr int kMaskWords = kTileRows / 32;    // a bit to each row of a tile (at most 256, with G = 1)
 constexpr int kWindow = 1 << 15;              // blocks whose union is taken in one go
 constexpr int kListWarps = 4;
@@ -762,7 +767,7 @@ chunk_attn_kernel(Args a, AttnPlan plan)
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lanes + half * 128, tO = tmem + lanes + 256 + half * D;
         float m = -INFINITY, z = 0.f;          // reference (log2), sum
-        float q_down = 1.f;                    // what the queries were not multiplied by
+        float q_down = 1.f, q_sum = 0.f;       // the queries' factor, inverse; what their scores are bounded by
         int cur = -1, pos = -1, token = 0, ops = 0, splits = 0;
         bool used = false;
         Item it{};
@@ -796,7 +801,7 @@ chunk_attn_kernel(Args a, AttnPlan plan)
                     const int rr = (warp & 3) * 32 + (j0 + j) * RPI + lane / CPR;
                     uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
                     float2 f[4];
-                    float top = 0.f;
+                    float top = 0.f, sum = 0.f;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         f[k] = unpack_bf16(w[k]);
@@ -810,11 +815,17 @@ chunk_attn_kernel(Args a, AttnPlan plan)
                     for (int k = 0; k < 4; ++k) {
                         const __half2 h = __floats2half2_rn(f[k].x * up, f[k].y * up);
                         w[k] = *reinterpret_cast<const uint32_t *>(&h);
+                        sum += fabsf(f[k].x * up) + fabsf(f[k].y * up);
                     }
+#pragma unroll
+                    for (int o = 1; o < CPR; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                     *reinterpret_cast<uint4 *>(sm + half * S::TILE + (c >> 3) * kSub + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                     const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-                    const float of_row = __shfl_sync(0xffffffffu, down, (lane % RPI) * CPR);
-                    if (lane / RPI == j0 + j) q_down = of_row;
+                    const float of_row = __shfl_sync(0xffffffffu, down, (lane % RPI) * CPR), its_sum = __shfl_sync(0xffffffffu, sum, (lane % RPI) * CPR);
+                    if (lane / RPI == j0 + j) {
+                        q_down = of_row;
+                        q_sum = its_sum * 452.f;                   // 448, and what the sum's roundings could lack
+                    }
                 }
             }
             fence_proxy_async();
@@ -832,51 +843,53 @@ chunk_attn_kernel(Args a, AttnPlan plan)
 #pragma unroll 1
                 for (int c = 0; c < 64; c += 16) tmem_st16(tS + c, none);
             } else {
-                // two passes over the scores, 32 at a time, the next ones on their way from TMEM meanwhile; rolled up, so that
-                // the code stays small
-                const bool all = __all_sync(0xffffffffu, lim >= kPage - 1);
                 uint32_t x[32], y[32];
-                float mq[2] = {-INFINITY, -INFINITY};
-                auto top = [&](uint32_t (&v)[32], int c) {
-                    if (!all) {                    // masked scores: minus infinity from here on
+                // masked scores: minus infinity from here on
+                if (!__all_sync(0xffffffffu, lim >= kPage - 1)) {
+#pragma unroll 1
+                    for (int c = 0; c < kPage; c += 32) {
+                        tmem_ld32_nowait(tS + c, x);
+                        tmem_wait32(x);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = c + j <= lim ? v[j] : 0xFF800000u;
-                        tmem_st16(tS + c, v);
-                        tmem_st16(tS + c + 16, v + 16);
+                        for (int j = 0; j < 32; ++j) x[j] = c + j <= lim ? x[j] : 0xFF800000u;
+                        tmem_st16(tS + c, x);
+                        tmem_st16(tS + c + 16, x + 16);
                     }
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) mq[j >> 1 & 1] = fmaxf(mq[j >> 1 & 1], fmaxf(__uint_as_float(v[j]), __uint_as_float(v[j + 1])));
-                };
-                tmem_ld32_nowait(tS, x);
-#pragma unroll 1
-                for (int c = 0; c < kPage; c += 64) {
-                    tmem_wait32(x);
-                    tmem_ld32_nowait(tS + c + 32, y);
-                    top(x, c);
-                    tmem_wait32(y);
-                    if (c + 64 < kPage) tmem_ld32_nowait(tS + c + 64, x);
-                    top(y, c + 32);
+                    tmem_wait_st();
                 }
-                if (!all) tmem_wait_st();
-                tmem_ld32_nowait(tS, x);
-                const float t = fmaxf(mq[0], mq[1]) * fa + lv;
-                const bool up = t > m + kLag;
-                if (__any_sync(0xffffffffu, up)) {
-                    const float keep = up ? ex2(m - t) : 1.f;
-                    if (!first) {
+                // the largest score is looked for where one could lie too far above the reference
+                const bool far = !(q_sum * fa + lv <= m + kFar) && lim >= 0;
+                if (__any_sync(0xffffffffu, far)) {
+                    float top = -INFINITY;
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 16) {
-                            uint32_t o[16];
-                            tmem_ld16_nowait(tO + c, o);
-                            tmem_wait16(o);
+                    for (int c = 0; c < kPage; c += 64) {
+                        tmem_ld32_nowait(tS + c, x);
+                        tmem_ld32_nowait(tS + c + 32, y);
+                        tmem_wait32(x);
+                        tmem_wait32(y);
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
-                            tmem_st16(tO + c, o);
+                        for (int j = 0; j < 32; ++j) top = fmaxf(top, fmaxf(__uint_as_float(x[j]), __uint_as_float(y[j])));
+                    }
+                    const float t = top * fa + lv;
+                    const bool up = far && t > m + kLag;
+                    if (__any_sync(0xffffffffu, up)) {
+                        const float keep = up ? ex2(m - t) : 1.f;
+                        if (!first) {
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 16) {
+                                uint32_t o[16];
+                                tmem_ld16_nowait(tO + c, o);
+                                tmem_wait16(o);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
+                                tmem_st16(tO + c, o);
+                            }
                         }
+                        z *= keep;
+                        m = up ? t : m;
                     }
-                    z *= keep;
-                    m = up ? t : m;
                 }
+                tmem_ld32_nowait(tS, x);
                 const float c0 = m == -INFINITY ? lv : lv - m;
                 const uint64_t fa2 = pair(fa, fa), c02 = pair(c0, c0);
                 uint64_t zp[2] = {0, 0};
