@@ -71,7 +71,7 @@ constexpr int kLeast = 4;                     // products to a stretch at least
 // log2 of what a probability may outgrow its reference by where it has been looked at, and where it cannot by more: sums of
 // 2^20 probabilities of at most 2^kFar times codes of at most 2^9 stay finite.
 constexpr float kLag = 8.f, kFar = 90.f;
-constexpr int kMaskWords = kTileRows / 32;    // a bit to each row of a tile (at most 256, with G = 1)
+constexpr int kMaskWords = kTileRows / 64;    // with a selection, a bit to each row of a tile (at most 128, with G = 1)
 constexpr int kWindow = 1 << 15;              // blocks whose union is taken in one go
 constexpr int kListWarps = 4;
 
@@ -354,8 +354,8 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7
 // lanes store to eight different places of the swizzle.
 template <int D>
 struct Place {
-    int token, feature;        // of word 0; word j's is kStep tokens on
-    static constexpr int kWords = D / 16, kStep = D == 128 ? 16 : 32;
+    int token, feature;        // of a thread's first 16 codes; the next ones are kStep tokens on
+    static constexpr int kStep = D == 128 ? 16 : 32;
     __device__ explicit Place(int tid)
     {
         const int w = tid >> 5, lane = tid & 31;
@@ -570,7 +570,7 @@ chunk_attn_kernel(Args a, AttnPlan plan)
                 float ks = 0.f, vs = 0.f;
                 if (lane < n) {
                     block = a.sel ? plan.blocks[at + c + lane] : c + lane;
-                    for (int w = 0; w < kMaskWords; ++w) mask[w] = a.sel ? w < a.words ? plan.masks[(at + c + lane) * a.words + w] : 0u : ~0u;
+                    for (int w = 0; w < kMaskWords; ++w) mask[w] = w < a.words && a.sel ? plan.masks[(at + c + lane) * a.words + w] : 0u;
                     page = table[block];
                     if ((unsigned)page < (unsigned)p.n_pages) {
                         ks = a.k_scale[(long long)page * p.Hkv + g];
@@ -580,27 +580,11 @@ chunk_attn_kernel(Args a, AttnPlan plan)
                         page = -1;
                     }
                 }
-                // half A's rows are those of the first 128 / G tokens
-                int halves = 3;
-                if (a.sel && mt == 2 && lane < n) {
-                    const int half = kTileRows / 2 / p.G;
-                    uint32_t lo = 0, hi = 0;
-                    if (half >= 32) {
-                        for (int w = 0; w < kMaskWords; ++w) (w < half / 32 ? lo : hi) |= mask[w];
-                    } else {
-                        lo = mask[0] & ((1u << half) - 1);
-                        hi = mask[0] >> half;
-                    }
-                    halves = (lo ? 1 : 0) | (hi || !lo ? 2 : 0);
-                }
                 unsigned todo = __ballot_sync(0xffffffffu, page >= 0);
                 for (; ok && todo; todo &= todo - 1) {
                     const int j = __ffs(todo) - 1;
-                    int h = __shfl_sync(0xffffffffu, halves, j);
-                    if (mt == 1) {
-                        h = 1 + turn;
-                        turn ^= 1;
-                    }
+                    const int h = mt == 1 ? 1 + turn : 3;
+                    turn ^= 1;
                     if (!(ok = open())) break;
                     if (lane == j) {
                         Entry &x = ring[e % kRing];
@@ -725,7 +709,8 @@ chunk_attn_kernel(Args a, AttnPlan plan)
                 if (!(ok = wait(&q_full[h], (uint32_t)item & 1u, st, 188, abort_flag))) break;
                 begun = item;
             }
-            const bool o = due >= 0;           // whosever this page is: V's place is waited for
+            // its own next page, the end, or a page whose V waits for that one's place
+            const bool o = due >= 0 && (mine || kind == kEndEntry || (int)n >= due + kStages);
             if (o && !(ok = p_there())) break;
             // the halves take turns
             if (!(ok = wait(&turn[h], ((uint32_t)e & 1u) ^ (h == 0), st, 193, abort_flag))) break;
@@ -770,11 +755,10 @@ chunk_attn_kernel(Args a, AttnPlan plan)
         float q_down = 1.f, q_sum = 0.f;       // the queries' factor, inverse; what their scores are bounded by
         int cur = -1, pos = -1, token = 0, ops = 0, splits = 0;
         bool used = false;
-        Item it{};
 
         auto begin = [&](int item) {
             cur = item;
-            it = items[item % kRing];
+            const Item &it = items[item % kRing];
             const int rho = it.split ? r : half * 128 + r, pairs = it.rows * p.G;
             token = rho >> a.shift;
             pos = rho < pairs ? a.row_pos[it.row + token] : -1;
@@ -785,47 +769,52 @@ chunk_attn_kernel(Args a, AttnPlan plan)
             // this warp's 32 pairs of queries, as fp16: each times the power of two that brings its largest feature to 2^14 or above
             constexpr int CPR = D / 8, RPI = 32 / CPR, N = 32 / RPI;
             constexpr int ROUND = N < 8 ? N : 8;
-            const int c = lane % CPR;
+            const int c = lane % CPR, first = (warp & 3) * 32 + lane / CPR;
+            auto place = [&](int rr) { return reinterpret_cast<uint4 *>(sm + half * S::TILE + (c >> 3) * kSub + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)); };
 #pragma unroll 1
             for (int j0 = 0; j0 < N; j0 += ROUND) {
                 uint4 u[ROUND];
 #pragma unroll
                 for (int j = 0; j < ROUND; ++j) {
-                    const int rr = (warp & 3) * 32 + (j0 + j) * RPI + lane / CPR, rh = it.split ? rr : half * 128 + rr;
+                    const int rr = first + (j0 + j) * RPI, rh = it.split ? rr : half * 128 + rr;
                     u[j] = make_uint4(0, 0, 0, 0);
                     if (rh < pairs)
                         u[j] = __ldg(reinterpret_cast<const uint4 *>(a.q + ((long long)(it.row + (rh >> a.shift)) * p.Hq + it.group * p.G + (rh & (p.G - 1))) * D) + c);
                 }
 #pragma unroll
-                for (int j = 0; j < ROUND; ++j) {
-                    const int rr = (warp & 3) * 32 + (j0 + j) * RPI + lane / CPR;
-                    uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
-                    float2 f[4];
-                    float top = 0.f, sum = 0.f;
+                for (int j = 0; j < ROUND; ++j) *place(first + (j0 + j) * RPI) = u[j];
+            }
+#pragma unroll 1
+            for (int j = 0; j < N; ++j) {
+                const int rr = first + j * RPI;
+                const uint4 q = *place(rr);
+                uint32_t w[4] = {q.x, q.y, q.z, q.w};
+                float top = 0.f, sum = 0.f;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        f[k] = unpack_bf16(w[k]);
-                        top = fmaxf(top, fmaxf(fabsf(f[k].x), fabsf(f[k].y)));
-                    }
+                for (int k = 0; k < 4; ++k) {
+                    const float2 f = unpack_bf16(w[k]);
+                    top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    sum += fabsf(f.x) + fabsf(f.y);
+                }
 #pragma unroll
-                    for (int o = 1; o < CPR; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    const int ex = top > 0.f ? min(14 - ((int)(__float_as_uint(top) >> 23) - 127), 126) : 0;   // 126 falls short below 2^-112
-                    const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
+                for (int o = 1; o < CPR; o <<= 1) {
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                }
+                const int ex = top > 0.f ? min(14 - ((int)(__float_as_uint(top) >> 23) - 127), 126) : 0;   // 126 falls short below 2^-112
+                const float up = __uint_as_float((uint32_t)(127 + ex) << 23), down = __uint_as_float((uint32_t)(127 - ex) << 23);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const __half2 h = __floats2half2_rn(f[k].x * up, f[k].y * up);
-                        w[k] = *reinterpret_cast<const uint32_t *>(&h);
-                        sum += fabsf(f[k].x * up) + fabsf(f[k].y * up);
-                    }
-#pragma unroll
-                    for (int o = 1; o < CPR; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    *reinterpret_cast<uint4 *>(sm + half * S::TILE + (c >> 3) * kSub + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                    const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-                    const float of_row = __shfl_sync(0xffffffffu, down, (lane % RPI) * CPR), its_sum = __shfl_sync(0xffffffffu, sum, (lane % RPI) * CPR);
-                    if (lane / RPI == j0 + j) {
-                        q_down = of_row;
-                        q_sum = its_sum * 452.f;                   // 448, and what the sum's roundings could lack
-                    }
+                for (int k = 0; k < 4; ++k) {
+                    const float2 f = unpack_bf16(w[k]);
+                    const __half2 h = __floats2half2_rn(f.x * up, f.y * up);
+                    w[k] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+                *place(rr) = make_uint4(w[0], w[1], w[2], w[3]);
+                // 452: the largest code, 448, and what the sum's roundings could lack
+                const float of_row = __shfl_sync(0xffffffffu, down, (lane % RPI) * CPR), its_sum = __shfl_sync(0xffffffffu, sum * up * 452.f, (lane % RPI) * CPR);
+                if (lane / RPI == j) {
+                    q_down = of_row;
+                    q_sum = its_sum;
                 }
             }
             fence_proxy_async();
@@ -844,8 +833,11 @@ chunk_attn_kernel(Args a, AttnPlan plan)
                 for (int c = 0; c < 64; c += 16) tmem_st16(tS + c, none);
             } else {
                 uint32_t x[32], y[32];
-                // masked scores: minus infinity from here on
-                if (!__all_sync(0xffffffffu, lim >= kPage - 1)) {
+                // rows that see nothing of the page: their probabilities are put to 0
+                const bool mixed = !__all_sync(0xffffffffu, lim >= 0);
+                const uint32_t seen = lim >= 0 ? ~0u : 0u;
+                // rows that see a part of it: masked scores are minus infinity from here on
+                if (__builtin_expect(__any_sync(0xffffffffu, lim >= 0 && lim < kPage - 1), 0)) {
 #pragma unroll 1
                     for (int c = 0; c < kPage; c += 32) {
                         tmem_ld32_nowait(tS + c, x);
@@ -904,13 +896,17 @@ chunk_attn_kernel(Args a, AttnPlan plan)
                         zp[j >> 1 & 1] = add2(zp[j >> 1 & 1], pair(e0, e1));
                         pk[j / 2] = pack_bf16(e0, e1);
                     }
-                    if (pv != 1.f) {               // exact: a power of two
+                    if (__builtin_expect(pv != 1.f, 0)) {               // exact: a power of two
                         const __nv_bfloat162 pv2 = __float2bfloat162_rn(pv);
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             const __nv_bfloat162 q = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&pk[j]), pv2);
                             pk[j] = *reinterpret_cast<const uint32_t *>(&q);
                         }
+                    }
+                    if (mixed) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) pk[j] &= seen;
                     }
                     tmem_st16(tS + c / 2, pk);
                 };
@@ -925,7 +921,7 @@ chunk_attn_kernel(Args a, AttnPlan plan)
                 }
                 float z0, z1;
                 split(add2(zp[0], zp[1]), z0, z1);
-                z += (z0 + z1) * il;
+                if (seen) z += (z0 + z1) * il;
             }
             tmem_wait_st();
             fence_before_sync();
@@ -935,6 +931,7 @@ chunk_attn_kernel(Args a, AttnPlan plan)
         };
 
         auto finish = [&](int item) {
+            const Item &it = items[item % kRing];
             if (!wait(&o_full[half], (uint32_t)item & 1u, st, 190, abort_flag)) return false;
             fence_after_sync();
             const int rho = it.split ? r : half * 128 + r;
@@ -1012,15 +1009,17 @@ chunk_attn_kernel(Args a, AttnPlan plan)
             if (kind == kExit) break;
             if (item != cur) begin(item);
             if (kind == kPageEntry && (x.halves >> half & 1)) {
-                const bool seen = x.mask[token >> 5] >> (token & 31) & 1;
+                const bool seen = !a.sel || x.mask[token >> 5] >> (token & 31) & 1;
                 const int lim = seen ? min(pos - x.block * kPage, kPage - 1) : -1;
                 const bool first = x.first >> half & 1;
-                const float fa = x.a * q_down, lv = x.lv, il = x.il, pv = x.pv;
+                float fa = x.a * q_down;
+                if (fa == 0.f) fa = 0x1p-126f;                    // so that masked scores stay minus infinity
+                const float lv = x.lv, il = x.il, pv = x.pv;
                 done_entry(e);
                 if (!page(lim, first, fa, lv, il, pv)) break;
             } else {
-                done_entry(e);
                 if (kind == kEndEntry && !finish(item)) break;
+                done_entry(e);                     // not before: the item's place may be taken once its end is let go
             }
         }
     }
@@ -1086,10 +1085,13 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(Args a, AttnPlan plan)
     if (lane == 0) a.lse[row] = z == 0.f ? -INFINITY : (m + log2f(z)) * kLn2;
 }
 
-int mask_words(const PagedProblem &p) { return std::max(1, kTileRows / p.G / 32); }
+// Rows of a tile: 256 pairs, or 128 with a selection.  Fewer rows have fewer blocks in their union, and the two halves
+// take them in turn, where the halves of 256 pairs would wait for each other at blocks that only one of them has.
+int attn_tokens(const PagedProblem &p, bool listed) { return (listed ? kTileRows / 2 : kTileRows) / p.G; }
+int mask_words(const PagedProblem &p) { return std::max(1, attn_tokens(p, true) / 32); }
 AttnPlan attn_plan(const PagedProblem &p, void *scratch, bool listed)
 {
-    const long long most = chunk_tiles(p, kTileRows / p.G);
+    const long long most = chunk_tiles(p, attn_tokens(p, listed));
     return AttnPlan(scratch, most, p, ChunkPlan::bytes(most), listed, mask_words(p), p.num_sms);
 }
 
@@ -1097,14 +1099,14 @@ AttnPlan attn_plan(const PagedProblem &p, void *scratch, bool listed)
 
 size_t paged_chunk_scratch_bytes(const PagedProblem &p, bool attention)
 {
-    return attention ? attn_plan(p, nullptr, true).bytes : paged_chunk_scores_scratch(p);
+    return attention ? std::max(attn_plan(p, nullptr, true).bytes, attn_plan(p, nullptr, false).bytes) : paged_chunk_scores_scratch(p);
 }
 
 cudaError_t launch_paged_chunk_attn(const PagedProblem &p, const bf16 *q, const uint8_t *k8, const uint8_t *v8, const float *k_scale,
                                     const float *v_scale, const int32_t *block_table, const int32_t *q_starts, const int32_t *row_pos,
                                     const int32_t *sel, bf16 *o, float *lse, void *scratch, DeviceStatus *st, cudaStream_t s)
 {
-    const int tokens = kTileRows / p.G;
+    const int tokens = attn_tokens(p, sel != nullptr);
     cudaError_t e = launch_chunk_plan(p, q_starts, row_pos, tokens, p.G, scratch, st, s);
     if (e != cudaSuccess) return e;
     const AttnPlan plan = attn_plan(p, scratch, sel != nullptr);
@@ -1120,7 +1122,7 @@ cudaError_t launch_paged_chunk_attn(const PagedProblem &p, const bf16 *q, const 
         if ((e = allow_smem(chunk_attn_kernel<D>, AttnSmem<D>::ALLOC, allowed)) != cudaSuccess) return e;
         e = launch_chained("paged_chunk_attn_kernel", chunk_attn_kernel<D>, dim3(p.num_sms), kThreads, AttnSmem<D>::ALLOC, s, a, plan);
         if (e != cudaSuccess) return e;
-        return launch_chained("paged_chunk_join_kernel", chunk_join_kernel<D>, dim3(p.num_sms, kTileRows / 8), 256, 0, s, a, plan);
+        return launch_chained("paged_chunk_join_kernel", chunk_join_kernel<D>, dim3(p.num_sms, (sel ? kTileRows / 2 : kTileRows) / 8), 256, 0, s, a, plan);
     };
     return p.d == 128 ? run(std::integral_constant<int, 128>{}) : run(std::integral_constant<int, 64>{});
 }
