@@ -866,7 +866,7 @@ chunk_attn_kernel(Args a, AttnPlan plan)
                     const bool up = far && t > m + kLag;
                     if (__any_sync(0xffffffffu, up)) {
                         const float keep = up ? ex2(m - t) : 1.f;
-                        if (!first) {
+                        if (!first && __any_sync(0xffffffffu, up && m != -INFINITY)) {      // (rows that see their first page have no sums)
 #pragma unroll 1
                             for (int c = 0; c < D; c += 16) {
                                 uint32_t o[16];

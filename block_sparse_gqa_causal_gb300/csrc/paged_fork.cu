@@ -5,12 +5,12 @@
 // the references to p.  Slot r with a source s != r drops the references of its
 // row and takes some of s's: whole pages as they are, a page of its own for a
 // last one that is only partly filled (the caller's copies, `moves`).  All
-// slots change at once (beams trade places), so every page's changes are summed
-// up first, cnt[p] = taken - dropped, and shares[p] + cnt[p] < 0 then says that
-// nobody holds p any more.  Several slots may drop the same page; one of them,
-// the first in the order of (slot, block), stands for it (owner[p], a minimum
-// over keys, the same whatever the order of the atomics), writes its new count
-// and gives it back, so that the ring's order does not depend on timing.
+// slots change at once (beams trade places), so all that is taken and dropped is
+// summed into shares first, and shares[p] < 0 then says that nobody holds p any
+// more.  Several slots may drop the same page; one of them, the first in the
+// order of (slot, block), stands for it (owner[p], a minimum over keys, the same
+// whatever the order of the atomics) and gives it back, so that the ring's order
+// does not depend on timing.
 //
 // Compaction.  A bitmap of the pages in use; u of them.  The i-th one at or
 // above u moves to the i-th hole below u: both lists are sums of bits over the
@@ -18,8 +18,8 @@
 //
 // Both are phases over a few thousand table entries, each a handful of dependent
 // reads, with a barrier between them: latency is all there is.  One cluster of
-// eight CTAs runs all phases in one launch, its barrier in hardware; a warp takes
-// a row of the table.
+// eight CTAs runs all phases in one launch, its barrier in hardware.  A warp takes
+// 256 entries of a row, eight loads of a thread in flight.
 #include <algorithm>
 
 #include "paged.h"
@@ -61,6 +61,16 @@ __device__ Sum cta_sum(Sum v, Sum *buf)
     return v;
 }
 
+// The largest x >= 0 of the CTA, on every thread.
+__device__ int cta_max(int x, int *buf)
+{
+    x = __reduce_max_sync(0xffffffffu, x);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
+    __syncthreads();
+    return __reduce_max_sync(0xffffffffu, buf[threadIdx.x & 31]);
+}
+
 // Exclusive sums of one int a thread over the CTA; total on every thread.
 __device__ int cta_scan(int x, int *buf, int &total)
 {
@@ -85,25 +95,24 @@ __device__ int cta_scan(int x, int *buf, int &total)
     return before + in - x;
 }
 
-// scratch of a fork: by page {owner's key, count}, by request {tokens, pages before, page taken, pages given back}, the rows
-// of ended requests as they were
+// A warp's share of a row.
+constexpr int kDeep = 8, kPiece = 32 * kDeep;
+
+// scratch of a fork: by page the key of the slot and block that give it back; by request {tokens, pages before, page taken};
+// by piece of a row the pages given back; the rows as they were
 struct ForkScratch {
     u64 *owner;
-    int32_t *cnt, *new_len, *had, *take_at, *back_at, *old;
+    int32_t *new_len, *had, *take_at, *back_at, *old;
     __host__ __device__ ForkScratch(void *at, const PagedProblem &p)
     {
         owner = static_cast<u64 *>(at);
-        cnt = reinterpret_cast<int32_t *>(owner + p.n_pages);
-        new_len = cnt + p.n_pages;
+        new_len = reinterpret_cast<int32_t *>(owner + p.n_pages);
         had = new_len + p.R;
         take_at = had + p.R;
         back_at = take_at + p.R;
-        old = back_at + p.R;
+        old = back_at + (size_t)p.R * ((p.max_blocks + kPiece - 1) / kPiece);
     }
 };
-
-constexpr u64 kTaker = 1ull << 63;   // of a key: takes before none that drops
-constexpr int kFreed = INT_MIN;
 
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(kCtas, 1, 1)
 fork_kernel(PagedProblem p, ForkArgs a, void *scratch, DeviceStatus *st)
@@ -122,7 +131,7 @@ fork_kernel(PagedProblem p, ForkArgs a, void *scratch, DeviceStatus *st)
     // ---- what each slot becomes; every CTA looks at all of them, the first writes it down
     const int head = a.free_state[0], count = a.free_state[1];
     Sum total{0, 0};
-    int taken = 0;
+    int taken = 0, most = 0;
     for (int r0 = 0; r0 < R; r0 += kThreads) {
         const int r = r0 + tid;
         int take = 0;
@@ -139,6 +148,7 @@ fork_kernel(PagedProblem p, ForkArgs a, void *scratch, DeviceStatus *st)
             }
             total.bad |= !fine;
             total.a += take;
+            most = max(most, s == r ? 0 : max(had, n / kPage));
             if (cta == 0) {
                 x.new_len[r] = n;
                 x.had[r] = had;
@@ -164,107 +174,122 @@ fork_kernel(PagedProblem p, ForkArgs a, void *scratch, DeviceStatus *st)
     }
     cluster_sync();
 
-    // A row's dropped and taken entries: fn(page, key, drops) for each, warp by warp.
-    auto entries = [&](auto fn) {
-        for (int r = gwarp; r < R; r += kWarps) {
-            const int s = a.src[r];
-            if (s == r) continue;
-            const int had = x.had[r], full = s >= 0 ? x.new_len[r] / kPage : 0;
-            const int32_t *mine = row(r), *theirs = s >= 0 ? row(s) : mine;
-            for (int b0 = 0; b0 < max(had, full); b0 += 32) {
-                const int b = b0 + lane;
-                const u64 key = (u64)r * (u64)nb + (u64)b;
-                const int drop = b < had ? mine[b] : -1, take = b < full ? theirs[b] : -1;
-                fn(r, b, key, drop, b < had, take, b < full);
-            }
+    // The rows' pieces that change, warp by warp: fn(r, s, first block, pages before, whole pages taken, piece).
+    const int pieces = (cta_max(most, ints) + kPiece - 1) / kPiece;
+    const long long items = (long long)R * pieces;
+    auto each = [&](auto fn) {
+        for (long long i = gwarp; i < items; i += kWarps) {
+            const int r = (int)(i / pieces), s = a.src[r];
+            if (s != r) fn(r, s, (int)(i % pieces) * kPiece, x.had[r], s >= 0 ? x.new_len[r] / kPage : 0, i);
         }
     };
+    auto load = [&](int (&to)[kDeep], const int32_t *from, int first, int n) {
+#pragma unroll
+        for (int j = 0; j < kDeep; ++j) to[j] = first + 32 * j + lane < n ? from[first + 32 * j + lane] : -1;
+    };
+    auto key_of = [&](int r, int b) { return (u64)r * (u64)nb + (u64)b; };
 
-    // ---- the pages concerned: nothing counted yet
-    entries([&](int r, int b, u64, int drop, bool drops, int take, bool takes) {
-        if (drops) x.old[(long long)r * nb + b] = drop;
-        if (is_page(drop)) {
-            x.cnt[drop] = 0;
-            x.owner[drop] = ~0ull;
-        }
-        if (is_page(take)) {
-            x.cnt[take] = 0;
-            x.owner[take] = ~0ull;
-        }
-        if ((drops && !is_page(drop)) || (takes && !is_page(take))) report(st, kDevCheck, 161, r);
-    });
-    cluster_sync();
-    entries([&](int, int, u64 key, int drop, bool, int take, bool) {
-        if (is_page(drop)) {
-            atomicAdd(&x.cnt[drop], -1);
-            atomicMin(&x.owner[drop], key);
-        }
-        if (is_page(take)) {
-            atomicAdd(&x.cnt[take], 1);
-            atomicMin(&x.owner[take], key | kTaker);
+    // ---- the rows as they are; nobody gives a page back yet
+    each([&](int r, int, int b0, int had, int, long long) {
+        int drop[kDeep];
+        load(drop, row(r), b0, had);
+#pragma unroll
+        for (int j = 0; j < kDeep; ++j) {
+            const int b = b0 + 32 * j + lane;
+            if (b >= had) continue;
+            x.old[(long long)r * nb + b] = drop[j];
+            if (is_page(drop[j])) x.owner[drop[j]] = ~0ull;
+            else report(st, kDevCheck, 161, r);
         }
     });
     cluster_sync();
-    // ---- the owner of a page writes its count; pages given back, row by row
-    for (int r = gwarp; r < R; r += kWarps) {
-        const int s = a.src[r];
-        int back = 0;
-        if (s != r) {
-            const int had = x.had[r], full = s >= 0 ? x.new_len[r] / kPage : 0;
-            const int32_t *mine = row(r), *theirs = s >= 0 ? row(s) : mine;
-            for (int b0 = 0; b0 < max(had, full); b0 += 32) {
-                const int b = b0 + lane;
-                const u64 key = (u64)r * (u64)nb + (u64)b;
-                const int drop = b < had ? mine[b] : -1, take = b < full ? theirs[b] : -1;
-                bool freed = false;
-                if (is_page(drop) && x.owner[drop] == key) {
-                    const int left = a.shares[drop] + x.cnt[drop];
-                    freed = left < 0;
-                    a.shares[drop] = max(left, 0);
-                    if (freed) x.cnt[drop] = kFreed;
-                }
-                if (is_page(take) && x.owner[take] == (key | kTaker)) a.shares[take] += x.cnt[take];
-                back += __popc(__ballot_sync(0xffffffffu, freed));
+    each([&](int r, int s, int b0, int had, int full, long long) {
+        int drop[kDeep], take[kDeep];
+        load(drop, row(r), b0, had);
+        load(take, s >= 0 ? row(s) : row(r), b0, full);
+#pragma unroll
+        for (int j = 0; j < kDeep; ++j) {
+            const int b = b0 + 32 * j + lane;
+            if (is_page(drop[j])) {
+                atomicAdd(&a.shares[drop[j]], -1);
+                atomicMin(&x.owner[drop[j]], key_of(r, b));
             }
+            if (is_page(take[j])) atomicAdd(&a.shares[take[j]], 1);
+            else if (b < full) report(st, kDevCheck, 161, r);
         }
-        if (lane == 0) x.back_at[r] = back;
+    });
+    cluster_sync();
+    // Whether (r, b) gives its page back, for each of a thread's blocks.
+    auto frees = [&](bool (&is)[kDeep], const int (&drop)[kDeep], int r, int b0) {
+        u64 key[kDeep];
+        int left[kDeep];
+#pragma unroll
+        for (int j = 0; j < kDeep; ++j) {
+            const bool fine = is_page(drop[j]);
+            key[j] = fine ? x.owner[drop[j]] : ~0ull;
+            left[j] = fine ? a.shares[drop[j]] : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < kDeep; ++j) is[j] = left[j] < 0 && key[j] == key_of(r, b0 + 32 * j + lane);
+    };
+    // ---- pages given back, piece by piece
+    for (long long i = cta * kThreads + tid; i < items; i += kCtas * kThreads) {
+        const int r = (int)(i / pieces);
+        if (a.src[r] == r) x.back_at[i] = 0;
     }
+    each([&](int r, int, int b0, int had, int, long long i) {
+        int drop[kDeep], back = 0;
+        bool is[kDeep];
+        load(drop, row(r), b0, had);
+        frees(is, drop, r, b0);
+#pragma unroll
+        for (int j = 0; j < kDeep; ++j) back += __popc(__ballot_sync(0xffffffffu, is[j]));
+        if (lane == 0) x.back_at[i] = back;
+    });
     cluster_sync();
     int given = 0;
     if (cta == 0) {
-        for (int r0 = 0; r0 < R; r0 += kThreads) {
-            const int r = r0 + tid;
+        for (long long i0 = 0; i0 < items; i0 += kThreads) {
+            const long long i = i0 + tid;
             int all;
-            const int before = cta_scan(r < R ? x.back_at[r] : 0, ints, all);
-            if (r < R) x.back_at[r] = given + before;
+            const int before = cta_scan(i < items ? x.back_at[i] : 0, ints, all);
+            if (i < items) x.back_at[i] = given + before;
             given += all;
         }
     }
     cluster_sync();
     // ---- the ring, the tables and the moves
-    for (int r = gwarp; r < R; r += kWarps) {
+    // s's row as it was: its copy where s changes too
+    auto source = [&](int s) { return a.src[s] != s ? x.old + (long long)s * nb : row(s); };
+    each([&](int r, int s, int b0, int had, int full, long long i) {
+        int drop[kDeep], take[kDeep];
+        bool is[kDeep];
+        int back = x.back_at[i];
+        load(drop, x.old + (long long)r * nb, b0, had);
+        load(take, s >= 0 ? source(s) : row(r), b0, full);
+        frees(is, drop, r, b0);
+#pragma unroll
+        for (int j = 0; j < kDeep; ++j) {
+            const int b = b0 + 32 * j + lane;
+            const unsigned all = __ballot_sync(0xffffffffu, is[j]);
+            if (is[j]) {
+                a.free_pages[((long long)head + count + back + __popc(all & ((1u << lane) - 1))) % p.n_pages] = drop[j];
+                a.shares[drop[j]] = 0;                 // nobody but this block's thread looks at it
+            }
+            back += __popc(all);
+            if (b < full) row(r)[b] = take[j];
+        }
+    });
+    for (int r = cta * kThreads + tid; r < R; r += kCtas * kThreads) {
         const int s = a.src[r];
         int from = -1, to = -1, rows = 0;
         if (s != r) {
-            const int had = x.had[r], n = x.new_len[r], full = n / kPage, rest = s >= 0 ? n % kPage : 0;
-            int32_t *mine = row(r);
-            // s's row as it was: its copy where s changes too
-            const int32_t *theirs = s < 0 ? mine : a.src[s] != s ? x.old + (long long)s * nb : row(s);
-            int back = x.back_at[r];
-            for (int b0 = 0; b0 < max(had, full); b0 += 32) {
-                const int b = b0 + lane;
-                const int drop = b < had ? x.old[(long long)r * nb + b] : -1;
-                const bool freed = is_page(drop) && x.cnt[drop] == kFreed && x.owner[drop] == (u64)r * (u64)nb + (u64)b;
-                const unsigned all = __ballot_sync(0xffffffffu, freed);
-                if (freed) a.free_pages[((long long)head + count + back + __popc(all & ((1u << lane) - 1))) % p.n_pages] = drop;
-                back += __popc(all);
-                if (b < full) mine[b] = theirs[b];
-            }
-            if (rest && lane == 0) {
+            const int n = x.new_len[r], full = n / kPage, rest = s >= 0 ? n % kPage : 0;
+            if (rest) {
                 const int page = a.free_pages[((long long)head + x.take_at[r]) % p.n_pages];
-                from = theirs[full];
+                from = source(s)[full];
                 const bool fine = is_page(page);
-                mine[full] = fine ? page : -1;
+                row(r)[full] = fine ? page : -1;
                 if (fine) a.shares[page] = 0;
                 if (fine && is_page(from)) {
                     to = page;
@@ -274,16 +299,12 @@ fork_kernel(PagedProblem p, ForkArgs a, void *scratch, DeviceStatus *st)
                     from = -1;
                 }
             }
-            if (lane == 0) {
-                a.lens[r] = n;
-                if (a.held) a.held[r] = pages_of(n);
-            }
+            a.lens[r] = n;
+            if (a.held) a.held[r] = pages_of(n);
         }
-        if (lane == 0) {
-            a.moves[3 * (long long)r] = from;
-            a.moves[3 * (long long)r + 1] = to;
-            a.moves[3 * (long long)r + 2] = rows;
-        }
+        a.moves[3 * (long long)r] = from;
+        a.moves[3 * (long long)r + 1] = to;
+        a.moves[3 * (long long)r + 2] = rows;
     }
     if (cta == 0 && tid == 0) {
         a.free_state[0] = (int)((head + total.a) % p.n_pages);
@@ -479,7 +500,7 @@ copy_kernel(PagedProblem p, const int32_t *moves, int n_moves, uint8_t *k8, uint
 
 size_t paged_fork_scratch_bytes(const PagedProblem &p)
 {
-    return (size_t)p.n_pages * 12 + 4 * (4 * (size_t)p.R + (size_t)p.R * p.max_blocks);
+    return (size_t)p.n_pages * 8 + 4 * (size_t)p.R * (3 + (size_t)(p.max_blocks + kPiece - 1) / kPiece + p.max_blocks);
 }
 
 cudaError_t launch_paged_fork(const PagedProblem &p, const ForkArgs &a, void *scratch, DeviceStatus *st, cudaStream_t s)
