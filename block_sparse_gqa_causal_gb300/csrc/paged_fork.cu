@@ -189,17 +189,21 @@ fork_kernel(PagedProblem p, ForkArgs a, void *scratch, DeviceStatus *st)
     };
     auto key_of = [&](int r, int b) { return (u64)r * (u64)nb + (u64)b; };
 
+    // A page that a row drops and takes at the same block, as beams of one prompt do with nearly all of theirs, stays held:
+    // there is nothing to count, and nobody else gives it back either (256 requests of four prompts: 39 -> 21 us).
+
     // ---- the rows as they are; nobody gives a page back yet
-    each([&](int r, int, int b0, int had, int, long long) {
-        int drop[kDeep];
+    each([&](int r, int s, int b0, int had, int full, long long) {
+        int drop[kDeep], take[kDeep];
         load(drop, row(r), b0, had);
+        load(take, s >= 0 ? row(s) : row(r), b0, full);
 #pragma unroll
         for (int j = 0; j < kDeep; ++j) {
             const int b = b0 + 32 * j + lane;
             if (b >= had) continue;
             x.old[(long long)r * nb + b] = drop[j];
-            if (is_page(drop[j])) x.owner[drop[j]] = ~0ull;
-            else report(st, kDevCheck, 161, r);
+            if (!is_page(drop[j])) report(st, kDevCheck, 161, r);
+            else if (drop[j] != take[j]) x.owner[drop[j]] = ~0ull;
         }
     });
     cluster_sync();
@@ -210,6 +214,7 @@ fork_kernel(PagedProblem p, ForkArgs a, void *scratch, DeviceStatus *st)
 #pragma unroll
         for (int j = 0; j < kDeep; ++j) {
             const int b = b0 + 32 * j + lane;
+            if (drop[j] == take[j]) continue;
             if (is_page(drop[j])) {
                 atomicAdd(&a.shares[drop[j]], -1);
                 atomicMin(&x.owner[drop[j]], key_of(r, b));
@@ -220,12 +225,12 @@ fork_kernel(PagedProblem p, ForkArgs a, void *scratch, DeviceStatus *st)
     });
     cluster_sync();
     // Whether (r, b) gives its page back, for each of a thread's blocks.
-    auto frees = [&](bool (&is)[kDeep], const int (&drop)[kDeep], int r, int b0) {
+    auto frees = [&](bool (&is)[kDeep], const int (&drop)[kDeep], const int (&take)[kDeep], int r, int b0) {
         u64 key[kDeep];
         int left[kDeep];
 #pragma unroll
         for (int j = 0; j < kDeep; ++j) {
-            const bool fine = is_page(drop[j]);
+            const bool fine = drop[j] != take[j] && is_page(drop[j]);
             key[j] = fine ? x.owner[drop[j]] : ~0ull;
             left[j] = fine ? a.shares[drop[j]] : 0;
         }
@@ -237,11 +242,12 @@ fork_kernel(PagedProblem p, ForkArgs a, void *scratch, DeviceStatus *st)
         const int r = (int)(i / pieces);
         if (a.src[r] == r) x.back_at[i] = 0;
     }
-    each([&](int r, int, int b0, int had, int, long long i) {
-        int drop[kDeep], back = 0;
+    each([&](int r, int s, int b0, int had, int full, long long i) {
+        int drop[kDeep], take[kDeep], back = 0;
         bool is[kDeep];
         load(drop, row(r), b0, had);
-        frees(is, drop, r, b0);
+        load(take, s >= 0 ? row(s) : row(r), b0, full);
+        frees(is, drop, take, r, b0);
 #pragma unroll
         for (int j = 0; j < kDeep; ++j) back += __popc(__ballot_sync(0xffffffffu, is[j]));
         if (lane == 0) x.back_at[i] = back;
@@ -267,7 +273,7 @@ fork_kernel(PagedProblem p, ForkArgs a, void *scratch, DeviceStatus *st)
         int back = x.back_at[i];
         load(drop, x.old + (long long)r * nb, b0, had);
         load(take, s >= 0 ? source(s) : row(r), b0, full);
-        frees(is, drop, r, b0);
+        frees(is, drop, take, r, b0);
 #pragma unroll
         for (int j = 0; j < kDeep; ++j) {
             const int b = b0 + 32 * j + lane;
@@ -277,7 +283,7 @@ fork_kernel(PagedProblem p, ForkArgs a, void *scratch, DeviceStatus *st)
                 a.shares[drop[j]] = 0;                 // nobody but this block's thread looks at it
             }
             back += __popc(all);
-            if (b < full) row(r)[b] = take[j];
+            if (b < full && drop[j] != take[j]) row(r)[b] = take[j];
         }
     });
     for (int r = cta * kThreads + tid; r < R; r += kCtas * kThreads) {
