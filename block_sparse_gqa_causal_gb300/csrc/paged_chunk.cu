@@ -13,9 +13,14 @@
 // part 1) and so on, cut into equal stretches for persistent CTAs, whatever the
 // requests' lengths.  Pages and queries come by TMA; the queries have two
 // buffers, so that a tile's first product does not wait for them.
+// Each half has an issuer of its own: issuing blocks until the tensor cores take the
+// instruction, so one warp's waits for the next page and accumulator came on top of
+// its products (116 us for 2,048 rows of 8 groups over 32,768 tokens, against 101;
+// the tensor cores' rate gives 68).  With the queries in TMEM instead, which leaves
+// three accumulators, one issuer took 115: it was not shared memory that it waited for.
 //   warp 0      TMA producer
-//   warp 1      TMEM, tcgen05.mma issuer
-//   warps 2..9  one (row, group) to a thread: TMEM -> registers, causal mask, maximum, store
+//   warps 1, 2  tcgen05.mma issuers of the halves; TMEM
+//   warps 3..10 one (row, group) to a thread: TMEM -> registers, causal mask, maximum, store
 #include <algorithm>
 #include <climits>
 
@@ -122,7 +127,7 @@ chunk_plan_kernel(PagedProblem p, const int32_t *q_starts, const int32_t *row_po
 constexpr int kStages = 3;
 constexpr int kLeast = 2;                      // units of work to a stretch at least
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kThreads = 32 * (3 + kEpiWarps);
 constexpr int kSub = 128 * 128;               // [128 rows][64 bf16], swizzled
 
 template <int DI>
@@ -175,21 +180,23 @@ chunk_scores_kernel(PagedProblem p, const __grid_constant__ CUtensorMap tmap_q, 
     uint8_t *sK = smem + S::OFF_K;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::OFF_BAR);
     uint64_t *full = bars, *empty = bars + kStages, *q_full = bars + 2 * kStages, *q_empty = q_full + 2;
-    uint64_t *acc_full = q_full + 4, *acc_empty = q_full + 6;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(q_full + 8);
+    uint64_t *acc_full = q_full + 4, *acc_empty = q_full + 8;      // [half][2]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(q_full + 12);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     __shared__ int sh_tile;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&empty[s], 2);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&q_full[a], 1);
-            mbar_init(&q_empty[a], 1);
+            mbar_init(&q_empty[a], 2);
+        }
+        for (int a = 0; a < 4; ++a) {
             mbar_init(&acc_full[a], 1);
-            mbar_init(&acc_empty[a], kEpiWarps);
+            mbar_init(&acc_empty[a], kEpiWarps / 2);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -258,48 +265,54 @@ chunk_scores_kernel(PagedProblem p, const __grid_constant__ CUtensorMap tmap_q, 
             for (int i = max(0, issued - kStages); i < issued; ++i)
                 mbar_wait(&full[i % kStages], (uint32_t)(i / kStages) & 1u, nullptr, 0, nullptr);
         }
-    } else if (warp == 1) {
+    } else if (warp <= 2) {
         constexpr uint32_t kIdesc = idesc_bf16(128, 128);
-        int n = 0, qn = 0;
+        const int m = warp - 1;
+        uint64_t *my_full = acc_full + 2 * m, *my_empty = acc_empty + 2 * m;
+        int n = 0, unit = 0, qn = 0;
         bool ok = true;
         while (ok && walk.next()) {
             const int aq = qn & 1;
-            const int mt = walk.mt;
+            const bool part_of = m < walk.mt;         // a tile of one half passes the second's issuer by
             if (!(ok = mbar_wait_warp(&q_full[aq], (uint32_t)(qn >> 1) & 1u, st, 175, abort_flag))) break;
-            const uint64_t dq = sdesc_k128(smem_u32(smem + aq * S::Q));
+            const uint64_t dq = sdesc_k128(smem_u32(smem + aq * S::Q + m * S::KB * kSub));
             for (int c = walk.c0; c < walk.c1; ++c, ++n) {
-                const int s = n % kStages, a = n & 1;
-                if (!(ok = mbar_wait_warp(&acc_empty[a], ((uint32_t)(n >> 1) & 1u) ^ 1u, st, 176, abort_flag))) break;
+                const int s = n % kStages, a = unit & 1;
+                if (part_of && !(ok = mbar_wait_warp(&my_empty[a], ((uint32_t)(unit >> 1) & 1u) ^ 1u, st, 176, abort_flag))) break;
                 if (!(ok = mbar_wait_warp(&full[s], (uint32_t)(n / kStages) & 1u, st, 177, abort_flag))) break;
                 fence_after_sync();
                 const uint64_t dk = sdesc_k128(smem_u32(sK + s * S::K));
                 if (elect_one()) {
-                    for (int m = 0; m < mt; ++m) {
+                    if (part_of) {
 #pragma unroll
                         for (int ks = 0; ks < DI / 16; ++ks) {
                             const uint32_t off = (ks >> 2) * kSub + (ks & 3) * 32;
-                            mma_bf16(tmem + (uint32_t)((a * 2 + m) * 128), desc_adv(dq, m * S::KB * kSub + off), desc_adv(dk, off), kIdesc, ks > 0);
+                            mma_bf16(tmem + (uint32_t)((m * 2 + a) * 128), desc_adv(dq, off), desc_adv(dk, off), kIdesc, ks > 0);
                         }
+                        mma_commit(&my_full[a]);
+                        mma_commit(&empty[s]);
+                        if (c + 1 == walk.c1) mma_commit(&q_empty[aq]);
+                    } else {
+                        mbar_arrive(&empty[s]);
+                        if (c + 1 == walk.c1) mbar_arrive(&q_empty[aq]);
                     }
-                    mma_commit(&empty[s]);
-                    mma_commit(&acc_full[a]);
-                    if (c + 1 == walk.c1) mma_commit(&q_empty[aq]);
                 }
                 __syncwarp();
+                unit += part_of;
             }
             ++qn;
         }
-        if (*abort_flag && n > 0)       // MMAs end in order: the last batch's end is that of all
-            mbar_wait(&acc_full[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u, nullptr, 0, nullptr);
+        if (*abort_flag && unit > 0)    // MMAs end in order: the last batch's end is that of all
+            mbar_wait(&my_full[(unit - 1) & 1], (uint32_t)((unit - 1) >> 1) & 1u, nullptr, 0, nullptr);
     } else {
-        const int e = warp - 2, m = e >> 2, quarter = warp & 3;
+        const int m = (warp - 3) >> 2, quarter = warp & 3;
         const int row = m * 128 + quarter * 32 + lane;          // of the tile
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-        int n = 0;
+        int unit = 0;
         bool ok = true;
         while (ok && walk.next()) {
+            if (m >= walk.mt) continue;
             const int here = parts > 1 ? min(kTileRows, p.Hkv - walk.part * kTileRows) : walk.t.rows * p.Hkv;
-            const int mt = walk.mt;
             const long long rho = (long long)walk.t.row * p.Hkv + walk.part * kTileRows + row;
             const bool mine = row < here;
             int pos = mine ? row_pos[rho / p.Hkv] : -1;
@@ -313,52 +326,44 @@ chunk_scores_kernel(PagedProblem p, const __grid_constant__ CUtensorMap tmap_q, 
                 const unsigned good = __ballot_sync(0xffffffffu, lane < pages && (unsigned)table[c8 + lane] < (unsigned)p.n_pages);
                 float grp[8];
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    grp[u] = -INFINITY;
-                    if (u >= pages) break;
-                    const int a = n & 1;
-                    if (!mbar_wait_warp(&acc_full[a], (uint32_t)(n >> 1) & 1u, st, 178, abort_flag)) {
+                for (int k = 0; k < 8; ++k) grp[k] = -INFINITY;
+                // (rolled: eight copies of this do not stay in the instruction cache)
+#pragma unroll 1
+                for (int u = 0; u < pages; ++u, ++unit) {
+                    const int a = m * 2 + (unit & 1);
+                    if (!mbar_wait_warp(&acc_full[a], (uint32_t)(unit >> 1) & 1u, st, 178, abort_flag)) {
                         ok = false;
                         break;
                     }
-                    ++n;
                     fence_after_sync();
-                    if (m >= mt) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&acc_empty[a]);
-                        continue;
-                    }
+                    const uint32_t base = tmem + lane_base + (uint32_t)(a * 128);
+                    uint32_t v[4][32];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) tmem_ld32_nowait(base + k * 32, v[k]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) tmem_wait32(v[k]);
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&acc_empty[a]);
                     const int j0 = (c8 + u) * kPage;
-                    const bool whole = j0 + kPage - 1 <= first_pos;
-                    const int lim = min(pos - j0, kPage - 1);          // last visible token of the page for this row
-                    const uint32_t base = tmem + lane_base + (uint32_t)((a * 2 + m) * 128);
+                    if (j0 + kPage - 1 > first_pos) {
+                        const int lim = min(pos - j0, kPage - 1);      // last visible token of the page for this row
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (k * 32 + j > lim) v[k][j] = __float_as_uint(-INFINITY);
+                    }
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t v0[32], v1[32];
-                        tmem_ld32_nowait(base + h * 64, v0);
-                        tmem_ld32_nowait(base + h * 64 + 32, v1);
-                        tmem_wait32(v0);
-                        tmem_wait32(v1);
-                        if (h == 1) {
-                            fence_before_sync();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&acc_empty[a]);
-                        }
-                        if (whole) {
+                    for (int k = 0; k < 4; k += 2)
 #pragma unroll
-                            for (int jj = 0; jj < 32; ++jj)
-                                m4[jj & 3] = fmaxf(m4[jj & 3], fmaxf(__uint_as_float(v0[jj]), __uint_as_float(v1[jj])));
-                        } else {
+                        for (int j = 0; j < 32; ++j)
+                            m4[j & 3] = fmaxf(m4[j & 3], fmaxf(__uint_as_float(v[k][j]), __uint_as_float(v[k + 1][j])));
+                    const float most = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_idx;
 #pragma unroll
-                            for (int jj = 0; jj < 32; ++jj) {
-                                const int jo = h * 64 + jj;
-                                m4[jj & 3] = fmaxf(m4[jj & 3], fmaxf(jo <= lim ? __uint_as_float(v0[jj]) : -INFINITY,
-                                                                     jo + 32 <= lim ? __uint_as_float(v1[jj]) : -INFINITY));
-                            }
-                        }
-                    }
-                    if (good >> u & 1) grp[u] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_idx;
+                    for (int k = 0; k < 8; ++k)
+                        if (k == u && (good >> u & 1)) grp[k] = most;
                 }
                 if (!ok) break;
                 const int last = min(c8 + pages - 1, c_last);

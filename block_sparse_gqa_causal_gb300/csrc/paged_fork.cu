@@ -19,7 +19,9 @@
 // Both are phases over a few thousand table entries, each a handful of dependent
 // reads, with a barrier between them: latency is all there is.  One cluster of
 // eight CTAs runs all phases in one launch, its barrier in hardware.  A warp takes
-// 256 entries of a row, eight loads of a thread in flight.
+// 256 entries of a row, eight loads of a thread in flight.  Sixteen CTAs were
+// no faster.  8 beams of 1,000 tokens fork in 10 us, 256 requests of up to 32,120
+// in 17; the plan of a compaction of 4,300 pages takes 14.
 #include <algorithm>
 
 #include "paged.h"
@@ -429,7 +431,8 @@ compact_kernel(PagedProblem p, CompactArgs a, void *scratch, DeviceStatus *st)
 
 // ---------------------------------------------------------------- copies
 // Work comes in pieces: one head's K or V codes of a move, or its index keys (and the scales).  A CTA looks at 256 pieces
-// at a time, a thread to each, and copies those that are any: a 16-KB tile in one go, five CTAs to an SM.
+// at a time, a thread to each, and copies those that are any: a 16-KB tile in one go, five CTAs to an SM.  The memory
+// bounds it: a compaction's 630 MB, read and written, take 100 us (93 at the copy rate).
 constexpr int kCopyThreads = 256;
 
 __global__ void __launch_bounds__(kCopyThreads, 5)

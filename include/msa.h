@@ -569,10 +569,11 @@ msa_status msa_paged_copy(const msa_paged_shape *shape, const int32_t *moves, in
  *
  * Attention: queries enter the products with 8 significant bits, features
  * below 2^-31 of their row's and head's largest off by 2^-39 of it at most;
- * probabilities with 8 significant bits, however small; sums are fp32.  With a selection, a tile
- * reads the blocks that any of its rows selected.  Entries that msa_paged_attn
- * leaves out and records are left out and recorded here too.  Deterministic.
- * A NaN in a cached row reaches those rows only that see it.
+ * probabilities with 8 significant bits, down to 2^-126 of the largest that the
+ * row has met in its first page (below it they count as 0); sums are fp32.  With
+ * a selection, a tile reads the blocks that any of its rows selected.  Entries
+ * that msa_paged_attn leaves out and records are left out and recorded here too.
+ * Deterministic.  A NaN in a cached row reaches those rows only that see it.
  */
 msa_status msa_paged_chunk_scores(const msa_paged_shape *shape, const void *q_idx, const void *k_idx, const int32_t *block_table,
                                   const int32_t *q_starts, const int32_t *row_pos, float *block_scores, void *workspace,
