@@ -11,7 +11,13 @@
 // and with a few hundred rows to a page the tensor cores bound it: 4 x 128 x 128
 // x d operations a page and 128 pairs.  A tile has 256 pairs (256 / G rows): two
 // halves, A and B, whose products alternate on the tensor cores while the other
-// half's scores become probabilities.
+// half's scores become probabilities.  2,048 rows of 64 heads over 32,768 tokens
+// take 1,785 us (1,190 TFLOP/s), where the tensor cores' rate gives 1,088: a page
+// takes some 3,500 cycles, of which the products need 2,050, and as many of shared
+// memory's (both sides of S, V, and the tiles laid down); the conversion of the
+// codes, 2,800 of its warps', and the softmax, 2,300 of each half's, are near it,
+// so that every wait between them counts.  The halves' issuers take turns: when both
+// issue at once the products get in one another's way (2,240 us).
 //
 // Codes to 16 bits.  e4m3 products would need queries and probabilities as pairs
 // of e4m3 terms, and small probabilities as several levels of those.  So four
@@ -35,15 +41,16 @@
 // then) get theirs when they are written.
 //
 // With a selection, a tile walks the union of its rows' blocks (made by a kernel
-// before, with a bit to each row that selected the block); a half without any
-// such row is passed over.
+// before, with a bit to each row that selected the block).  3,000 rows of 32 heads
+// that selected 16 of up to 391 blocks each take 540 us: the unions of 32 rows have
+// 47 blocks, three times what a row selected.
 // The work is one list of products, those of (tile 0, group 0), (tile 0, group 1)
 // and so on, cut into equal stretches for persistent CTAs.  A stretch cuts at
 // most two tiles; those pieces' states go to the workspace, and a kernel after
 // joins them, in the order of their pages.  A tile of up to 128 pairs has only half
 // A: its pages go to the two halves in turn, both with the same queries, and A joins them.
 //   warps 0..3, 4..7   softmax of half A, B, a pair to a thread
-//   warps 8..11        codes of K and V to bf16 tiles in shared memory, loaded a tile ahead
+//   warps 8..11        codes of K and V to 16-bit tiles in shared memory, loaded a tile ahead
 //   warps 12, 13       tcgen05.mma issuers of half A, B
 //   warp 14            planner: pages, scales and masks, through a ring
 #include <algorithm>
@@ -1032,7 +1039,10 @@ chunk_attn_kernel(Args a, AttnPlan plan)
 }
 
 // ---------------------------------------------------------------- cut tiles
-// A CTA of 8 rows for each stretch: those of the item that ends in it and was begun before.
+// CTAs of 64 pairs for each stretch: those of the item that ends in it and was begun before.  A warp takes eight, whose
+// states it loads at once: finding the item is a chain of loads as long as the rest (a pair to a warp: 35 us instead of
+// 21 for the tiles of 256 that 152 stretches cut).
+constexpr int kJoin = 8;
 template <int D>
 __global__ void __launch_bounds__(256) chunk_join_kernel(Args a, AttnPlan plan)
 {
@@ -1051,38 +1061,52 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(Args a, AttnPlan plan)
     int c0, c1;
     cut(start, pages, mt, mine.from, mine.to, c0, c1);
     if (c0 == 0 || c0 >= c1 || c1 != pages) return;
-    const int rho = blockIdx.y * 8 + warp;
-    if (rho >= t.rows * p.G) return;
-    const int pos = a.row_pos[t.row + rho / p.G];
-    if (pos < 0 || (long long)pos >= (long long)p.max_blocks * kPage) return;
+    const int rho0 = (blockIdx.y * 8 + warp) * kJoin, pairs = t.rows * p.G;
+    if (rho0 >= pairs) return;
     const float2 *stats = plan.stats(a.ctas, D);
-    const int from = (int)(start / mine.share);
-    auto slot = [&](int k) -> long long {
+    const bool has = lane * 4 < D;
+    float m[kJoin], z[kJoin], x[kJoin][4];
+#pragma unroll
+    for (int i = 0; i < kJoin; ++i) {
+        m[i] = -INFINITY;
+        z[i] = x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
+    }
+    for (int k = (int)(start / mine.share); k <= cta; ++k) {
         int b0, b1;
         cut(start, pages, mt, mine.share * k, min(pieces.total, mine.share * (k + 1)), b0, b1);
-        return b0 < b1 ? ((long long)2 * k + (b0 == 0)) * kTileRows + rho : -1;
-    };
-    float m = -INFINITY, z = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int k = from; k <= cta; ++k) {
-        const long long s = slot(k);
-        if (s < 0) continue;
-        const float2 b = stats[s];
-        if (b.y == 0.f) continue;                              // none of its pages visible
-        const float top = fmaxf(m, b.x), wa = m == top ? 1.f : ex2(m - top), wb = b.x == top ? 1.f : ex2(b.x - top);
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (lane * 4 < D) y = *reinterpret_cast<const float4 *>(plan.part + s * D + lane * 4);
-        z = z * wa + b.y * wb;
-        x[0] = x[0] * wa + y.x * wb;
-        x[1] = x[1] * wa + y.y * wb;
-        x[2] = x[2] * wa + y.z * wb;
-        x[3] = x[3] * wa + y.w * wb;
-        m = top;
+        if (b0 >= b1) continue;
+        const long long s = ((long long)2 * k + (b0 == 0)) * kTileRows + rho0;      // (a slot has 256 pairs, whatever the tile's)
+        float2 b[kJoin];
+        float4 y[kJoin];
+#pragma unroll
+        for (int i = 0; i < kJoin; ++i) {
+            b[i] = stats[s + i];
+            y[i] = has ? *reinterpret_cast<const float4 *>(plan.part + (s + i) * D + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < kJoin; ++i) {
+            if (b[i].y == 0.f) continue;                       // none of its pages visible
+            const float top = fmaxf(m[i], b[i].x), wa = m[i] == top ? 1.f : ex2(m[i] - top), wb = b[i].x == top ? 1.f : ex2(b[i].x - top);
+            z[i] = z[i] * wa + b[i].y * wb;
+            x[i][0] = x[i][0] * wa + y[i].x * wb;
+            x[i][1] = x[i][1] * wa + y[i].y * wb;
+            x[i][2] = x[i][2] * wa + y[i].z * wb;
+            x[i][3] = x[i][3] * wa + y[i].w * wb;
+            m[i] = top;
+        }
     }
-    const long long row = (long long)(t.row + rho / p.G) * p.Hq + g * p.G + rho % p.G;
-    const float inv = z == 0.f ? 0.f : 1.f / z;
-    if (lane * 4 < D)
-        *reinterpret_cast<uint2 *>(a.o + row * D + lane * 4) = make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
-    if (lane == 0) a.lse[row] = z == 0.f ? -INFINITY : (m + log2f(z)) * kLn2;
+#pragma unroll
+    for (int i = 0; i < kJoin; ++i) {
+        const int rho = rho0 + i;
+        const int pos = rho < pairs ? a.row_pos[t.row + rho / p.G] : -1;
+        if (pos < 0 || (long long)pos >= (long long)p.max_blocks * kPage) continue;
+        const long long row = (long long)(t.row + rho / p.G) * p.Hq + g * p.G + rho % p.G;
+        const float inv = z[i] == 0.f ? 0.f : 1.f / z[i];
+        if (has)
+            *reinterpret_cast<uint2 *>(a.o + row * D + lane * 4) =
+                make_uint2(pack_bf16(x[i][0] * inv, x[i][1] * inv), pack_bf16(x[i][2] * inv, x[i][3] * inv));
+        if (lane == 0) a.lse[row] = z[i] == 0.f ? -INFINITY : (m[i] + log2f(z[i])) * kLn2;
+    }
 }
 
 // Rows of a tile: 256 pairs, or 128 with a selection.  Fewer rows have fewer blocks in their union, and the two halves
@@ -1122,7 +1146,7 @@ cudaError_t launch_paged_chunk_attn(const PagedProblem &p, const bf16 *q, const 
         if ((e = allow_smem(chunk_attn_kernel<D>, AttnSmem<D>::ALLOC, allowed)) != cudaSuccess) return e;
         e = launch_chained("paged_chunk_attn_kernel", chunk_attn_kernel<D>, dim3(p.num_sms), kThreads, AttnSmem<D>::ALLOC, s, a, plan);
         if (e != cudaSuccess) return e;
-        return launch_chained("paged_chunk_join_kernel", chunk_join_kernel<D>, dim3(p.num_sms, (sel ? kTileRows / 2 : kTileRows) / 8), 256, 0, s, a, plan);
+        return launch_chained("paged_chunk_join_kernel", chunk_join_kernel<D>, dim3(p.num_sms, (sel ? kTileRows / 2 : kTileRows) / (8 * kJoin)), 256, 0, s, a, plan);
     };
     return p.d == 128 ? run(std::integral_constant<int, 128>{}) : run(std::integral_constant<int, 64>{});
 }
