@@ -409,3 +409,74 @@ def test_chunk_blocks_that_one_half_of_a_tile_selects(api, G, Hkv, stretch):
     for t, p in enumerate(pos):
         sel[t, :, min(24, p // PAGE + 1):] = -1
     check_chunk(api, sh, args, starts_of(q), sel, r[:8] + (sel,) + r[9:], sh.T)
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), 3e38])
+@pytest.mark.parametrize("sparse", [True, False])
+def test_chunk_extreme_queries_stay_in_their_rows(api, value, sparse):
+    import torch
+    c = dict(lens=[700, 300], q=[150, 10], Hq=8, Hkv=2, d=64, k=3)
+    sh, args, sel, r = attn_case(api, sparse=sparse, **c)
+    _, o0, l0 = run_chunk(api, sh, args, [0, 150, 160], sel, 160)
+    q = args[0].clone()
+    q[40, 6, 11], q[155, 1, :] = value, value
+    _, o, l = run_chunk(api, sh, (q,) + args[1:], [0, 150, 160], sel, 160)
+    hit = torch.zeros(160, 8, dtype=torch.bool, device="cuda")
+    hit[40, 6] = hit[155, 1] = True
+    assert torch.equal(o[~hit], o0[~hit]) and torch.equal(l[~hit], l0[~hit])
+    if np.isinf(value):
+        assert not torch.isfinite(l[hit]).any()
+
+
+def test_chunk_calls_on_two_streams_at_once(api):
+    import torch
+    jobs = []
+    for c, sparse in ((dict(lens=[3000, 1700], q=[300, 130], Hq=16, Hkv=4, d=128, k=8), True), (dict(lens=[2000], q=[500], Hq=8, Hkv=2, d=64, k=4), False)):
+        sh, args, sel, r = attn_case(api, sparse=sparse, **c)
+        jobs.append((sh, args[:6] + (i32(starts_of(c["q"])), args[7]), None if sel is None else i32(sel)))
+    alone = [api.paged_chunk_attn(sh, *a, sel_idx=s) for sh, a, s in jobs]
+    spaces = [api.new_paged_workspace(sh, api.OP_PAGED_CHUNK_ATTN) for sh, _, _ in jobs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[api.paged_chunk_attn(sh, *a, sel_idx=s, workspace=ws, stream=st) for (sh, a, s), ws, st in zip(jobs, spaces, streams)] for _ in range(6)]
+    torch.cuda.synchronize()
+    for both in got:
+        for (o, l), (o0, l0) in zip(both, alone):
+            assert torch.equal(o, o0) and torch.equal(l, l0)
+    for ws in spaces:
+        api.check_device_status(ws)
+
+
+def test_one_workspace_for_all_calls_and_shapes(api):
+    """A workspace of the largest need serves smaller shapes and the other calls in between."""
+    import torch
+    big = attn_case(api, sparse=True, lens=[3000, 1700, 20], q=[200, 130, 20], Hq=16, Hkv=4, d=128, k=8)
+    small = attn_case(api, sparse=False, lens=[130, 1], q=[5, 1], Hq=8, Hkv=2, d=64, k=4)
+    calls = [(big[0], big[1], i32(big[2]), [200, 130, 20]), (small[0], small[1], None, [5, 1])]
+    ws = api.new_paged_workspace(big[0], api.OP_PAGED_CHUNK_ATTN)
+    need = max(api.new_paged_workspace(c[0], op).numel() for c in calls for op in (api.OP_PAGED_CHUNK_ATTN, api.OP_PAGED_CHUNK_SCORES))
+    assert ws.numel() >= need
+    run = lambda c, w: api.paged_chunk_attn(c[0], *c[1][:6], i32(starts_of(c[3])), c[1][7], sel_idx=c[2], workspace=w)
+    first = [run(c, None) for c in calls]
+    kx, _ = bf(np.random.default_rng(0).standard_normal((small[0].n_pages, PAGE, 64)))
+    qx, _ = bf(np.random.default_rng(1).standard_normal((small[0].T, 2, 64)))
+    for _ in range(3):
+        for c, f in zip(calls, first):
+            o, l = run(c, ws)
+            n = sum(c[3])
+            assert torch.equal(o[:n], f[0][:n]) and torch.equal(l[:n], f[1][:n])
+            api.paged_chunk_scores(small[0], qx, kx, small[1][5], i32(starts_of([5, 1])), small[1][7], workspace=ws)
+    api.check_device_status(ws)
+    assert not ws[:4096].any()
+
+
+@pytest.mark.parametrize("sparse", [True, False])
+def test_chunk_calls_with_a_page_twice_and_single_tokens(api, sparse):
+    """Requests whose tables name one page at several blocks, most of them without rows, the others with one."""
+    q = [0] * 400 + [1] * 70 + [0] * 30 + [2]
+    c = dict(lens=[0] * 400 + [200 + 11 * i for i in range(70)] + [0] * 30 + [900], q=q, Hq=8, Hkv=2, d=64, k=4)
+    sh, args, sel, r = attn_case(api, sparse=sparse, **c)
+    table = r[5].copy()
+    table[410:420, 1] = table[410:420, 0]
+    table[-1, 1:] = table[-1, 0]
+    check_chunk(api, sh, args[:5] + (i32(table),) + args[6:], starts_of(q), sel, r[:5] + (table,) + r[6:], sum(q))

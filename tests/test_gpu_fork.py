@@ -230,3 +230,42 @@ def test_copy_leaves_out_bad_moves(api, bad):
         api.check_device_status(ws)
     for x, w in zip(c, want):
         assert np.array_equal(raw(x), w)
+
+
+@pytest.mark.parametrize("R,nb,families", [(3, 300, 2), (5, 1100, 2), (40, 513, 3), (2, 257, 1)])
+@pytest.mark.parametrize("kind", ["swap", "one", "end", "half"])
+def test_fork_of_long_rows(api, R, nb, families, kind):
+    """Rows of more entries than a warp takes at a time; of `half`, some requests go on from a part of another's."""
+    rng = np.random.default_rng(R + nb)
+    s = state(rng, R, nb, families, spare=R + 5)
+    src = {"swap": rng.permutation(R), "one": np.full(R, R // 2), "end": np.full(R, -1), "half": rng.integers(0, R, R)}[kind]
+    fl = np.array([s[0][x] // 2 if x >= 0 else 0 for x in src]) if kind == "half" else None
+    ws, got = run_fork(api, src, fl, s)
+    api.check_device_status(ws)
+    want = ref.fork(src, s[0], s[2], s[3], s[4], s[5], fl, s[1])
+    for name, g, w in zip(("lens", "held", "table", "ring", "free", "shares", "moves"), got, want):
+        if g is not None:
+            assert np.array_equal(g, w), name
+
+
+def test_forks_on_two_streams_at_once(api):
+    """Two pools, each with its tables and its workspace; the calls of both overlap."""
+    import torch
+    rng = np.random.default_rng(3)
+    jobs = [state(rng, 200, 40, 5, spare=205), state(rng, 64, 300, 4, spare=70)]
+    want, got = [], []
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in jobs:
+        R = len(s[0])
+        s_src = rng.integers(-1, R, R)
+        want.append(ref.fork(s_src, s[0], s[2], s[3], s[4], s[5], None, None))
+        got.append((s_src, [i32(x) for x in (s_src, s[0], s[2], s[3], s[4], s[5])], shape(api, s[2], len(s[3]))))
+    spaces = [api.new_paged_workspace(g[2], api.OP_PAGED_FORK) for g in got]
+    torch.cuda.synchronize()
+    moves = [api.paged_fork(g[2], *g[1], workspace=ws, stream=st) for g, ws, st in zip(got, spaces, streams)]
+    torch.cuda.synchronize()
+    for g, w, m, ws in zip(got, want, moves, spaces):
+        api.check_device_status(ws)
+        lens, _, table, ring, free, shares, wm = w
+        for a, b in zip(g[1][1:] + [m], (lens, table, ring, free, shares, wm)):
+            assert np.array_equal(a.cpu().numpy(), b)
