@@ -571,7 +571,10 @@ msa_status msa_paged_copy(const msa_paged_shape *shape, const int32_t *moves, in
  * below 2^-31 of their row's and head's largest off by 2^-39 of it at most;
  * probabilities with 8 significant bits, down to 2^-126 of the largest that the
  * row has met in its first page (below it they count as 0); sums are fp32.  With
- * a selection, a tile reads the blocks that any of its rows selected.  Entries
+ * a selection, a tile of 128 pairs computes the blocks that any of its rows
+ * selected for all of them: that pays while they are fewer than about a quarter of
+ * what its rows selected one by one; msa_paged_attn is faster for rows that have
+ * little in common, and for fewer than 16 rows a request.  Entries
  * that msa_paged_attn leaves out and records are left out and recorded here too.
  * Deterministic.  A NaN in a cached row reaches those rows only that see it.
  */
