@@ -18,6 +18,8 @@
 // its products (116 us for 2,048 rows of 8 groups over 32,768 tokens, against 101;
 // the tensor cores' rate gives 68).  With the queries in TMEM instead, which leaves
 // three accumulators, one issuer took 115: it was not shared memory that it waited for.
+// Of the 101, 77 are pages (1,400 cycles each, of which the products need 1,024), the
+// rest the start, the first queries and the blocks past the rows.
 //   warp 0      TMA producer
 //   warps 1, 2  tcgen05.mma issuers of the halves; TMEM
 //   warps 3..10 one (row, group) to a thread: TMEM -> registers, causal mask, maximum, store
