@@ -247,6 +247,7 @@ int64_t token_stride(const at::Tensor &t, int64_t T, int64_t heads, int64_t d)
     int64_t stride = 0, next = 0;
     for (int64_t i = n - 3; i >= 0; --i) {
         if (t.size(i) == 1) continue;
+        if (t.stride(i) <= 0) return -1;     // (an expanded tensor: tokens that share their memory)
         if (!stride) stride = t.stride(i);
         else if (t.stride(i) != next) return -1;
         next = t.stride(i) * t.size(i);

@@ -147,3 +147,18 @@ def test_on_a_stream_and_in_a_graph(api):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out[0], want[0] * 2) and torch.equal(back[0], api.rotary_bwd(sh, want[0] * 2, None, f)[0])
+
+
+def test_tensors_without_memory_of_their_own_are_refused(api):
+    """Expanded tensors have one token's memory for all, or one head's: neither as inputs nor as outputs."""
+    import torch
+    sh = api.RotaryShape(T=6, Hq=4, Hkv=2, d=64)
+    f = api.rotary_freqs(64)
+    z = lambda *n: torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    q = z(6, 4, 64)
+    for bad in (z(1, 4, 64).expand(6, 4, 64), z(6, 1, 64).expand(6, 4, 64), z(1, 3, 4, 64).expand(2, 3, 4, 64), z(2, 1, 4, 64).expand(2, 3, 4, 64)):
+        with pytest.raises(ValueError, match="q: need"):
+            api.rotary_fwd(sh, bad, None, f)
+        with pytest.raises(ValueError, match="q_out: need"):
+            api.rotary_fwd(sh, q, None, f, q_out=bad)
+    assert not q.any()
