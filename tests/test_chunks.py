@@ -72,8 +72,8 @@ def test_workspaces_grow_with_the_shape(api):
     for op in (api.OP_PAGED_FORK, api.OP_PAGED_COMPACT, api.OP_PAGED_CHUNK_SCORES, api.OP_PAGED_CHUNK_ATTN):
         a, b = api.paged_workspace_size(small, op), api.paged_workspace_size(big, op)
         assert 4096 <= a <= b and a % 256 == b % 256 == 0
-    # a count and a key by page, four numbers by request, a copy of the table
-    assert api.paged_workspace_size(big, api.OP_PAGED_FORK) >= 4096 + 5000 * 12 + 40 * 16 + 40 * 16 * 4
+    # a key by page, three numbers by request, one by piece of a row, a copy of the table
+    assert api.paged_workspace_size(big, api.OP_PAGED_FORK) >= 4096 + 5000 * 8 + 40 * 12 + 40 * 4 + 40 * 16 * 4
     with pytest.raises(api.MsaError):
         api.paged_workspace_size(small, 37)
 
