@@ -184,15 +184,20 @@ __device__ __forceinline__ bool selected(const PagedProblem &p, const int32_t *s
     const int c_last = pos / kPage, entries = min(p.topk, c_last + 1);
     int prev = -1;
     bool fine = true;
-    for (int i = 0; i < p.topk; ++i) {
-        const int c = s[i];
-        if (c == -1) continue;
-        if (i >= entries || c <= prev || c > c_last) {
-            fine = false;
-            continue;
+    for (int i0 = 0; i0 < p.topk; i0 += 8) {
+        int c[8];                              // eight loads in flight: one after another they were most of the kernel
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c[j] = i0 + j < p.topk ? s[i0 + j] : -1;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (c[j] == -1) continue;
+            if (i0 + j >= entries || c[j] <= prev || c[j] > c_last) {
+                fine = false;
+                continue;
+            }
+            prev = c[j];
+            fn(c[j]);
         }
-        prev = c;
-        fn(c);
     }
     return fine;
 }
