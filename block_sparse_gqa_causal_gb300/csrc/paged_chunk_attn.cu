@@ -74,7 +74,7 @@ constexpr int kThreads = 32 * (kPlanner + 1);
 constexpr int kStages = 2;                    // K and V tiles
 constexpr int kRing = 8;                      // pages the planner is ahead
 constexpr int kSub = 128 * 128;               // [128 rows][64 bf16], swizzled
-constexpr int kLeast = 4;                     // products to a stretch at least
+constexpr int kLeast = 4;                     // products to a stretch at least, where an item has as many
 // log2 of what a probability may outgrow its reference by where it has been looked at, and where it cannot by more: sums of
 // 2^20 probabilities of at most 2^kFar times codes of at most 2^9 stay finite.
 constexpr float kLag = 8.f, kFar = 90.f;
@@ -320,6 +320,10 @@ struct Pieces {
         n_items = n * ar.p.Hkv;
         total = ar.sel ? pl.before[n_items] : pl.tiles.before[n] * ar.p.Hkv;
     }
+    // Units of a stretch at least: an item costs as much as four to five pages to begin and end, and one that is cut has to be
+    // joined, so items of a few pages stay whole, but no CTA takes a second one for having too little to do (13 rows over one
+    // page, 8 items: 46 us in two CTAs, 18 in eight).
+    __device__ int least() const { return (int)max(1ll, min((long long)kLeast, (total + n_items - 1) / max(n_items, 1))); }
     // the item that unit w is in, by a whole warp
     __device__ int find(long long w, int lane) const
     {
@@ -532,7 +536,7 @@ chunk_attn_kernel(Args a, AttnPlan plan)
 
     if (warp == kPlanner) {
         const Pieces pieces(plan, a);
-        const ChunkShare mine(pieces.total, gridDim.x, kLeast, blockIdx.x);
+        const ChunkShare mine(pieces.total, gridDim.x, pieces.least(), blockIdx.x);
         int e = 0, seq = 0;
         bool ok = true;
         auto open = [&]() { return wait(&ring_empty[e % kRing], ((uint32_t)(e / kRing) & 1u) ^ 1u, st, 182, abort_flag); };
@@ -1056,7 +1060,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(Args a, AttnPlan plan)
     const PagedProblem &p = a.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
     const Pieces pieces(plan, a);
-    const ChunkShare mine(pieces.total, a.ctas, kLeast, cta);
+    const ChunkShare mine(pieces.total, a.ctas, pieces.least(), cta);
     if (mine.from >= mine.to) return;
     const int item = pieces.find(mine.from, lane);
     const long long start = pieces.start(item);
