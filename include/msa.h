@@ -570,7 +570,8 @@ msa_status msa_paged_copy(const msa_paged_shape *shape, const int32_t *moves, in
  * Attention: queries enter the products with 8 significant bits, features
  * below 2^-31 of their row's and head's largest off by 2^-39 of it at most;
  * probabilities with 8 significant bits, down to 2^-126 of the largest that the
- * row has met in its first page (below it they count as 0); sums are fp32.  With
+ * row met in its first page, each times its page's V scale (to fewer bits below,
+ * and to 0 from 2^-134 on); sums are fp32.  With
  * a selection, a tile of 128 pairs computes the blocks that any of its rows
  * selected for all of them: that pays while they are fewer than about a quarter of
  * what its rows selected one by one; msa_paged_attn is faster for rows that have
