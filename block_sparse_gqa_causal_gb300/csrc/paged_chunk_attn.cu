@@ -27,14 +27,24 @@
 // head; V to bf16, so that probabilities keep their 8 bits at any size, which
 // takes five.
 //
-// Softmax.  With t_j = l_j log2 e + log2 vs, the weight of token j's codes is
-// 2^t_j and that of the sum 2^t_j / vs, so one reference m per row bounds both
-// and P V adds up in TMEM across pages of different scales.  bf16 and fp32 keep
-// their bits at any size, so m need not be the largest t, only within 2^90 of it:
-// it is that of the row's first page, and the pages after it are searched for a
-// larger one only if the codes' largest value, 448, times the row's sum of |q|
-// could pass 2^90 times the reference.  Otherwise the scores are read once.  P
+// Softmax.  With t_j = l_j log2 e + lv, 2^lv the page's V scale over that of the
+// stretch's first page of the tile (2^base), the weight of token j's codes is
+// P = 2^(t_j - m) and its part of the sum P 2^-lv, so one reference m per row does
+// for both and P V adds up in TMEM across pages of different scales.  bf16 and fp32
+// keep their bits at any size, so m need not be the largest t, only within 2^kFar
+// of it: it is that of the row's first page, and the pages after it are searched for
+// a larger one only if the codes' largest value, 448, times the row's sum of |q|
+// could pass 2^kFar times the reference.  Otherwise the scores are read once.  P
 // (bf16) takes their place in TMEM and is read from there as the A operand.
+//
+// What keeps the sums finite: with P up to 2^kFar and the 2^30 tokens that a table
+// can name, P V ends below 2^(89 + 8.9 + 30), and the row's sum below
+// 2^(89 + 30 + kBelow) if no lv is below -kBelow: a page whose scale is smaller than
+// that, zeros for one (which are appended with 2^-112), has lv = -kBelow and what is
+// left, pv < 1, on its P.  Scales above 2^(base + kAbove) leave a pv > 1: there the
+// largest score is always looked for.  kAbove keeps the sum of a row that only sees
+// such pages, and what other pages add to it, well inside fp32; the bounds on base
+// leave pv at 2^67 at most, so that P V stays finite with it.
 //
 // A NaN code must not reach rows that do not see its token, and 0 x NaN does:
 // NaNs of V enter the products as 0, and rows that see one (looked for only
@@ -75,9 +85,10 @@ constexpr int kStages = 2;                    // K and V tiles
 constexpr int kRing = 8;                      // pages the planner is ahead
 constexpr int kSub = 128 * 128;               // [128 rows][64 bf16], swizzled
 constexpr int kLeast = 4;                     // products to a stretch at least, where an item has as many
-// log2 of what a probability may outgrow its reference by where it has been looked at, and where it cannot by more: sums of
-// 2^20 probabilities of at most 2^kFar times codes of at most 2^9 stay finite.
-constexpr float kLag = 8.f, kFar = 90.f;
+// log2 of what a probability may outgrow its reference by where it has been looked at, and where it cannot by more.
+constexpr float kLag = 8.f, kFar = 89.f;
+// log2 of how far a page's V scale is taken into t below and above the first page's, and of the largest and least of that.
+constexpr int kBelow = 8, kAbove = 90, kBase = 30;
 constexpr int kMaskWords = kTileRows / 64;    // with a selection, a bit to each row of a tile (at most 128, with G = 1)
 constexpr int kWindow = 1 << 15;              // blocks whose union is taken in one go
 constexpr int kListWarps = 4;
@@ -109,13 +120,14 @@ enum Kind { kPageEntry = 0, kEndEntry = 1, kExit = 2 };
 struct Entry {                 // a page of the ring
     int kind, item, page, block;
     int halves, first;         // bits of the halves that take it; of those whose first page it is
-    float a, lv, il, pv;       // logits' factor, log2 of the V scale (-100 at least), 2^-lv, what lv leaves of the scale (1)
+    float a, lv, il, pv;       // logits' factor, log2 of the V scale over 2^base (cut off), 2^-lv, and what lv leaves of it (1)
     uint32_t mask[kMaskWords];
 };
 struct Item {                  // a tile's piece
     int row, rows, req, group, part;    // part: the piece's place among the partial states; -1: a whole tile
     int split;                 // one half's pairs, pages in turn
     int c0, c1;
+    int base;                  // log2 of the V scale that its sums are in
     long long at;              // of the tile's list
 };
 
@@ -573,11 +585,12 @@ chunk_attn_kernel(Args a, AttnPlan plan)
                 i.split = mt == 1;
                 i.c0 = c0;
                 i.c1 = c1;
+                i.base = 0;
                 i.at = at;
             }
             __syncwarp();
             const int32_t *table = a.block_table + (long long)t.req * p.max_blocks;
-            int turn = 0;
+            int turn = 0, base = 0;
             unsigned begun = 0;
             for (int c = c0; ok && c < c1; c += 32) {
                 const int n = min(32, c1 - c);
@@ -597,6 +610,8 @@ chunk_attn_kernel(Args a, AttnPlan plan)
                     }
                 }
                 unsigned todo = __ballot_sync(0xffffffffu, page >= 0);
+                const int ev = (int)(__float_as_uint(vs) >> 23 & 255) - 127;
+                if (!begun && todo) base = __shfl_sync(0xffffffffu, min(max(ev, -kBase), kBase), __ffs(todo) - 1);
                 for (; ok && todo; todo &= todo - 1) {
                     const int j = __ffs(todo) - 1;
                     const int h = mt == 1 ? 1 + turn : 3;
@@ -611,10 +626,11 @@ chunk_attn_kernel(Args a, AttnPlan plan)
                         x.halves = h;
                         x.first = h & ~begun;
                         x.a = qk * ks;
-                        const int ex = min(max((int)(__float_as_uint(vs) >> 23 & 255) - 127, -100), 126);
-                        x.lv = (float)ex;
-                        x.il = __uint_as_float((uint32_t)(127 - ex) << 23);
-                        x.pv = vs * x.il;
+                        const int lv = min(max(ev - base, -kBelow), kAbove);
+                        x.lv = (float)lv;
+                        x.il = __uint_as_float((uint32_t)(127 - lv) << 23);
+                        x.pv = vs * __uint_as_float((uint32_t)(127 - lv - base) << 23);
+                        if (!begun) items[seq % kRing].base = base;      // read after the item's end, which this entry comes before
                         for (int w = 0; w < kMaskWords; ++w) x.mask[w] = mask[w];
                         mbar_arrive(&ring_full[e % kRing]);
                     }
@@ -866,7 +882,7 @@ chunk_attn_kernel(Args a, AttnPlan plan)
                     tmem_wait_st();
                 }
                 // the largest score is looked for where one could lie too far above the reference
-                const bool far = !(q_sum * fa + lv <= m + kFar) && lim >= 0;
+                const bool far = (!(q_sum * fa + lv <= m + kFar) || pv > 1.f) && lim >= 0;
                 if (__any_sync(0xffffffffu, far)) {
                     float top = -INFINITY;
 #pragma unroll 1
@@ -971,7 +987,14 @@ chunk_attn_kernel(Args a, AttnPlan plan)
                 m = top;
             }
             const bool any_a = __any_sync(0xffffffffu, wa != 0.f), any_b = __any_sync(0xffffffffu, wb != 0.f);
-            const float inv = it.part >= 0 ? 1.f : z == 0.f ? 0.f : 1.f / z;
+            // z = f 2^k, f below 1.  A whole tile's outputs are O 2^base / z.  A piece's state is (m + k, f) and O 2^(base - k), no
+            // larger than outputs, so that pieces in different bases join.  2^(base - k) in two steps: what is between them is no larger
+            // than the larger end.  (A sum that is NaN stays in f.)
+            const int ez = (int)(__float_as_uint(z) >> 23 & 255), k = ez == 0 || ez == 255 ? 0 : min(ez - 126, 126);
+            const float f = z * __uint_as_float((uint32_t)(127 - k) << 23);
+            const int by = it.base - k, half_by = by >> 1;
+            const float by0 = z == 0.f ? 0.f : __uint_as_float((uint32_t)(127 + half_by) << 23);
+            const float by1 = __uint_as_float((uint32_t)(127 + by - half_by) << 23), inv = it.part >= 0 || z == 0.f ? by1 : by1 / f;
             const long long row = (long long)(it.row + token) * p.Hq + it.group * p.G + (rho & (p.G - 1));
             float *part = it.part >= 0 ? plan.part + ((long long)it.part * kTileRows + rho) * D : nullptr;
 #pragma unroll 1
@@ -992,6 +1015,8 @@ chunk_attn_kernel(Args a, AttnPlan plan)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) x[j] += wb == 0.f ? 0.f : __uint_as_float(o[j]) * wb;
                 }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] = x[j] * by0 * inv;
                 if (mine && part) {
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) *reinterpret_cast<float4 *>(part + c + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
@@ -999,14 +1024,13 @@ chunk_attn_kernel(Args a, AttnPlan plan)
 #pragma unroll
                     for (int j = 0; j < 16; j += 8)
                         *reinterpret_cast<uint4 *>(a.o + row * D + c + j) =
-                            make_uint4(pack_bf16(x[j] * inv, x[j + 1] * inv), pack_bf16(x[j + 2] * inv, x[j + 3] * inv),
-                                       pack_bf16(x[j + 4] * inv, x[j + 5] * inv), pack_bf16(x[j + 6] * inv, x[j + 7] * inv));
+                            make_uint4(pack_bf16(x[j], x[j + 1]), pack_bf16(x[j + 2], x[j + 3]), pack_bf16(x[j + 4], x[j + 5]), pack_bf16(x[j + 6], x[j + 7]));
                 }
                 __syncwarp();
             }
             if (mine) {
-                if (part) plan.stats(a.ctas, D)[(long long)it.part * kTileRows + rho] = make_float2(z == 0.f ? -INFINITY : m, z);
-                else a.lse[row] = z == 0.f ? -INFINITY : (m + log2f(z)) * kLn2;
+                if (part) plan.stats(a.ctas, D)[(long long)it.part * kTileRows + rho] = make_float2(z == 0.f ? -INFINITY : m + (float)k, f);
+                else a.lse[row] = z == 0.f ? -INFINITY : (m + (float)k + log2f(f)) * kLn2;
                 if (nan_item[item % kRing] == item) spoil<D>(a, plan, it, pos, token, part, a.o + row * D);
             }
             __syncwarp();
@@ -1095,7 +1119,8 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(Args a, AttnPlan plan)
 #pragma unroll
         for (int i = 0; i < kJoin; ++i) {
             if (b[i].y == 0.f) continue;                       // none of its pages visible
-            const float top = fmaxf(m[i], b[i].x), wa = m[i] == top ? 1.f : ex2(m[i] - top), wb = b[i].x == top ? 1.f : ex2(b[i].x - top);
+            // (2^-10: sums of values near the largest that there are stay finite)
+            const float top = fmaxf(m[i], b[i].x), wa = m[i] == top ? 1.f : ex2(m[i] - top), wb = (b[i].x == top ? 1.f : ex2(b[i].x - top)) * 0x1p-10f;
             z[i] = z[i] * wa + b[i].y * wb;
             x[i][0] = x[i][0] * wa + y[i].x * wb;
             x[i][1] = x[i][1] * wa + y[i].y * wb;
@@ -1114,7 +1139,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(Args a, AttnPlan plan)
         if (has)
             *reinterpret_cast<uint2 *>(a.o + row * D + lane * 4) =
                 make_uint2(pack_bf16(x[i][0] * inv, x[i][1] * inv), pack_bf16(x[i][2] * inv, x[i][3] * inv));
-        if (lane == 0) a.lse[row] = z[i] == 0.f ? -INFINITY : (m[i] + log2f(z[i])) * kLn2;
+        if (lane == 0) a.lse[row] = z[i] == 0.f ? -INFINITY : (m[i] + log2f(z[i] * 0x1p10f)) * kLn2;
     }
 }
 

@@ -571,7 +571,9 @@ msa_status msa_paged_copy(const msa_paged_shape *shape, const int32_t *moves, in
  * below 2^-31 of their row's and head's largest off by 2^-39 of it at most;
  * probabilities with 8 significant bits, down to 2^-126 of the largest that the
  * row met in its first page, each times its page's V scale (to fewer bits below,
- * and to 0 from 2^-134 on); sums are fp32.  With
+ * and to 0 from 2^-134 on; the first page's scale counts as no less than 2^-8 of
+ * that of the first page of the row's tile, or than 2^-38); sums are fp32, and
+ * finite whatever the pages' scales.  With
  * a selection, a tile of 128 pairs computes the blocks that any of its rows
  * selected for all of them: that pays while they are fewer than about a quarter of
  * what its rows selected one by one; msa_paged_attn is faster for rows that have
