@@ -90,6 +90,7 @@ constexpr float kLag = 8.f, kFar = 89.f;
 // log2 of how far a page's V scale is taken into t below and above the first page's, and of the largest and least of that.
 constexpr int kBelow = 8, kAbove = 90, kBase = 30;
 constexpr int kMaskWords = kTileRows / 64;    // with a selection, a bit to each row of a tile (at most 128, with G = 1)
+constexpr int kNoBlock = 1 << 23;             // behind any block of a table
 constexpr int kWindow = 1 << 15;              // blocks whose union is taken in one go
 constexpr int kListWarps = 4;
 
@@ -610,6 +611,18 @@ chunk_attn_kernel(Args a, AttnPlan plan)
                     }
                 }
                 unsigned todo = __ballot_sync(0xffffffffu, page >= 0);
+                // A piece none of whose pages is one gets a page that no row sees, so that every end follows a page of its item:
+                // the warps that convert the codes look for the next page before they lay down a V, and the ends before it are
+                // held until that V has been multiplied (eight in a row would fill the ring).
+                if (!begun && !todo && c + 32 >= c1) {
+                    if (lane == 0) {
+                        page = 0;
+                        block = kNoBlock;
+                        vs = 1.f;
+                        for (int w = 0; w < kMaskWords; ++w) mask[w] = 0;
+                    }
+                    todo = 1;
+                }
                 const int ev = (int)(__float_as_uint(vs) >> 23 & 255) - 127;
                 if (!begun && todo) base = __shfl_sync(0xffffffffu, min(max(ev, -kBase), kBase), __ffs(todo) - 1);
                 for (; ok && todo; todo &= todo - 1) {
