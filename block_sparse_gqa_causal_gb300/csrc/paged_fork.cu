@@ -189,6 +189,8 @@ fork_kernel(PagedProblem p, ForkArgs a, void *scratch, DeviceStatus *st)
 #pragma unroll
         for (int j = 0; j < kDeep; ++j) to[j] = first + 32 * j + lane < n ? from[first + 32 * j + lane] : -1;
     };
+    // whether a row drops and takes a page (or the same entry that is none) at block b; outside of a row there is neither
+    auto same = [&](int drop, int take, int b, int had, int full) { return drop == take && b < had && b < full; };
     auto key_of = [&](int r, int b) { return (u64)r * (u64)nb + (u64)b; };
 
     // A page that a row drops and takes at the same block, as beams of one prompt do with nearly all of theirs, stays held:
@@ -205,7 +207,7 @@ fork_kernel(PagedProblem p, ForkArgs a, void *scratch, DeviceStatus *st)
             if (b >= had) continue;
             x.old[(long long)r * nb + b] = drop[j];
             if (!is_page(drop[j])) report(st, kDevCheck, 161, r);
-            else if (drop[j] != take[j]) x.owner[drop[j]] = ~0ull;
+            else if (!same(drop[j], take[j], b, had, full)) x.owner[drop[j]] = ~0ull;
         }
     });
     cluster_sync();
@@ -216,7 +218,7 @@ fork_kernel(PagedProblem p, ForkArgs a, void *scratch, DeviceStatus *st)
 #pragma unroll
         for (int j = 0; j < kDeep; ++j) {
             const int b = b0 + 32 * j + lane;
-            if (drop[j] == take[j]) continue;
+            if (same(drop[j], take[j], b, had, full)) continue;
             if (is_page(drop[j])) {
                 atomicAdd(&a.shares[drop[j]], -1);
                 atomicMin(&x.owner[drop[j]], key_of(r, b));
@@ -227,12 +229,12 @@ fork_kernel(PagedProblem p, ForkArgs a, void *scratch, DeviceStatus *st)
     });
     cluster_sync();
     // Whether (r, b) gives its page back, for each of a thread's blocks.
-    auto frees = [&](bool (&is)[kDeep], const int (&drop)[kDeep], const int (&take)[kDeep], int r, int b0) {
+    auto frees = [&](bool (&is)[kDeep], const int (&drop)[kDeep], const int (&take)[kDeep], int r, int b0, int had, int full) {
         u64 key[kDeep];
         int left[kDeep];
 #pragma unroll
         for (int j = 0; j < kDeep; ++j) {
-            const bool fine = drop[j] != take[j] && is_page(drop[j]);
+            const bool fine = is_page(drop[j]) && !same(drop[j], take[j], b0 + 32 * j + lane, had, full);
             key[j] = fine ? x.owner[drop[j]] : ~0ull;
             left[j] = fine ? a.shares[drop[j]] : 0;
         }
@@ -249,7 +251,7 @@ fork_kernel(PagedProblem p, ForkArgs a, void *scratch, DeviceStatus *st)
         bool is[kDeep];
         load(drop, row(r), b0, had);
         load(take, s >= 0 ? row(s) : row(r), b0, full);
-        frees(is, drop, take, r, b0);
+        frees(is, drop, take, r, b0, had, full);
 #pragma unroll
         for (int j = 0; j < kDeep; ++j) back += __popc(__ballot_sync(0xffffffffu, is[j]));
         if (lane == 0) x.back_at[i] = back;
@@ -275,7 +277,7 @@ fork_kernel(PagedProblem p, ForkArgs a, void *scratch, DeviceStatus *st)
         int back = x.back_at[i];
         load(drop, x.old + (long long)r * nb, b0, had);
         load(take, s >= 0 ? source(s) : row(r), b0, full);
-        frees(is, drop, take, r, b0);
+        frees(is, drop, take, r, b0, had, full);
 #pragma unroll
         for (int j = 0; j < kDeep; ++j) {
             const int b = b0 + 32 * j + lane;
@@ -285,7 +287,7 @@ fork_kernel(PagedProblem p, ForkArgs a, void *scratch, DeviceStatus *st)
                 a.shares[drop[j]] = 0;                 // nobody but this block's thread looks at it
             }
             back += __popc(all);
-            if (b < full && drop[j] != take[j]) row(r)[b] = take[j];
+            if (b < full && !same(drop[j], take[j], b, had, full)) row(r)[b] = take[j];
         }
     });
     for (int r = cta * kThreads + tid; r < R; r += kCtas * kThreads) {
