@@ -863,6 +863,7 @@ chunk_attn_kernel(Args a, AttnPlan plan)
                 }
             }
             fence_proxy_async();
+            fence_before_sync();                              // the item before has read its sums
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_full[half]);
         };
@@ -986,11 +987,13 @@ chunk_attn_kernel(Args a, AttnPlan plan)
                 const uint32_t turn = splits++ & 1u;
                 if (half == 1) {
                     state[r] = make_float2(used ? m : -INFINITY, used ? z : 0.f);
+                    fence_before_sync();                      // A reads the sums that this half's products left
                     __syncwarp();
                     if (lane == 0) mbar_arrive(b_ready);
                     return wait(b_read, turn, st, 191, abort_flag);   // A has read this half's sums
                 }
                 if (!wait(b_ready, turn, st, 192, abort_flag)) return false;
+                fence_after_sync();
                 const float2 b = state[r];
                 const bool none = b.y == 0.f;                 // nothing visible on B's pages
                 const float top = none ? m : fmaxf(m, b.x);
