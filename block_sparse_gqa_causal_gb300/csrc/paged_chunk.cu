@@ -65,10 +65,13 @@ chunk_plan_kernel(PagedProblem p, const int32_t *q_starts, const int32_t *row_po
 {
     __shared__ int first[kPlanThreads], start[kPlanThreads], rows[kPlanThreads];
     __shared__ long long buf[32];
+    __shared__ int left_out;
     chain_next();
     chain_wait(q_starts, row_pos, at);
     const ChunkPlan plan(at, most);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) left_out = 0;
+    __syncthreads();
     int n = 0;
     for (int r0 = 0; r0 < p.R; r0 += kPlanThreads) {
         const int r = r0 + tid;
@@ -77,7 +80,10 @@ chunk_plan_kernel(PagedProblem p, const int32_t *q_starts, const int32_t *row_po
             a = q_starts[r];
             const int b = q_starts[r + 1];
             if (a >= 0 && a <= b && b <= p.T) m = b - a;
-            else report(st, kDevCheck, 170, r);
+            else {
+                report(st, kDevCheck, 170, r);
+                left_out = 1;
+            }
         }
         long long all;
         const int mine = (int)plan_scan((m + tokens - 1) / tokens, buf, all);
@@ -121,7 +127,8 @@ chunk_plan_kernel(PagedProblem p, const int32_t *q_starts, const int32_t *row_po
     }
     if (tid == 0) {
         plan.before[n] = sum;
-        *plan.n_tiles = n;
+        plan.n_tiles[0] = n;
+        plan.n_tiles[1] = left_out;
     }
 }
 
@@ -380,13 +387,17 @@ chunk_scores_kernel(PagedProblem p, const __grid_constant__ CUtensorMap tmap_q, 
             }
         }
     }
-    // the blocks past each row's own, a warp to a (row, group)
-    const int begin = max(0, q_starts[0]), behind = min(p.T, q_starts[p.R]);
-    for (long long i = (long long)blockIdx.x * (kThreads / 32) + warp; i < (long long)p.T * p.Hkv; i += (long long)gridDim.x * (kThreads / 32)) {
-        const int t = (int)(i / p.Hkv), pos = row_pos[t];
-        if (t < begin || t >= behind || pos < 0) continue;
+    // the blocks past each row's own, a warp to a (row, group); tile by tile where a request was left out
+    auto past = [&](long long i, int pos) {
         float *dst = scores + i * p.max_blocks;
-        for (int c = min(pos / kPage + 1, p.max_blocks) + lane; c < p.max_blocks; c += 32) dst[c] = -INFINITY;
+        for (int c = min(pos / kPage + 1, p.max_blocks) + lane; pos >= 0 && c < p.max_blocks; c += 32) dst[c] = -INFINITY;
+    };
+    const int me = (int)blockIdx.x * (kThreads / 32) + warp, all = (int)gridDim.x * (kThreads / 32);
+    if (!plan.n_tiles[1]) {
+        for (long long i = (long long)q_starts[0] * p.Hkv + me; i < (long long)q_starts[p.R] * p.Hkv; i += all) past(i, row_pos[i / p.Hkv]);
+    } else {
+        for (int n = me; n < n_tiles; n += all)
+            for (int j = 0; j < plan.tiles[n].rows * p.Hkv; ++j) past((long long)plan.tiles[n].row * p.Hkv + j, row_pos[plan.tiles[n].row + j / p.Hkv]);
     }
     fence_before_sync();
     __syncthreads();

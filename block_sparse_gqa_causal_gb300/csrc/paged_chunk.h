@@ -16,7 +16,7 @@ constexpr int kTileRows = 256;      // (row, head) pairs of a tile: two products
 // Products that a page costs a tile of `pairs` pairs.
 __host__ __device__ __forceinline__ int tile_halves(int pairs) { return pairs > kTileRows / 2 ? 2 : 1; }
 
-// The plan: the number of tiles, the tiles in the order of rows, and the work of those before each (one more than
+// The plan: the number of tiles and whether any request was left out, the tiles in the order of rows, and the work of those before each (one more than
 // tiles), in products: pages x halves.
 struct ChunkPlan {
     int *n_tiles;
