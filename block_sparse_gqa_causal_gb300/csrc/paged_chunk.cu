@@ -59,32 +59,59 @@ __device__ long long plan_scan(long long x, long long *buf, long long &total)
     return (warp ? before : 0) + in - x;
 }
 
+// The largest x of the threads before this one and of all, at least `least`.
+__device__ int plan_max(int x, int least, int *buf, int &all)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto up_to = [&](int v) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v = max(v, y);
+        }
+        return v;
+    };
+    const int in = up_to(max(x, least));
+    __syncthreads();
+    if (lane == 31) buf[warp] = in;
+    __syncthreads();
+    const int w = up_to(buf[lane]);
+    all = __shfl_sync(0xffffffffu, w, 31);
+    const int warps = __shfl_sync(0xffffffffu, w, warp ? warp - 1 : 0), lanes = __shfl_up_sync(0xffffffffu, in, 1);
+    return max(warp ? warps : least, lane ? lanes : least);
+}
+
 // One CTA: a request to a thread, then a tile to a thread, then a tile to a warp for the furthest position of its rows.
 __global__ void __launch_bounds__(kPlanThreads)
 chunk_plan_kernel(PagedProblem p, const int32_t *q_starts, const int32_t *row_pos, int tokens, int pairs, int most, void *at, DeviceStatus *st)
 {
     __shared__ int first[kPlanThreads], start[kPlanThreads], rows[kPlanThreads];
     __shared__ long long buf[32];
-    __shared__ int left_out;
     chain_next();
     chain_wait(q_starts, row_pos, at);
     const ChunkPlan plan(at, most);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0) left_out = 0;
-    __syncthreads();
-    int n = 0;
+    int n = 0, left_out = 0, end = 0;              // end: of the requests so far
     for (int r0 = 0; r0 < p.R; r0 += kPlanThreads) {
         const int r = r0 + tid;
-        int a = 0, m = 0;
+        int a = 0, b = 0;
+        bool fine = true;
         if (r < p.R) {
             a = q_starts[r];
-            const int b = q_starts[r + 1];
-            if (a >= 0 && a <= b && b <= p.T) m = b - a;
-            else {
-                report(st, kDevCheck, 170, r);
-                left_out = 1;
-            }
+            b = q_starts[r + 1];
+            fine = a >= 0 && a <= b && b <= p.T;
         }
+        left_out |= __syncthreads_or(!fine);
+        if (left_out) {                            // a request behind one that does not fit may begin in rows of those before it
+            int all;
+            const int before = plan_max(fine ? b : 0, end, first, all);
+            fine = fine && (r >= p.R || a >= before);
+            end = all;
+        } else {
+            end = q_starts[min(r0 + kPlanThreads, p.R)];
+        }
+        if (!fine) report(st, kDevCheck, 170, r);
+        const int m = fine ? b - a : 0;
         long long all;
         const int mine = (int)plan_scan((m + tokens - 1) / tokens, buf, all);
         first[tid] = mine;
@@ -99,10 +126,9 @@ chunk_plan_kernel(PagedProblem p, const int32_t *q_starts, const int32_t *row_po
                 else hi = mid;
             }
             const int off = (i - first[lo]) * tokens;
-            if (n + i < most) plan.tiles[n + i] = ChunkTile{start[lo] + off, min(tokens, rows[lo] - off), r0 + lo, 0};
-            else report(st, kDevCheck, 170, -1);         // starts that do not ascend
+            plan.tiles[n + i] = ChunkTile{start[lo] + off, min(tokens, rows[lo] - off), r0 + lo, 0};      // no two tiles have a row
         }
-        n = (int)min((long long)most, n + all);
+        n += (int)all;
         __syncthreads();
     }
     for (int i = warp; i < n; i += kPlanThreads / 32) {

@@ -564,7 +564,8 @@ msa_status msa_paged_copy(const msa_paged_shape *shape, const int32_t *moves, in
  * that read a page once for all of them.  A request's rows are those from
  * q_starts[r] to q_starts[r + 1], 0 <= q_starts[0], ascending, at most T; a row with a
  * negative position, or behind the last request, is left as it was.
- * A row_pos past 128 * max_blocks - 1, and starts that do not ascend, are left
+ * A row_pos past 128 * max_blocks - 1, and a request whose starts do not ascend, or
+ * that begins before the end of an earlier one, are left
  * out and recorded in the status word.  Scores are made for any Hkv.
  *
  * Attention: queries enter the products with 8 significant bits, features
