@@ -237,7 +237,8 @@ class PagedCompact(NamedTuple):
 
 class _CRotaryShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("T", "Hq", "Hkv", "d", "d_rot", "interleaved", "period", "offset")] + [
-        ("scale", ctypes.c_float)] + [(n, ctypes.c_longlong) for n in ("q_stride", "k_stride", "q_out_stride", "k_out_stride")]
+        ("scale", ctypes.c_float)] + [(n, ctypes.c_longlong) for n in ("q_stride", "k_stride", "q_out_stride", "k_out_stride")] + [
+        ("zeros", ctypes.c_int)]
 
 
 @dataclass(frozen=True)
@@ -714,7 +715,9 @@ def _rotary(shape: RotaryShape, back: bool, q, k, freqs, positions, q_out, k_out
 def rotary_fwd(shape: RotaryShape, q, k, freqs, *, positions=None, q_out=None, k_out=None, stream=None):
     """msa_rotary_fwd: (q_out, k_out) of q [.., Hq, d] and k [.., Hkv, d] bf16, T tokens
     each, evenly spaced (slices of one projection's output, say); one may be
-    None.  freqs: rotary_freqs'.  positions [T] int32.  q_out may be q, k_out k."""
+    None.  freqs: rotary_freqs'.  positions [T] int32.  q_out may be q, k_out k.
+    Outputs that are not given are zeros for tokens with a negative position, those
+    given are left as they were."""
     return _rotary(shape, False, q, k, freqs, positions, q_out, k_out, stream)
 
 

@@ -151,7 +151,7 @@ cudaError_t launch_paged_chunk_attn(const PagedProblem &p, const bf16 *q, const 
 
 // Rotary positions (rotary.cu).
 struct RotaryProblem {
-    int T, Hq, Hkv, d, d_rot, period, offset, num_sms;
+    int T, Hq, Hkv, d, d_rot, period, offset, num_sms, zeros;
     bool interleaved, backward;
     float scale;
     long long q_stride, k_stride, q_out_stride, k_out_stride;

@@ -344,13 +344,14 @@ msa_status rotary(const msa_rotary_shape *s, bool backward, const void *q, const
                       "offset=%d)", s->T, s->Hq, s->Hkv, s->d, s->d_rot, s->period, s->offset);
     if (s->d_rot > s->d) return refuse(MSA_ERR_INVALID_ARGUMENT, "d_rot (%d) is larger than d (%d)", s->d_rot, s->d);
     if (!(s->scale >= 0.f) || isinf(s->scale)) return refuse(MSA_ERR_INVALID_ARGUMENT, "scale must be finite and >= 0 (0 selects 1)");
+    if (s->zeros < 0 || s->zeros > 3) return refuse(MSA_ERR_INVALID_ARGUMENT, "zeros must be 0..3 (got %d)", s->zeros);
     if (s->d % 16 || s->d > 256) return refuse(MSA_ERR_UNSUPPORTED, "d must be a multiple of 16 up to 256 (got %d)", s->d);
     if (s->d_rot % 16) return refuse(MSA_ERR_UNSUPPORTED, "d_rot must be a multiple of 16 (got %d)", s->d_rot);
     if (s->Hq > 32768 || s->Hkv > 32768) return refuse(MSA_ERR_UNSUPPORTED, "Hq and Hkv must be <= 32768 (got %d, %d)", s->Hq, s->Hkv);
     RotaryProblem p;
     p.T = s->T; p.Hq = q ? s->Hq : 0; p.Hkv = k ? s->Hkv : 0; p.d = s->d; p.d_rot = s->d_rot;
     p.period = s->period ? s->period : s->T; p.offset = s->offset; p.num_sms = current_sms();
-    p.interleaved = s->interleaved != 0; p.backward = backward;
+    p.interleaved = s->interleaved != 0; p.backward = backward; p.zeros = s->zeros;
     p.scale = s->scale > 0.f ? s->scale : 1.f;
     if (!positions && (long long)p.offset + p.period > (1LL << 31)) return refuse(MSA_ERR_INVALID_ARGUMENT, "positions pass 2^31 - 1");
     auto stride = [&](long long given, int heads) { return given ? given : (long long)heads * s->d; };
@@ -366,6 +367,8 @@ msa_status rotary(const msa_rotary_shape *s, bool backward, const void *q, const
     if (st != MSA_OK || (st = optional4(positions, "positions")) != MSA_OK) return st;
     if ((q && q == q_out && p.q_stride != p.q_out_stride) || (k && k == k_out && p.k_stride != p.k_out_stride))
         return refuse(MSA_ERR_INVALID_ARGUMENT, "an output in its input's place has another stride");
+    if ((q && q == q_out && (s->zeros & 1)) || (k && k == k_out && (s->zeros & 2)))
+        return refuse(MSA_ERR_INVALID_ARGUMENT, "zeros for an output in its input's place");
     return done(launch_rotary(p, b16(q), b16(k), positions, freqs, static_cast<bf16 *>(q_out), static_cast<bf16 *>(k_out),
                               static_cast<cudaStream_t>(stream)),
                 "rotary launch");

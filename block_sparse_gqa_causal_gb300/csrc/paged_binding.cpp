@@ -300,6 +300,7 @@ PyObject *rotary(PyObject *, PyObject *const *args, Py_ssize_t nargs)
         if (!t[at] && i >= 2) {
             fresh[io] = at::empty(t[io]->sizes(), at::TensorOptions().dtype(at::kBFloat16).device(*dev));
             ptr[i] = fresh[io].data_ptr();
+            s.zeros |= 1 << io;          // there is nothing in it that could be left as it was
             continue;
         }
         if (!t[at]) continue;

@@ -50,12 +50,15 @@ rotary_kernel(RotaryProblem p, const bf16 *q, const bf16 *k, const int32_t *posi
     const int heads = p.Hq + p.Hkv, units = heads * per_head;
     for (int i = tid; i < toks * units; i += kThreads) {
         const int tk = i / units, r = i - tk * units, h = r / per_head, j = r - h * per_head;
-        if (skip[tk]) continue;
         const bool is_q = h < p.Hq;
         const long long t = t0 + tk;
         const bf16 *x = is_q ? q + t * p.q_stride + (long long)h * p.d : k + t * p.k_stride + (long long)(h - p.Hq) * p.d;
         bf16 *y = is_q ? q_out + t * p.q_out_stride + (long long)h * p.d : k_out + t * p.k_out_stride + (long long)(h - p.Hq) * p.d;
         const int w0 = INTER || j >= turned ? 2 * j : j, w1 = INTER || j >= turned ? 2 * j + 1 : j + turned;
+        if (skip[tk]) {
+            if (p.zeros & (is_q ? 1 : 2)) reinterpret_cast<uint4 *>(y)[w0] = reinterpret_cast<uint4 *>(y)[w1] = make_uint4(0, 0, 0, 0);
+            continue;
+        }
         uint4 a = reinterpret_cast<const uint4 *>(x)[w0], b = reinterpret_cast<const uint4 *>(x)[w1];
         if (j < turned) {
             const float4 *f = reinterpret_cast<const float4 *>(&cs[tk][8 * j]);

@@ -603,8 +603,8 @@ msa_status msa_paged_chunk_attn(const msa_paged_shape *shape, const void *q, con
  *   q, q_out [T, Hq, d], k, k_out [T, Hkv, d] bf16, the heads of a token one
  *           after another, tokens q_stride, .. elements apart (0: Hq * d, Hkv * d);
  *           a pair may be NULL; an output may be its input (same stride), nothing else overlaps
- *   positions [T] int32; a token with a negative one is left as it was.  NULL:
- *           offset + t % period (0: T)
+ *   positions [T] int32; of a token with a negative one the outputs are left as they were, or,
+ *           with bit 0 (q_out), bit 1 (k_out) of zeros, set to 0.  NULL: offset + t % period (0: T)
  *   freqs   [d_rot / 2] 64-bit: f_i / 2 pi turns, as a fraction of 2^64, so that
  *           p * freqs[i] mod 2^64 is the angle's turn, exact at any position
  * Supported: d a multiple of 16 up to 256, d_rot a multiple of 16 up to d,
@@ -615,6 +615,7 @@ typedef struct {
     int T, Hq, Hkv, d, d_rot, interleaved, period, offset;
     float scale;         /* 0 -> 1 */
     long long q_stride, k_stride, q_out_stride, k_out_stride;
+    int zeros;
 } msa_rotary_shape;
 msa_status msa_rotary_fwd(const msa_rotary_shape *shape, const void *q, const void *k, const int32_t *positions,
                           const unsigned long long *freqs, void *q_out, void *k_out, void *stream);
