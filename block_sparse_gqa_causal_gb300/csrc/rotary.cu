@@ -91,7 +91,7 @@ cudaError_t launch_rotary(const RotaryProblem &p, const bf16 *q, const bf16 *k, 
                           const unsigned long long *freqs, bf16 *q_out, bf16 *k_out, cudaStream_t s)
 {
     auto run = [&](auto kernel, int tok) {
-        return launch_chained("rotary_kernel", kernel, dim3((unsigned)((p.T + tok - 1) / tok)), kThreads, 0, s, p, q, k, positions, freqs,
+        return launch_chained("rotary_kernel", kernel, dim3((unsigned)((p.T + (long long)tok - 1) / tok)), kThreads, 0, s, p, q, k, positions, freqs,
                               q_out, k_out);
     };
     // four tokens share a CTA's set-up where that leaves a CTA to every place on the GPU
