@@ -107,19 +107,6 @@ class _CPagedShape(ctypes.Structure):
         ("scale", ctypes.c_float), ("scale_idx", ctypes.c_float)]
 
 
-class _MoreCalls(dict):
-    """A shape's handles by op; those of OP_PAGED_COPY by (op, number of moves), made when they are first asked for."""
-
-    def __init__(self, fields, specs):
-        self.fields, self.copied = fields, specs.pop(OP_PAGED_COPY)
-        super().__init__({op: binding().prepare(op[0] if isinstance(op, tuple) else op, fields, args) for op, args in specs.items()})
-
-    def __missing__(self, op):
-        call, moves = op
-        self[op] = binding().prepare(call, self.fields, [("moves", (moves, 3), 0, 0), *self.copied])
-        return self[op]
-
-
 @dataclass(frozen=True)
 class PagedShape:
     """msa_paged_shape: R requests, T rows (query tokens) of a step, block tables
@@ -184,7 +171,7 @@ class PagedShape:
         return (self.R, self.T, self.max_blocks, self.n_pages, self.Hq, self.Hkv, self.d, self.d_idx, self.topk, self.scale, self.scale_idx)
 
     @cached_property
-    def _more_calls(self) -> "_MoreCalls":
+    def _more_calls(self) -> dict:
         """As _calls, of the calls for shared pages and chunks."""
         i32, f32, bf, f8 = 0, 1, 2, 3
         need, maybe, out = 0, 1, 2
@@ -198,7 +185,7 @@ class PagedShape:
             OP_PAGED_FORK: [("src", (R,), i32, need), ("fork_lens", (R,), i32, maybe), ("lens", (R,), i32, need), ("held", (R,), i32, maybe),
                             table, ("free_pages", (N,), i32, need), ("free_state", (2,), i32, need), ("shares", (N,), i32, need),
                             ("moves", (R, 3), i32, out)],
-            OP_PAGED_COPY: [*cache(maybe), ("k_idx", k_idx, bf, maybe)],      # behind the moves, of any number
+            OP_PAGED_COPY: [("moves", (-1, 3), i32, need), *cache(maybe), ("k_idx", k_idx, bf, maybe)],      # -1: any number
             OP_PAGED_CHUNK_SCORES: [("q_idx", (T, H, self.d_idx), bf, need), ("k_idx", k_idx, bf, need), *starts_pos,
                                     ("block_scores", (T, H, self.max_blocks), f32, out)],
             OP_PAGED_CHUNK_ATTN: [("q", (T, self.Hq, D), bf, need), *cache(need), *starts_pos, ("sel_idx", (T, H, self.topk), i32, maybe),
@@ -208,7 +195,7 @@ class PagedShape:
             specs[op] = [("lens", (R,), i32, need), ("held", (R,), i32, maybe), table, ("shares", (N,), i32, given),
                          ("block_table", (R, self.max_blocks), i32, out), ("free_pages", (N,), i32, out), ("free_state", (2,), i32, out),
                          ("shares", (N,), i32, made), ("moves", (max(1, N // 2), 3), i32, out)]
-        return _MoreCalls(self._fields, specs)
+        return {op: binding().prepare(op[0] if isinstance(op, tuple) else op, self._fields, args) for op, args in specs.items()}
 
 
 class PagedPlan(NamedTuple):
@@ -663,7 +650,7 @@ def paged_compact(shape: PagedShape, lens, block_table, shares=None, *, held=Non
 def paged_copy(shape: PagedShape, moves, k8, v8, k_scale, v_scale, k_idx, *, workspace=None, stream=None) -> None:
     """msa_paged_copy: the moves [n, 3] int32 of paged_fork or paged_compact, made in a
     layer's caches (as paged_append's).  The K and V group, or k_idx, may be None."""
-    _paged(shape, (OP_PAGED_COPY, moves.shape[0]), workspace, stream, moves, k8, v8, k_scale, v_scale, k_idx)
+    _paged(shape, OP_PAGED_COPY, workspace, stream, moves, k8, v8, k_scale, v_scale, k_idx)
 
 
 def paged_chunk_scores(shape: PagedShape, q_idx, k_idx, block_table, q_starts, row_pos, *, block_scores=None, workspace=None, stream=None):

@@ -11,6 +11,8 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
+#include <climits>
 #include <sstream>
 #include <string>
 #include <vector>
@@ -23,7 +25,7 @@ enum Kind { kRequired = 0, kOptional = 1, kOutput = 2 };   // kOutput: allocated
 
 struct Arg {
     std::string name;
-    std::vector<int64_t> shape;
+    std::vector<int64_t> shape;     // a first dimension of -1: of any size (an input's)
     at::ScalarType dtype;
     int kind;
 };
@@ -90,7 +92,8 @@ std::string described(const at::Tensor &t)
     return s.str();
 }
 
-int launch(const Call &c, void *const *p, void *ws, size_t n, void *stream)
+// any: the size of a first dimension that may be any
+int launch(const Call &c, void *const *p, int any, void *ws, size_t n, void *stream)
 {
     auto i32 = [&](int i) { return static_cast<int32_t *>(p[i]); };
     auto f32 = [&](int i) { return static_cast<float *>(p[i]); };
@@ -109,7 +112,7 @@ int launch(const Call &c, void *const *p, void *ws, size_t n, void *stream)
     case MSA_OP_PAGED_COMPACT:
         return msa_paged_compact(&c.shape, i32(0), i32(1), i32(2), i32(3), i32(4), i32(5), i32(6), i32(7), i32(8), ws, n, stream);
     case MSA_OP_PAGED_COPY:
-        return msa_paged_copy(&c.shape, i32(0), (int)c.args[0].shape[0], p[1], p[2], f32(3), f32(4), p[5], ws, n, stream);
+        return msa_paged_copy(&c.shape, i32(0), any, p[1], p[2], f32(3), f32(4), p[5], ws, n, stream);
     case MSA_OP_PAGED_CHUNK_SCORES:
         return msa_paged_chunk_scores(&c.shape, p[0], p[1], i32(2), i32(3), i32(4), f32(5), ws, n, stream);
     case MSA_OP_PAGED_CHUNK_ATTN:
@@ -141,7 +144,7 @@ PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t nargs)
         PyErr_SetString(PyExc_ValueError, what.c_str());
         return static_cast<PyObject *>(nullptr);
     };
-    int made = 0, outputs = 0;
+    int made = 0, outputs = 0, any = 0;
     for (size_t i = 0; i < n; ++i) {
         const Arg &a = c->args[i];
         PyObject *obj = args[2 + i];
@@ -155,7 +158,11 @@ PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t nargs)
         if (!THPVariable_Check(obj)) return complain(a.name + ": need a tensor");
         const at::Tensor &t = THPVariable_Unpack(obj);
         if (!dev) dev = t.device();
-        if (t.scalar_type() != a.dtype || t.sizes() != at::IntArrayRef(a.shape) || !t.is_contiguous() || t.device() != *dev) {
+        const at::IntArrayRef want(a.shape);
+        const bool free = !want.empty() && want[0] < 0;
+        if (free && t.dim() > 0) any = (int)std::min<int64_t>(t.size(0), INT_MAX);
+        const bool fits = free ? t.dim() == (int64_t)want.size() && t.sizes().slice(1) == want.slice(1) : t.sizes() == want;
+        if (t.scalar_type() != a.dtype || !fits || !t.is_contiguous() || t.device() != *dev) {
             std::ostringstream s;
             s << a.name << ": need a contiguous " << a.dtype << " tensor of shape " << at::IntArrayRef(a.shape) << " on " << *dev
               << ", got " << described(t);
@@ -199,7 +206,7 @@ PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t nargs)
             ptr[i] = fresh[i].data_ptr();
         }
     }
-    const int status = launch(*c, ptr, ws.data_ptr(), (size_t)ws.numel(), c10::cuda::getCurrentCUDAStream(dev->index()).stream());
+    const int status = launch(*c, ptr, any, ws.data_ptr(), (size_t)ws.numel(), c10::cuda::getCurrentCUDAStream(dev->index()).stream());
     if (status != MSA_OK) return PyLong_FromLong(status);
     PyObject *out = PyTuple_New(outputs);
     if (!out) return nullptr;
