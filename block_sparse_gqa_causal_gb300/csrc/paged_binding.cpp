@@ -236,6 +236,7 @@ void destroy_rotary(PyObject *capsule) { delete static_cast<msa_rotary_shape *>(
 // prepare_rotary(T, Hq, Hkv, d, d_rot, interleaved, period, offset, scale) -> handle of the calls
 PyObject *prepare_rotary(PyObject *, PyObject *args)
 {
+    HANDLE_TH_ERRORS
     auto s = std::make_unique<msa_rotary_shape>();
     *s = msa_rotary_shape{};
     if (!PyArg_ParseTuple(args, "iiiiipiif", &s->T, &s->Hq, &s->Hkv, &s->d, &s->d_rot, &s->interleaved, &s->period, &s->offset, &s->scale))
@@ -243,6 +244,7 @@ PyObject *prepare_rotary(PyObject *, PyObject *args)
     PyObject *capsule = PyCapsule_New(s.get(), kRotaryCapsule, destroy_rotary);
     if (capsule) s.release();
     return capsule;
+    END_HANDLE_TH_ERRORS
 }
 
 // The distance between the T tokens of a bf16 tensor [.., heads, d], a token's heads one after another; -1 where there is none.
