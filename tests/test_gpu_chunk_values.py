@@ -71,3 +71,21 @@ def test_chunk_sums_over_zero_values_stay_finite(api, sparse):
     o, lse = api.paged_chunk_attn(sh, *args[:6], i32([0, 20, 120]), args[7], sel_idx=None if sel is None else i32(sel))
     want = chunk_ref.attn(*r)
     assert not o.any() and np.all(np.abs(lse.double().cpu().numpy() - want[1]) <= want[3]) and lse.max() > 39.0
+
+
+@pytest.mark.parametrize("flat", [True, False])
+@pytest.mark.parametrize("c", [dict(lens=[2100], q=[300], Hq=8, Hkv=1, d=128, k=6), dict(lens=[900, 130, 1500], q=[5, 130, 70], Hq=4, Hkv=2, d=64, k=4),
+                               dict(lens=[300 + i for i in range(60)], q=[9] * 60, Hq=8, Hkv=2, d=64, k=2), dict(lens=[30000], q=[20], Hq=8, Hkv=1, d=64, k=32)])
+@pytest.mark.parametrize("sparse", [True, False])
+def test_chunk_no_token_is_missing(api, flat, c, sparse):
+    """Each token's value is a single feature's, so that a feature is the weight of a few tokens and its bound theirs: one of a
+    thousand that went missing, or was taken twice, shows (flat: equal weights, from queries of zero)."""
+    from test_gpu_paged import attn_case
+    sh, args, sel, r = attn_case(api, sparse=sparse, qgain=0.0 if flat else 1.0, **c)
+    v8 = np.zeros_like(r[2])
+    j = np.arange(PAGE)
+    for page in range(sh.n_pages):
+        v8[page, :, j, (j * 5 + page * 3) % sh.d] = 0x38            # 1
+    v8[r[2] % 128 == 0x7F] = 0x7F                                   # tokens that nobody wrote
+    vs = np.where(np.isnan(r[4]), r[4], np.float32(0.25))
+    check_chunk(api, sh, args[:2] + (f8(v8), args[3], dev(vs)) + args[5:], starts_of(c["q"]), sel, r[:2] + (v8, r[3], vs) + r[5:], sum(c["q"]))
