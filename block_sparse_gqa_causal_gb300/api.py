@@ -670,7 +670,10 @@ def rotary_freqs(d_rot: int, base: float = 10000.0, *, factor: float = 1.0, orig
     base^(-2i / d_rot) radians a position.  For contexts `factor` times longer: all
     divided by it (original_len 0), or only those that turn `low` times or less over
     the original_len tokens that the model was trained on; those that turn `high`
-    times or more stay, and between the two the share that is divided falls evenly."""
+    times or more stay, and between the two the share that is divided falls evenly.
+    low and high, and whether the turned features are scaled as well, are what a
+    checkpoint was adapted with: the defaults, 1 and 4, go with no scale; 1 and 32
+    with rotary_scale(factor)."""
     if d_rot < 2 or d_rot % 2 or not base > 1 or not factor >= 1 or original_len < 0 or not 0 <= low < high:
         raise ValueError("rotary_freqs: need an even d_rot >= 2, base > 1, factor >= 1, original_len >= 0, 0 <= low < high")
     turns = []
@@ -682,7 +685,8 @@ def rotary_freqs(d_rot: int, base: float = 10000.0, *, factor: float = 1.0, orig
 
 
 def rotary_scale(factor: float) -> float:
-    """The usual scale of the turned features in contexts `factor` times longer: 1 + 0.1 ln factor."""
+    """The scale of the turned features that goes with rotary_freqs(.., factor=factor, low=1, high=32): 1 + 0.1 ln factor.
+    Not for checkpoints of the default ramp, whose logits it would make (1 + 0.1 ln factor)^2 times as large."""
     return 1.0 + 0.1 * math.log(factor) if factor > 1 else 1.0
 
 

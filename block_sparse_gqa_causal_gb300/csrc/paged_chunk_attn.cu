@@ -12,12 +12,13 @@
 // x d operations a page and 128 pairs.  A tile has 256 pairs (256 / G rows): two
 // halves, A and B, whose products alternate on the tensor cores while the other
 // half's scores become probabilities.  2,048 rows of 64 heads over 32,768 tokens
-// take 1,785 us (1,190 TFLOP/s), where the tensor cores' rate gives 1,088: a page
-// takes some 3,500 cycles, of which the products need 2,050 (the tensor pipe is 41%
-// active, shared memory 27% busy); the conversion of the codes, 2,800 of its warps',
-// and the softmax, 2,300 of each half's, share the issue slots and wait for one
-// another, so that every handover between them counts.  The halves' issuers take turns: when both
-// issue at once the products get in one another's way (2,240 us).
+// take this kernel 1,780 us (1,196 TFLOP/s; the call, with the tiles' plan and the
+// joining, 1,866), where the tensor cores' rate gives 1,088: a page takes some
+// 3,500 cycles, of which the products need 2,050 (the tensor pipe is 41% active,
+// shared memory 27% busy); the conversion of the codes, 2,800 of its warps', and the
+// softmax, 2,300 of each half's, share the issue slots and wait for one another, so
+// that every handover between them counts.  The halves' issuers take turns: when
+// both issue at once the products get in one another's way (2,240 us).
 //
 // Codes to 16 bits.  e4m3 products would need queries and probabilities as pairs
 // of e4m3 terms, and small probabilities as several levels of those.  So four
@@ -25,7 +26,8 @@
 // converted to a probability computed): K to fp16, which is one instruction for
 // two codes, against queries brought to fp16 by a power of two for each row and
 // head; V to bf16, so that probabilities keep their 8 bits at any size, which
-// takes five.
+// takes five.  Those 8 bits put outputs 2.3e-3 off (relative, a whole tensor), where
+// their own rounding to bf16 makes 1.7e-3; fp16 has 11, but down to 2^-14 only.
 //
 // Softmax.  With t_j = l_j log2 e + lv, 2^lv the page's V scale over that of the
 // stretch's first page of the tile (2^base), the weight of token j's codes is
@@ -52,7 +54,8 @@
 //
 // With a selection, a tile walks the union of its rows' blocks (made by a kernel
 // before, with a bit to each row that selected the block).  3,000 rows of 32 heads
-// that selected 16 of up to 391 blocks each take 540 us: the unions of 32 rows have
+// that selected 16 of up to 391 blocks each take this kernel 540 us (the call, with
+// the plan, the unions and the joining, 607): the unions of 32 rows have
 // 47 blocks, three times what a row selected.
 // The work is one list of products, those of (tile 0, group 0), (tile 0, group 1)
 // and so on, cut into equal stretches for persistent CTAs.  A stretch cuts at

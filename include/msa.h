@@ -641,7 +641,7 @@ msa_status msa_check_device_status(void *workspace, void *stream);
  * 256-byte aligned, status word zero.  Asynchronous on stream. */
 msa_status msa_selftest_wait_timeout(void *workspace, unsigned int spin_limit, void *stream);
 
-/* Library version string. *//* Library version string. */
+/* Library version string. */
 const char *msa_version(void);
 
 /* Number of kernels this process has launched through the library so far
